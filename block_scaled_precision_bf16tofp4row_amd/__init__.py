@@ -22,6 +22,19 @@ The binding has the same names as the C ABI:
 * ``mxfp4_fp8_grouped_gemm(a, a_scales, w, w_scales, y, offs, ...)`` (FP8 expert GEMM)
 * ``mxfp4_fp8_grouped_gemm_wgrad(dyT, dyT_scales, xT, xT_scales, dw, offs, ...)``
   (FP8 weight-gradient GEMM over the column layouts)
+* ``mxfp4_route_topk(logits, ids, weights, bias, row_mask, ...)`` and
+  ``mxfp4_route_topk_backward(logits, ids, dweights, dlogits, ...)`` (routing to experts)
+* ``mxfp4_expert_map(ids, offs, pos, workspace, src, first_expert, ...)`` (offsets and rows of
+  the routed slots; ``mxfp4_expert_map_workspace(T, k, G)`` bytes of workspace)
+* ``mxfp4_dispatch_rows(x, pos, codes, scales, ...)`` and
+  ``mxfp4_dispatch_fp8_rows(x, pos, y, y_scales, ...)`` (token rows quantized into expert
+  order, MXFP4 or E4M3 with FP32 scales), ``mxfp4_bf16_to_fp8_rows_f32(x, y, y_scales, offs,
+  ...)`` (the latter for rows in expert order)
+* ``mxfp4_fp8_block_gemm(a, a_scales, w, w_scales, y, offs, ...)`` (expert product with FP32
+  scales, 1x128 and 128x128)
+* ``mxfp4_combine_rows(y, pos, out, weights, base, ...)`` and
+  ``mxfp4_combine_rows_backward(dout, y, pos, weights, dy, dweights, ...)`` (expert rows back
+  to the tokens)
 * ``mxfp4_cols_scale_capacity(M_cap, K, G)``, ``mxfp4_validate_offsets(offs, ...)``,
   ``mxfp4_status_string(status)``
 * ``mxfp4_wait_status(stream)`` (raises if a column conversion's bounded wait gave up
@@ -51,6 +64,9 @@ MXFP4_ERR_SHAPE = 2
 MXFP4_ERR_ALIGN = 3
 MXFP4_ERR_HIP = 4
 
+MXFP4_SCORE_SOFTMAX = 0
+MXFP4_SCORE_SIGMOID = 1
+
 EXPORTED = (
     "mxfp4_quantize_rows",
     "mxfp4_nvfp4_quantize_rows",
@@ -62,6 +78,16 @@ EXPORTED = (
     "mxfp4_bf16_to_fp8_rows_cols_ragged",
     "mxfp4_fp8_grouped_gemm",
     "mxfp4_fp8_grouped_gemm_wgrad",
+    "mxfp4_route_topk",
+    "mxfp4_route_topk_backward",
+    "mxfp4_expert_map_workspace",
+    "mxfp4_expert_map",
+    "mxfp4_dispatch_rows",
+    "mxfp4_dispatch_fp8_rows",
+    "mxfp4_bf16_to_fp8_rows_f32",
+    "mxfp4_fp8_block_gemm",
+    "mxfp4_combine_rows",
+    "mxfp4_combine_rows_backward",
     "mxfp4_cols_scale_capacity",
     "mxfp4_validate_offsets",
     "mxfp4_wait_status",
@@ -120,6 +146,27 @@ def load_library(path: str = LIB_PATH):
     lib.mxfp4_nvfp4_quantize_rows.restype = st
     lib.mxfp4_nvfp4_quantize_rows_sr.restype = st
     lib.mxfp4_fp8_grouped_gemm_wgrad.restype = st
+    F32 = ctypes.c_float
+    lib.mxfp4_route_topk.argtypes = [P, I32, P, P, P, P, I64, I32, I32, I32, I32, I32, I32, I32, F32, P]
+    lib.mxfp4_route_topk.restype = st
+    lib.mxfp4_route_topk_backward.argtypes = [P, I32, P, P, P, I64, I32, I32, I32, I32, F32, P]
+    lib.mxfp4_route_topk_backward.restype = st
+    lib.mxfp4_expert_map_workspace.argtypes = [I64, I32, I32]
+    lib.mxfp4_expert_map_workspace.restype = I64
+    lib.mxfp4_expert_map.argtypes = [P, P, P, P, P, I64, I32, I32, I32, I64, P]
+    lib.mxfp4_expert_map.restype = st
+    lib.mxfp4_dispatch_rows.argtypes = [P, P, P, P, I64, I32, I64, I64, P]
+    lib.mxfp4_dispatch_rows.restype = st
+    lib.mxfp4_dispatch_fp8_rows.argtypes = [P, P, P, P, I64, I32, I64, I64, P]
+    lib.mxfp4_dispatch_fp8_rows.restype = st
+    lib.mxfp4_bf16_to_fp8_rows_f32.argtypes = [P, P, P, P, I32, I64, I64, P]
+    lib.mxfp4_bf16_to_fp8_rows_f32.restype = st
+    lib.mxfp4_fp8_block_gemm.argtypes = [P, P, P, P, P, P, I32, I64, I64, I64, P]
+    lib.mxfp4_fp8_block_gemm.restype = st
+    lib.mxfp4_combine_rows.argtypes = [P, P, P, P, P, I64, I32, I64, I64, P]
+    lib.mxfp4_combine_rows.restype = st
+    lib.mxfp4_combine_rows_backward.argtypes = [P, P, P, P, P, P, I64, I32, I64, I64, P]
+    lib.mxfp4_combine_rows_backward.restype = st
     lib.mxfp4_cols_scale_capacity.argtypes = [I64, I64, I32]
     lib.mxfp4_cols_scale_capacity.restype = I64
     lib.mxfp4_validate_offsets.argtypes = [P, I32, I64, P]
@@ -367,6 +414,213 @@ def mxfp4_nvfp4_quantize_rows_sr(x, codes, scales, tensor_amax, offs, seed, G=No
     """NVFP4 with the element codes rounded stochastically (Philox4x32-10 bits under the
     64-bit seed); see the header."""
     mxfp4_nvfp4_quantize_rows(x, codes, scales, tensor_amax, offs, G=G, M_cap=M_cap, K=K, stream=stream, seed=seed)
+
+
+# ---- the expert layer: routing, dispatch, FP32-scaled product, combine ---------------
+
+_F32 = ("float32",)
+_I32 = ("int32",)
+_B16 = ("bfloat16", "int16", "uint16")
+
+
+def _score(score) -> int:
+    kinds = {"softmax": MXFP4_SCORE_SOFTMAX, "sigmoid": MXFP4_SCORE_SIGMOID}
+    if isinstance(score, str) and score not in kinds:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return kinds.get(score, score)
+
+
+def _at(t) -> int | None:
+    """_ptr, with an address that nothing reads for a tensor without elements (torch gives
+    those none, and NULL is an error)."""
+    return _ptr(t) or (16 if t is not None and not isinstance(t, int) and t.numel() == 0 else None)
+
+
+def _logits_dims(logits, ids, T, E, k, f32):
+    """T, E, k and whether the logits are FP32, from the tensors where they are not given."""
+    if T is None:
+        T = logits.shape[0]
+    if E is None:
+        E = logits.shape[1]
+    if k is None:
+        k = ids.shape[1]
+    if f32 is None:
+        f32 = isinstance(logits, int) or str(logits.dtype) == "torch.float32"
+    return int(T), int(E), int(k), bool(f32)
+
+
+def mxfp4_route_topk(logits, ids, weights, bias=None, row_mask=None, n_group=1, topk_group=1, group_best=1,
+                     score="softmax", renorm=True, scale=1.0, T=None, E=None, k=None, logits_f32=None, stream=None):
+    """logits [T, E] (float32 or bfloat16) -> ids [T, k] int32 and weights [T, k] float32 of
+    the k chosen experts; score "softmax" or "sigmoid" (see the header)."""
+    T, E, k, f32 = _logits_dims(logits, ids, T, E, k, logits_f32)
+    t, e, n = max(T, 0), max(E, 0), max(T, 0) * max(k, 0)
+    _need("mxfp4_route_topk", [(logits, (4 if f32 else 2) * t * e, "logits", _F32 if f32 else _B16),
+                               (bias, 4 * e, "bias", _F32), (row_mask, t, "row_mask", ("uint8", "bool")),
+                               (ids, 4 * n, "ids", _I32), (weights, 4 * n, "weights", _F32)])
+    _check(load_library().mxfp4_route_topk(_at(logits), f32, _at(bias), _at(row_mask), _at(ids), _at(weights),
+                                           T, E, int(n_group), int(topk_group), int(group_best), k, _score(score),
+                                           bool(renorm), float(scale), _stream(stream)), "mxfp4_route_topk")
+
+
+def mxfp4_route_topk_backward(logits, ids, dweights, dlogits, score="softmax", renorm=True, scale=1.0, T=None, E=None,
+                              k=None, logits_f32=None, stream=None):
+    """The weights' gradient dweights [T, k] -> dlogits [T, E], of the logits' type (see the
+    header)."""
+    T, E, k, f32 = _logits_dims(logits, ids, T, E, k, logits_f32)
+    t, e, n = max(T, 0), max(E, 0), max(T, 0) * max(k, 0)
+    el, kinds = (4, _F32) if f32 else (2, _B16)
+    _need("mxfp4_route_topk_backward", [(logits, el * t * e, "logits", kinds), (ids, 4 * n, "ids", _I32),
+                                        (dweights, 4 * n, "dweights", _F32), (dlogits, el * t * e, "dlogits", kinds)])
+    _check(load_library().mxfp4_route_topk_backward(_at(logits), f32, _at(ids), _at(dweights), _at(dlogits), T, E,
+                                                    k, _score(score), bool(renorm), float(scale), _stream(stream)),
+           "mxfp4_route_topk_backward")
+
+
+def mxfp4_expert_map_workspace(T: int, k: int, G: int) -> int:
+    return int(load_library().mxfp4_expert_map_workspace(int(T), int(k), int(G)))
+
+
+def mxfp4_expert_map(ids, offs, pos, workspace, src=None, first_expert=0, T=None, k=None, G=None, M_cap=None,
+                     stream=None):
+    """ids [T, k] int32 -> group offsets offs [G + 1], the row pos [T, k] of every slot (-1:
+    none) and, if given, the slot src [M_cap] of every row (see the header).  M_cap defaults
+    to src's size, or T k without it; workspace may be None where
+    mxfp4_expert_map_workspace(T, k, G) is 0."""
+    if T is None:
+        T = ids.shape[0]
+    if k is None:
+        k = ids.shape[1]
+    if G is None:
+        G = offs.numel() - 1
+    if M_cap is None:
+        M_cap = int(T) * int(k) if src is None or isinstance(src, int) else src.numel()
+    T, k, G, M_cap = int(T), int(k), int(G), int(M_cap)
+    n = max(T, 0) * max(k, 0)
+    _need("mxfp4_expert_map",
+          [(ids, 4 * n, "ids", _I32), (offs, 4 * (G + 1), "group_offsets", _I32), (pos, 4 * n, "pos", _I32),
+           (src, 4 * max(M_cap, 0), "src", _I32),
+           (workspace, max(mxfp4_expert_map_workspace(T, k, G), 0), "workspace", ("int32", "uint8", "float32"))])
+    _check(load_library().mxfp4_expert_map(_at(ids), _at(offs), _at(pos), _at(src), _at(workspace), T, k,
+                                           int(first_expert), G, M_cap, _stream(stream)), "mxfp4_expert_map")
+
+
+def _token_dims(rows, pos, out, T, k, M_cap, K):
+    """T and k from pos, K and M_cap from the token rows and the expert rows, where not given."""
+    if T is None:
+        T = pos.shape[0]
+    if k is None:
+        k = pos.shape[1]
+    if K is None:
+        K = rows.shape[1]
+    if M_cap is None:
+        M_cap = out.shape[0]
+    return int(T), int(k), int(M_cap), int(K)
+
+
+def mxfp4_dispatch_rows(x, pos, codes, scales, T=None, k=None, M_cap=None, K=None, stream=None):
+    """BF16 token rows x [T, K] -> MXFP4 codes [M_cap, K/2] and scales [M_cap, K/32] in expert
+    order, each row quantized once and written to its places pos [T, k]."""
+    T, k, M_cap, K = _token_dims(x, pos, codes, T, k, M_cap, K)
+    t, m, w = max(T, 0), max(M_cap, 0), max(K, 0)
+    _need("mxfp4_dispatch_rows", [(x, 2 * t * w, "x", _B16), (pos, 4 * t * max(k, 0), "pos", _I32),
+                                  (codes, m * w // 2, "codes", _U8), (scales, m * w // 32, "scales", _U8)])
+    _check(load_library().mxfp4_dispatch_rows(_at(x), _at(pos), _at(codes), _at(scales), T, k, M_cap, K,
+                                              _stream(stream)), "mxfp4_dispatch_rows")
+
+
+def mxfp4_dispatch_fp8_rows(x, pos, y, y_scales, T=None, k=None, M_cap=None, K=None, stream=None):
+    """BF16 token rows x [T, K] -> E4M3 y [M_cap, K] and FP32 y_scales [M_cap, ceil(K/128)] in
+    expert order, each row quantized once and written to its places pos [T, k]."""
+    T, k, M_cap, K = _token_dims(x, pos, y, T, k, M_cap, K)
+    t, m, w = max(T, 0), max(M_cap, 0), max(K, 0)
+    _need("mxfp4_dispatch_fp8_rows", [(x, 2 * t * w, "x", _B16), (pos, 4 * t * max(k, 0), "pos", _I32),
+                                      (y, m * w, "y", _FP8), (y_scales, 4 * m * ((w + 127) // 128), "y_scales", _F32)])
+    _check(load_library().mxfp4_dispatch_fp8_rows(_at(x), _at(pos), _at(y), _at(y_scales), T, k, M_cap, K,
+                                                  _stream(stream)), "mxfp4_dispatch_fp8_rows")
+
+
+def mxfp4_bf16_to_fp8_rows_f32(x, y, y_scales, offs, G=None, M_cap=None, K=None, stream=None):
+    """BF16 x [M_cap, K] -> E4M3 y [M_cap, K] + FP32 y_scales [M_cap, ceil(K/128)] for the rows
+    [0, offs[G]) (the quantizer of mxfp4_dispatch_fp8_rows)."""
+    G, M_cap, K = _dims(x, offs, G, M_cap, K)
+    m, w = max(M_cap, 0), max(K, 0)
+    _need("mxfp4_bf16_to_fp8_rows_f32", [(x, 2 * m * w, "x", _B16), (y, m * w, "y", _FP8),
+                                         (y_scales, 4 * m * ((w + 127) // 128), "y_scales", _F32),
+                                         (offs, 4 * (G + 1), "group_offsets", _I32)])
+    _check(load_library().mxfp4_bf16_to_fp8_rows_f32(_at(x), _at(y), _at(y_scales), _at(offs), G, M_cap, K,
+                                                     _stream(stream)), "mxfp4_bf16_to_fp8_rows_f32")
+
+
+def mxfp4_fp8_block_gemm(a, a_scales, w, w_scales, y, offs, G=None, M_cap=None, N=None, K=None, stream=None):
+    """E4M3 a [M_cap, K] (+ FP32 [M_cap, ceil(K/128)]) x per-expert E4M3 w [G, N, K] (+ FP32
+    [G, ceil(N/128), ceil(K/128)]) -> BF16 y [M_cap, N] (see the header)."""
+    if G is None:
+        G = offs.numel() - 1
+    if M_cap is None:
+        M_cap = a.shape[0]
+    if K is None:
+        K = a.shape[1]
+    if N is None:
+        N = w.shape[-2]
+    G, M_cap, N, K = int(G), int(M_cap), int(N), int(K)
+    g, m, n, k = max(G, 0), max(M_cap, 0), max(N, 0), max(K, 0)
+    nb, kb = (n + 127) // 128, (k + 127) // 128
+    _need("mxfp4_fp8_block_gemm", [(a, m * k, "a", _FP8), (a_scales, 4 * m * kb, "a_scales", _F32),
+                                   (w, g * n * k, "w", _FP8), (w_scales, 4 * g * nb * kb, "w_scales", _F32),
+                                   (y, 2 * m * n, "y", _B16), (offs, 4 * (G + 1), "group_offsets", _I32)])
+    _check(load_library().mxfp4_fp8_block_gemm(_at(a), _at(a_scales), _at(w), _at(w_scales), _at(y), _at(offs),
+                                               G, M_cap, N, K, _stream(stream)), "mxfp4_fp8_block_gemm")
+
+
+def mxfp4_combine_rows(y, pos, out, weights=None, base=None, T=None, k=None, M_cap=None, K=None, stream=None):
+    """out [T, K] = base [T, K] + sum over a token's rows of weights [T, k] * y[pos] (BF16 rows,
+    FP32 sum; without weights the plain sum, without base from zero)."""
+    T, k, M_cap, K = _token_dims(y, pos, y, T, k, M_cap, K)
+    t, w = max(T, 0), max(K, 0)
+    n = t * max(k, 0)
+    _need("mxfp4_combine_rows", [(y, 2 * max(M_cap, 0) * w, "y", _B16), (pos, 4 * n, "pos", _I32),
+                                 (weights, 4 * n, "weights", _F32), (base, 2 * t * w, "base", _B16),
+                                 (out, 2 * t * w, "out", _B16)])
+    _check(load_library().mxfp4_combine_rows(_at(y), _at(pos), _at(weights), _at(base), _at(out), T, k, M_cap, K,
+                                             _stream(stream)), "mxfp4_combine_rows")
+
+
+def mxfp4_combine_rows_backward(dout, y, pos, weights, dy, dweights, T=None, k=None, M_cap=None, K=None, stream=None):
+    """The gradients of mxfp4_combine_rows: dy [M_cap, K] (BF16, the rows that have a slot) and
+    dweights [T, k] (float32) from dout [T, K]."""
+    T, k, M_cap, K = _token_dims(dout, pos, y, T, k, M_cap, K)
+    t, m, w = max(T, 0), max(M_cap, 0), max(K, 0)
+    n = t * max(k, 0)
+    _need("mxfp4_combine_rows_backward", [(dout, 2 * t * w, "dout", _B16), (y, 2 * m * w, "y", _B16),
+                                          (pos, 4 * n, "pos", _I32), (weights, 4 * n, "weights", _F32),
+                                          (dy, 2 * m * w, "dy", _B16), (dweights, 4 * n, "dweights", _F32)])
+    _check(load_library().mxfp4_combine_rows_backward(_at(dout), _at(y), _at(pos), _at(weights), _at(dy),
+                                                      _at(dweights), T, k, M_cap, K, _stream(stream)),
+           "mxfp4_combine_rows_backward")
+
+
+def alloc_route_outputs(T: int, k: int, device="cuda"):
+    """ids and weights of mxfp4_route_topk."""
+    import torch
+    return (torch.empty((T, k), dtype=torch.int32, device=device),
+            torch.empty((T, k), dtype=torch.float32, device=device))
+
+
+def alloc_expert_map_outputs(T: int, k: int, G: int, device="cuda"):
+    """offs, pos and the workspace of mxfp4_expert_map."""
+    import torch
+    words = max(0, mxfp4_expert_map_workspace(T, k, G)) // 4
+    return (torch.empty(G + 1, dtype=torch.int32, device=device),
+            torch.empty((T, k), dtype=torch.int32, device=device),
+            torch.empty(max(1, words), dtype=torch.int32, device=device))
+
+
+def alloc_fp8_rows_f32_outputs(M_cap: int, K: int, device="cuda"):
+    """y and y_scales of mxfp4_dispatch_fp8_rows and mxfp4_bf16_to_fp8_rows_f32."""
+    import torch
+    return (torch.empty((M_cap, K), dtype=torch.uint8, device=device),
+            torch.empty((M_cap, (K + 127) // 128), dtype=torch.float32, device=device))
 
 
 def alloc_nvfp4_outputs(M_cap: int, K: int, device="cuda"):

@@ -1,6 +1,8 @@
 // abi.hip -- the C ABI of libmxfp4cvt (declared in include/mxfp4cvt.h): synchronous
 // argument validation, then the call's kernel launches on the caller's stream (one per
-// call, three for the NVFP4 quantizer), all through launch_kernel.
+// call, three for the NVFP4 quantizer, two for an expert map of many slots), all through
+// launch_kernel.
+#include <math.h>
 #include <stdlib.h>
 #include <string.h>
 
@@ -30,6 +32,25 @@ hipError_t launch_fp8q_cols(const uint16_t*, uint8_t*, uint8_t*, uint8_t*, uint8
                             int64_t, WaitCtl, hipStream_t);
 hipError_t launch_fp8q_rows(const uint16_t*, uint8_t*, uint8_t*, const int32_t*, int32_t, int64_t,
                             int64_t, hipStream_t);
+hipError_t launch_route(const void*, bool, const float*, const uint8_t*, int32_t*, float*, int64_t, int32_t, int32_t,
+                        int32_t, int32_t, int32_t, bool, bool, float, hipStream_t);
+hipError_t launch_route_backward(const void*, bool, const int32_t*, const float*, void*, int64_t, int32_t, int32_t,
+                                 bool, bool, float, hipStream_t);
+int64_t expert_map_chunks(int64_t slots);
+hipError_t launch_expert_map(const int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int64_t, int32_t, int32_t,
+                             int64_t, hipStream_t);
+hipError_t launch_dispatch_rows(const uint16_t*, const int32_t*, uint8_t*, uint8_t*, int64_t, int32_t, int64_t,
+                                int64_t, hipStream_t);
+hipError_t launch_dispatch_fp8_rows(const uint16_t*, const int32_t*, uint8_t*, float*, int64_t, int32_t, int64_t,
+                                    int64_t, hipStream_t);
+hipError_t launch_fp8_rows_f32(const uint16_t*, uint8_t*, float*, const int32_t*, int32_t, int64_t, int64_t,
+                               hipStream_t);
+hipError_t launch_block_gemm(const uint8_t*, const float*, const uint8_t*, const float*, uint16_t*, const int32_t*,
+                             int32_t, int64_t, int64_t, int64_t, hipStream_t);
+hipError_t launch_combine(const uint16_t*, const int32_t*, const float*, const uint16_t*, uint16_t*, int64_t, int32_t,
+                          int64_t, int64_t, hipStream_t);
+hipError_t launch_combine_backward(const uint16_t*, const uint16_t*, const int32_t*, const float*, uint16_t*, float*,
+                                   int64_t, int32_t, int64_t, int64_t, hipStream_t);
 }  // namespace mxfp4
 
 namespace {
@@ -54,6 +75,31 @@ mxfp4_status check_shape(int32_t G, int64_t M_cap, int64_t K, int64_t k_multiple
     if (M_cap > INT32_MAX)                   // offsets are int32
         return MXFP4_ERR_SHAPE;
     return MXFP4_OK;
+}
+
+// Largest number of experts a router or an expert map takes, and of choices per token.
+constexpr int32_t kMaxExperts = 1024;
+constexpr int32_t kMaxChoices = 64;
+
+// A call over the k choices of T tokens, rows of K elements, outputs or inputs of M_cap rows.
+mxfp4_status check_tokens(int64_t T, int32_t k, int64_t M_cap, int64_t K, int64_t k_multiple)
+{
+    if (T < 0 || k < 1 || k > kMaxChoices || M_cap < 0 || K <= 0 || K % k_multiple != 0)
+        return MXFP4_ERR_SHAPE;
+    if (T > INT32_MAX / k || M_cap > INT32_MAX)      // positions are int32
+        return MXFP4_ERR_SHAPE;
+    if ((T > 0 && K > kMaxElems / T) || (M_cap > 0 && K > kMaxElems / M_cap))
+        return MXFP4_ERR_SHAPE;
+    return MXFP4_OK;
+}
+
+mxfp4_status check_route(int64_t T, int32_t E, int32_t k, int32_t score, float scale)
+{
+    if (T < 0 || T > INT32_MAX || E < 1 || E > kMaxExperts || k < 1 || k > kMaxChoices || k > E)
+        return MXFP4_ERR_SHAPE;
+    if (T > INT32_MAX / k || (score != MXFP4_SCORE_SOFTMAX && score != MXFP4_SCORE_SIGMOID))
+        return MXFP4_ERR_SHAPE;
+    return isfinite(scale) ? MXFP4_OK : MXFP4_ERR_SHAPE;
 }
 
 mxfp4_status from_hip(hipError_t e) { return e == hipSuccess ? MXFP4_OK : MXFP4_ERR_HIP; }
@@ -338,6 +384,177 @@ mxfp4_status mxfp4_fp8_grouped_gemm_wgrad(const uint8_t* dyT_e4m3, const uint8_t
         return MXFP4_ERR_ALIGN;
     return from_hip(mxfp4::launch_fp8_wgrad(dyT_e4m3, dyT_scales, xT_e4m3, xT_scales, dw_bf16, group_offsets, G,
                                             M_cap, mxfp4::cols_block_capacity(M_cap, G), N, K, stream));
+}
+
+mxfp4_status mxfp4_route_topk(const void* logits, int32_t logits_f32, const float* bias, const uint8_t* row_mask,
+                              int32_t* ids, float* weights, int64_t T, int32_t E, int32_t n_group,
+                              int32_t topk_group, int32_t group_best, int32_t k, int32_t score, int32_t renorm,
+                              float scale, hipStream_t stream)
+{
+    if (!logits || !ids || !weights)
+        return MXFP4_ERR_NULL;
+    mxfp4_status st = check_route(T, E, k, score, scale);
+    if (st != MXFP4_OK)
+        return st;
+    if (n_group < 1 || n_group > 64 || E % n_group != 0 || topk_group < 1 || topk_group > n_group)
+        return MXFP4_ERR_SHAPE;
+    if (group_best < 1 || group_best > 2 || group_best > E / n_group || k > topk_group * (E / n_group))
+        return MXFP4_ERR_SHAPE;
+    if (!aligned(logits, 16) || !aligned(bias, 16) || !aligned(row_mask, 16) || !aligned(ids, 16) ||
+        !aligned(weights, 16))
+        return MXFP4_ERR_ALIGN;
+    if (T == 0)
+        return MXFP4_OK;
+    return from_hip(mxfp4::launch_route(logits, logits_f32 != 0, bias, row_mask, ids, weights, T, E, n_group,
+                                        topk_group, group_best, k, score == MXFP4_SCORE_SIGMOID, renorm != 0, scale,
+                                        stream));
+}
+
+mxfp4_status mxfp4_route_topk_backward(const void* logits, int32_t logits_f32, const int32_t* ids,
+                                       const float* dweights, void* dlogits, int64_t T, int32_t E, int32_t k,
+                                       int32_t score, int32_t renorm, float scale, hipStream_t stream)
+{
+    if (!logits || !ids || !dweights || !dlogits)
+        return MXFP4_ERR_NULL;
+    mxfp4_status st = check_route(T, E, k, score, scale);
+    if (st != MXFP4_OK)
+        return st;
+    if (!aligned(logits, 16) || !aligned(ids, 16) || !aligned(dweights, 16) || !aligned(dlogits, 16))
+        return MXFP4_ERR_ALIGN;
+    if (T == 0)
+        return MXFP4_OK;
+    return from_hip(mxfp4::launch_route_backward(logits, logits_f32 != 0, ids, dweights, dlogits, T, E, k,
+                                                 score == MXFP4_SCORE_SIGMOID, renorm != 0, scale, stream));
+}
+
+int64_t mxfp4_expert_map_workspace(int64_t T, int32_t k, int32_t G)
+{
+    if (check_tokens(T, k, 0, 1, 1) != MXFP4_OK || G < 1 || G > kMaxExperts)
+        return -1;
+    return 4 * mxfp4::expert_map_chunks(T * k) * G;
+}
+
+mxfp4_status mxfp4_expert_map(const int32_t* ids, int32_t* group_offsets, int32_t* pos, int32_t* src,
+                              void* workspace, int64_t T, int32_t k, int32_t first_expert, int32_t G, int64_t M_cap,
+                              hipStream_t stream)
+{
+    if (!ids || !group_offsets || !pos)
+        return MXFP4_ERR_NULL;
+    const int64_t need = mxfp4_expert_map_workspace(T, k, G);
+    if (need < 0 || first_expert < 0 || M_cap < 0 || M_cap > INT32_MAX)
+        return MXFP4_ERR_SHAPE;
+    if (need > 0 && !workspace)
+        return MXFP4_ERR_NULL;
+    if (!aligned(ids, 16) || !aligned(pos, 16) || !aligned(src, 16) || !aligned(workspace, 16) ||
+        !aligned(group_offsets, 4))
+        return MXFP4_ERR_ALIGN;
+    return from_hip(mxfp4::launch_expert_map(ids, group_offsets, pos, src, static_cast<int32_t*>(workspace), T * k,
+                                             first_expert, G, M_cap, stream));
+}
+
+mxfp4_status mxfp4_dispatch_rows(const uint16_t* x_bf16, const int32_t* pos, uint8_t* codes, uint8_t* scales,
+                                 int64_t T, int32_t k, int64_t M_cap, int64_t K, hipStream_t stream)
+{
+    if (!x_bf16 || !pos || !codes || !scales)
+        return MXFP4_ERR_NULL;
+    mxfp4_status st = check_tokens(T, k, M_cap, K, 32);
+    if (st != MXFP4_OK)
+        return st;
+    if (!aligned(x_bf16, 16) || !aligned(pos, 16) || !aligned(codes, 16) || !aligned(scales, 16))
+        return MXFP4_ERR_ALIGN;
+    if (T == 0 || M_cap == 0)
+        return MXFP4_OK;
+    return from_hip(mxfp4::launch_dispatch_rows(x_bf16, pos, codes, scales, T, k, M_cap, K, stream));
+}
+
+mxfp4_status mxfp4_dispatch_fp8_rows(const uint16_t* x_bf16, const int32_t* pos, uint8_t* y_e4m3, float* y_scales,
+                                     int64_t T, int32_t k, int64_t M_cap, int64_t K, hipStream_t stream)
+{
+    if (!x_bf16 || !pos || !y_e4m3 || !y_scales)
+        return MXFP4_ERR_NULL;
+    mxfp4_status st = check_tokens(T, k, M_cap, K, 16);
+    if (st != MXFP4_OK)
+        return st;
+    if (!aligned(x_bf16, 16) || !aligned(pos, 16) || !aligned(y_e4m3, 16) || !aligned(y_scales, 16))
+        return MXFP4_ERR_ALIGN;
+    if (T == 0 || M_cap == 0)
+        return MXFP4_OK;
+    return from_hip(mxfp4::launch_dispatch_fp8_rows(x_bf16, pos, y_e4m3, y_scales, T, k, M_cap, K, stream));
+}
+
+mxfp4_status mxfp4_bf16_to_fp8_rows_f32(const uint16_t* x_bf16, uint8_t* y_e4m3, float* y_scales,
+                                        const int32_t* group_offsets, int32_t G, int64_t M_cap, int64_t K,
+                                        hipStream_t stream)
+{
+    if (!x_bf16 || !y_e4m3 || !y_scales || !group_offsets)
+        return MXFP4_ERR_NULL;
+    mxfp4_status st = check_shape(G, M_cap, K, 16);
+    if (st != MXFP4_OK)
+        return st;
+    if (!aligned(x_bf16, 16) || !aligned(y_e4m3, 16) || !aligned(y_scales, 16) || !aligned(group_offsets, 4))
+        return MXFP4_ERR_ALIGN;
+    if (M_cap == 0)
+        return MXFP4_OK;
+    return from_hip(mxfp4::launch_fp8_rows_f32(x_bf16, y_e4m3, y_scales, group_offsets, G, M_cap, K, stream));
+}
+
+mxfp4_status mxfp4_fp8_block_gemm(const uint8_t* a_e4m3, const float* a_scales, const uint8_t* w_e4m3,
+                                  const float* w_scales, uint16_t* y_bf16, const int32_t* group_offsets, int32_t G,
+                                  int64_t M_cap, int64_t N, int64_t K, hipStream_t stream)
+{
+    if (!a_e4m3 || !a_scales || !w_e4m3 || !w_scales || !y_bf16 || !group_offsets)
+        return MXFP4_ERR_NULL;
+    mxfp4_status st = check_shape(G, M_cap, K, 16);
+    if (st != MXFP4_OK)
+        return st;
+    if (K > kMaxGemmDim || N <= 0 || N % 8 != 0 || N > kMaxGemmDim)
+        return MXFP4_ERR_SHAPE;
+    if (M_cap > 0 && N > kMaxElems / M_cap)          // output elements
+        return MXFP4_ERR_SHAPE;
+    if ((int64_t)G > kMaxElems / (N * K))             // weight elements
+        return MXFP4_ERR_SHAPE;
+    if (!aligned(a_e4m3, 16) || !aligned(a_scales, 16) || !aligned(w_e4m3, 16) || !aligned(w_scales, 16) ||
+        !aligned(y_bf16, 16) || !aligned(group_offsets, 4))
+        return MXFP4_ERR_ALIGN;
+    if (M_cap == 0)
+        return MXFP4_OK;
+    return from_hip(mxfp4::launch_block_gemm(a_e4m3, a_scales, w_e4m3, w_scales, y_bf16, group_offsets, G, M_cap, N,
+                                             K, stream));
+}
+
+mxfp4_status mxfp4_combine_rows(const uint16_t* y_bf16, const int32_t* pos, const float* weights,
+                                const uint16_t* base_bf16, uint16_t* out_bf16, int64_t T, int32_t k, int64_t M_cap,
+                                int64_t K, hipStream_t stream)
+{
+    if (!y_bf16 || !pos || !out_bf16)
+        return MXFP4_ERR_NULL;
+    mxfp4_status st = check_tokens(T, k, M_cap, K, 8);
+    if (st != MXFP4_OK)
+        return st;
+    if (!aligned(y_bf16, 16) || !aligned(pos, 16) || !aligned(weights, 16) || !aligned(base_bf16, 16) ||
+        !aligned(out_bf16, 16))
+        return MXFP4_ERR_ALIGN;
+    if (T == 0)
+        return MXFP4_OK;
+    return from_hip(mxfp4::launch_combine(y_bf16, pos, weights, base_bf16, out_bf16, T, k, M_cap, K, stream));
+}
+
+mxfp4_status mxfp4_combine_rows_backward(const uint16_t* dout_bf16, const uint16_t* y_bf16, const int32_t* pos,
+                                         const float* weights, uint16_t* dy_bf16, float* dweights, int64_t T,
+                                         int32_t k, int64_t M_cap, int64_t K, hipStream_t stream)
+{
+    if (!dout_bf16 || !y_bf16 || !pos || !weights || !dy_bf16 || !dweights)
+        return MXFP4_ERR_NULL;
+    mxfp4_status st = check_tokens(T, k, M_cap, K, 8);
+    if (st != MXFP4_OK)
+        return st;
+    if (!aligned(dout_bf16, 16) || !aligned(y_bf16, 16) || !aligned(pos, 16) || !aligned(weights, 16) ||
+        !aligned(dy_bf16, 16) || !aligned(dweights, 16))
+        return MXFP4_ERR_ALIGN;
+    if (T == 0)
+        return MXFP4_OK;
+    return from_hip(mxfp4::launch_combine_backward(dout_bf16, y_bf16, pos, weights, dy_bf16, dweights, T, k, M_cap, K,
+                                                   stream));
 }
 
 int64_t mxfp4_cols_scale_capacity(int64_t M_cap, int64_t K, int32_t G)

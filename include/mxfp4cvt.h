@@ -58,6 +58,12 @@ typedef enum {
     MXFP4_ERR_HIP = 4
 } mxfp4_status;
 
+/* Scores of the router (mxfp4_route_topk). */
+typedef enum {
+    MXFP4_SCORE_SOFTMAX = 0,
+    MXFP4_SCORE_SIGMOID = 1
+} mxfp4_score;
+
 /* BF16 -> MXFP4 (the page's BF16ToFP4Row; technical summary section 2, items 1-2).
  *   x_bf16  [M_cap, K] row-major BF16 bits (finite values).
  *   codes   [M_cap, K/2]  E2M1 codes, element 2i in the low nibble of byte i.
@@ -217,6 +223,126 @@ mxfp4_status mxfp4_fp8_grouped_gemm_wgrad(const uint8_t* dyT_e4m3, const uint8_t
                                           const uint8_t* xT_e4m3, const uint8_t* xT_scales,
                                           uint16_t* dw_bf16, const int32_t* group_offsets, int32_t G,
                                           int64_t M_cap, int64_t N, int64_t K, hipStream_t stream);
+
+/* ---- the expert layer around the path: routing, dispatch, FP32-scaled product, combine ----
+ *
+ * The entry points above take rows that are in expert order already and the offsets that
+ * say so.  These make both from the router's logits and bring the experts' results back to
+ * the tokens:
+ *     mxfp4_route_topk           logits -> ids, weights      (backward: dweights -> dlogits)
+ *     mxfp4_expert_map           ids -> group_offsets, pos   (the row of every routed slot)
+ *     mxfp4_dispatch_rows        token rows -> MXFP4 rows in expert order
+ *     mxfp4_dispatch_fp8_rows    token rows -> E4M3 rows with FP32 scales, in expert order
+ *     mxfp4_fp8_block_gemm       expert product of those with 128x128-scaled weights
+ *     mxfp4_combine_rows         expert rows -> tokens       (backward: dy, dweights)
+ * A slot is choice j < k of token t, number t k + j; T k is at most 2^31 - 1 and k at most
+ * 64 (else MXFP4_ERR_SHAPE).  T == 0 enqueues nothing (but mxfp4_expert_map, which writes
+ * the zero offsets).  Pointers called optional may be NULL; all others, their alignment
+ * (16 bytes) and the errors are as above. */
+
+/* Routing.  With l = the logits of a token, FP32 or BF16, all arithmetic in FP32:
+ *     s_e = softmax(l)_e (MXFP4_SCORE_SOFTMAX) or 1 / (1 + exp(-l_e)) (MXFP4_SCORE_SIGMOID)
+ *     c_e = s_e + bias_e  (the bias steers the choice only; optional)
+ *     groups: n_group runs of E / n_group experts; a group's value is the sum of its
+ *             group_best (1 or 2) largest c; only the topk_group best groups stay
+ *     ids:     the k experts of largest c in the groups that stay, largest first
+ *     weights: scale s_id / (sum of the k s_id + 1e-20) if renorm, else scale s_id
+ * Equal values (groups and experts): the lower index first; a NaN counts as lower than
+ * every number.  So the ids are k different experts whatever the logits are.  A row of
+ * -inf only has s = 0 under softmax; a row that holds a NaN or +inf has NaN weights there.
+ *   logits   [T, E] FP32 (logits_f32 != 0) or BF16.      bias [E] (optional).
+ *   row_mask [T] (optional): a row whose byte is 0 gets ids -1 and weights 0.
+ *   ids, weights [T, k].
+ *   E at most 1024, n_group at most 64 and a divisor of E, group_best at most E / n_group,
+ *   k at most topk_group E / n_group, scale finite (else MXFP4_ERR_SHAPE). */
+mxfp4_status mxfp4_route_topk(const void* logits, int32_t logits_f32, const float* bias, const uint8_t* row_mask,
+                              int32_t* ids, float* weights, int64_t T, int32_t E, int32_t n_group,
+                              int32_t topk_group, int32_t group_best, int32_t k, int32_t score, int32_t renorm,
+                              float scale, hipStream_t stream);
+
+/* The router's gradient: dlogits (the logits' type) from the weights' gradient.  With
+ * D = sum_i s_i + 1e-20 over a token's ids,
+ *     ds_j = scale (dw_j - sum_i dw_i s_i / D) / D  if renorm, else scale dw_j
+ *     softmax: dl_e = s_e (ds_e - sum_j ds_j s_j);   sigmoid: dl_e = s_e (1 - s_e) ds_e
+ * (ds_e = 0 where e was not chosen; the choice itself has no gradient).  Ids outside
+ * [0, E) (masked rows) count as no choice; a token's ids are distinct otherwise. */
+mxfp4_status mxfp4_route_topk_backward(const void* logits, int32_t logits_f32, const int32_t* ids,
+                                       const float* dweights, void* dlogits, int64_t T, int32_t E, int32_t k,
+                                       int32_t score, int32_t renorm, float scale, hipStream_t stream);
+
+/* Bytes of workspace mxfp4_expert_map needs (0 for few slots); -1 for invalid sizes.  At
+ * most 256 G. */
+int64_t mxfp4_expert_map_workspace(int64_t T, int32_t k, int32_t G);
+
+/* The map between slots and rows.  Expert g here is the id first_expert + g, g < G (all
+ * experts, or one rank's share); slots with any other id have no row.  Rows are ordered by
+ * expert and then by slot (the same result every time).
+ *   ids  [T, k].            group_offsets [G + 1]: as every entry point takes them.
+ *   pos  [T, k]: the slot's row, or -1.   src [M_cap] (optional): a row's slot; rows from
+ *   group_offsets[G] on are not written.
+ *   Rows that do not fit M_cap are dropped: their pos is -1 and the offsets end at M_cap.
+ *   workspace: mxfp4_expert_map_workspace bytes (may be NULL where that is 0), not shared
+ *   by calls that overlap.  G at most 1024. */
+mxfp4_status mxfp4_expert_map(const int32_t* ids, int32_t* group_offsets, int32_t* pos, int32_t* src,
+                              void* workspace, int64_t T, int32_t k, int32_t first_expert, int32_t G, int64_t M_cap,
+                              hipStream_t stream);
+
+/* Token rows -> MXFP4 rows in expert order (technical summary section 2, item 2:
+ * activations are quantized right before they go to their experts): row pos[t, j] of the
+ * outputs gets what mxfp4_quantize_rows writes for row t of x.  Positions outside
+ * [0, M_cap) are skipped; other rows are not written.
+ *   x_bf16 [T, K] (finite values), codes [M_cap, K/2], scales [M_cap, K/32].
+ *   K must be a multiple of 32. */
+mxfp4_status mxfp4_dispatch_rows(const uint16_t* x_bf16, const int32_t* pos, uint8_t* codes, uint8_t* scales,
+                                 int64_t T, int32_t k, int64_t M_cap, int64_t K, hipStream_t stream);
+
+/* Token rows -> E4M3 rows with one FP32 scale per 1x128 block, in expert order.  With
+ * a = max(amax of the block, 2^-100): scale = a / 448, byte = E4M3(x * (448 / a)), each
+ * quotient and the product rounded to FP32, the byte to nearest even; a partial last block
+ * uses its elements only.  The gradient of x is mxfp4_combine_rows without weights on the
+ * rows' gradients.
+ *   x_bf16 [T, K] (finite values), y_e4m3 [M_cap, K], y_scales [M_cap, ceil(K/128)].
+ *   K must be a multiple of 16. */
+mxfp4_status mxfp4_dispatch_fp8_rows(const uint16_t* x_bf16, const int32_t* pos, uint8_t* y_e4m3, float* y_scales,
+                                     int64_t T, int32_t k, int64_t M_cap, int64_t K, hipStream_t stream);
+
+/* The same quantizer for rows [0, offs[G]) that are in expert order already (the operand
+ * of an expert's second product). */
+mxfp4_status mxfp4_bf16_to_fp8_rows_f32(const uint16_t* x_bf16, uint8_t* y_e4m3, float* y_scales,
+                                        const int32_t* group_offsets, int32_t G, int64_t M_cap, int64_t K,
+                                        hipStream_t stream);
+
+/* Expert-grouped FP8 product with FP32 block scales (1x128 for the activations, 128x128
+ * for the weights).  For the expert g owning row m and b = k / 128:
+ *   y[m, n] = bf16( sum_b a_scales[m, b] w_scales[g, n / 128, b] sum_{k in b} A[m, k] W[g, n, k] )
+ *   a_e4m3   [M_cap, K], a_scales [M_cap, ceil(K/128)].
+ *   w_e4m3   [G, N, K],  w_scales [G, ceil(N/128), ceil(K/128)].
+ *   y_bf16   [M_cap, N]; rows [offs[G], M_cap) are not written.
+ *   Each block's sum is the matrix cores' (FP32), the sum over blocks FP32, rounded once.
+ *   K must be a multiple of 16, N a multiple of 8, both at most 2^20.  No NaN bytes in the
+ *   operands.  One dense matrix is G = 1.  The gradient of A is the same call with the
+ *   output gradient's rows and the weights transposed, W[g, n, k] -> [g, k, n] with
+ *   w_scales transposed alike (which loses nothing). */
+mxfp4_status mxfp4_fp8_block_gemm(const uint8_t* a_e4m3, const float* a_scales, const uint8_t* w_e4m3,
+                                  const float* w_scales, uint16_t* y_bf16, const int32_t* group_offsets, int32_t G,
+                                  int64_t M_cap, int64_t N, int64_t K, hipStream_t stream);
+
+/* Expert rows back to their tokens: out[t] = base[t] + sum_j weights[t, j] y[pos[t, j]] over
+ * the choices with 0 <= pos < M_cap, summed in FP32 in the order of j and rounded once.
+ *   y_bf16 [M_cap, K], pos [T, k], weights [T, k] (optional: 1), base_bf16 [T, K]
+ *   (optional: 0), out_bf16 [T, K] (every row is written).
+ *   K must be a multiple of 8. */
+mxfp4_status mxfp4_combine_rows(const uint16_t* y_bf16, const int32_t* pos, const float* weights,
+                                const uint16_t* base_bf16, uint16_t* out_bf16, int64_t T, int32_t k, int64_t M_cap,
+                                int64_t K, hipStream_t stream);
+
+/* Its gradients: dy[pos[t, j]] = bf16(weights[t, j] dout[t]), dweights[t, j] = <dout[t],
+ * y[pos[t, j]]> (FP32; 0 for a choice without a row).  Rows of dy without a slot are not
+ * written; the gradient of base is dout.  Positions are distinct (as mxfp4_expert_map
+ * makes them).  K must be a multiple of 8. */
+mxfp4_status mxfp4_combine_rows_backward(const uint16_t* dout_bf16, const uint16_t* y_bf16, const int32_t* pos,
+                                         const float* weights, uint16_t* dy_bf16, float* dweights, int64_t T,
+                                         int32_t k, int64_t M_cap, int64_t K, hipStream_t stream);
 
 /* Bytes the column-layout scale buffer needs for any offsets with offs[G] <= M_cap:
  * K * (ceil(M_cap / 128) + G).  Returns -1 for invalid sizes. */
