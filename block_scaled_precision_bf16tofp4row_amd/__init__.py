@@ -201,10 +201,19 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _current_stream() -> int:
+    """The raw current stream of the current device.  torch.cuda.current_stream() builds a
+    Stream object around it, which costs more than a small call's launch."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None or not torch.cuda.is_initialized():
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch._C._cuda_getDevice())
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -220,18 +229,29 @@ def _need(what: str, args):
     enough for the launch, of an accepted dtype and contiguous, then all on the GPU.
     `args` holds (tensor, bytes needed, name, accepted dtypes); raw int device
     addresses and None are passed through unchecked."""
-    tensors = [a for a in args if a[0] is not None and not isinstance(a[0], int)]
-    for t, nbytes, name, dtypes in tensors:
-        have = t.numel() * t.element_size()
+    for t, nbytes, name, dtypes in args:
+        if t is None or isinstance(t, int):
+            continue
+        have = t.nbytes
         if have < nbytes:
             raise ValueError(f"{what}: {name} holds {have} bytes, the launch needs {nbytes}")
-        if str(t.dtype).replace("torch.", "") not in dtypes:
+        if _dtype_name(t.dtype) not in dtypes:
             raise ValueError(f"{what}: {name} has dtype {t.dtype}, expected one of {', '.join(dtypes)}")
         if not t.is_contiguous():
             raise ValueError(f"{what}: {name} must be contiguous")
-    for t, _, name, _ in tensors:
-        if not t.is_cuda:
+    for t, _, name, _ in args:
+        if t is not None and not isinstance(t, int) and not t.is_cuda:
             raise ValueError(f"{what}: {name} must be a GPU tensor")
+
+
+_dtype_names: dict = {}
+
+
+def _dtype_name(dtype) -> str:
+    name = _dtype_names.get(dtype)
+    if name is None:
+        name = _dtype_names[dtype] = str(dtype).replace("torch.", "")
+    return name
 
 
 _U8 = ("uint8",)
@@ -433,7 +453,9 @@ def _score(score) -> int:
 def _at(t) -> int | None:
     """_ptr, with an address that nothing reads for a tensor without elements (torch gives
     those none, and NULL is an error)."""
-    return _ptr(t) or (16 if t is not None and not isinstance(t, int) and t.numel() == 0 else None)
+    if t is None or isinstance(t, int):
+        return t
+    return t.data_ptr() or 16
 
 
 def _logits_dims(logits, ids, T, E, k, f32):
@@ -445,7 +467,7 @@ def _logits_dims(logits, ids, T, E, k, f32):
     if k is None:
         k = ids.shape[1]
     if f32 is None:
-        f32 = isinstance(logits, int) or str(logits.dtype) == "torch.float32"
+        f32 = isinstance(logits, int) or _dtype_name(logits.dtype) == "float32"
     return int(T), int(E), int(k), bool(f32)
 
 
