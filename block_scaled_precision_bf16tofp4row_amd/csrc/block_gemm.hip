@@ -3,18 +3,27 @@
 // For the expert g that owns row m (offs[g] <= m < offs[g+1]):
 //     y[m, n] = bf16( sum_b sa[m, b] sw_g[n / 128, b] sum_{k in block b} A[m, k] W_g[n, k] )
 // A [M, K], W_g [N, K] E4M3, b = k / 128; the last block of K and of N may be partial.
-// The matrix cores cannot apply an FP32 scale, so each 128-block of K is summed by two
-// v_mfma_f32_32x32x64_f8f6f4 from zero and added to the FP32 accumulators under its scale
-// (16 multiply-adds of the vector unit per two 64-cycle matrix instructions).  With the
-// weights as the first operand and the tokens as the second, a lane's 16 results belong to
-// one token, so the scale sa sw is one number per lane and tile.
+// The matrix cores cannot apply an FP32 scale, so a block's sum has to leave them before it
+// is added: v_mfma_f32_16x16x128_f8f6f4 sums a whole block in one instruction from zero, and
+// its 4 results per lane go into the FP32 accumulators with one multiply-add each.  With the
+// weights as the first operand and the tokens as the second, a lane's results belong to one
+// token, so the scale sa sw is one number per lane and token tile.  (Two chained
+// v_mfma_f32_32x32x64 per block, 16 results each, measured 1490 us where this form, in the
+// first version of the same tile, took 1225.)
 //
-// A workgroup owns a TM x TN tile of one expert and walks K in stages of 128 through two
-// LDS buffers: the next stage's operand bytes go from memory to LDS (buffer_load ... lds)
-// while the present one is multiplied.  LDS rows are 128 bytes with 16-byte chunk c of row
-// r at chunk c ^ ((r >> 1) & 7), so that the fragment reads of 16 rows hit distinct banks.
-// Rows past the expert's and features past N are outside the buffers' ranges and read as
-// zero; so are a row's bytes past K (their lanes' offsets are put out of range).
+// What bounds it (32768 rows x 7168 x 4096, 8 experts, 960-980 us, 1.96-2.0 PFLOP/s; this
+// library's UE8M0-scaled product of that size, where the matrix cores apply the scales,
+// takes 802, the vendor library's per-tensor-scaled FP8 product 710): the matrix
+// instructions fill 2048 cycles of a 256 x 256 tile's stage, the scaled adds half as many
+// vector cycles beside them, the fragment reads 1536 LDS cycles and the loads 512.  With few
+// rows it is the weights' bytes: 128 rows over 32 experts x 4096 x 7168 take 157 us, 6.0 TB/s.
+//
+// Two kernels.  The tile kernel stages both operands in LDS and serves everything from a few
+// rows per expert on; the rows kernel reads fragments straight from memory and splits K over
+// its waves, for a row or so per expert, or so few tiles that a tile's walk along K is the
+// time.  Buffer loads take the bounds: rows past the expert's and features past N are
+// outside the ranges and read as zero, and a lane whose bytes are past K gets an offset
+// outside every range.
 #include "tiles.h"
 
 namespace mxfp4 {
@@ -22,12 +31,25 @@ namespace mxfp4 {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kBK = 128;                          // K per stage: one scale block
 constexpr uint32_t kOutOfRange = 0x80000000u;     // offset past every buffer's range
+// s_waitcnt immediate (gfx9 encoding) that waits for vmcnt <= n and nothing else.
+constexpr int vmcnt_at_most(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 constexpr int kUnitScale = 0x7F7F7F7F;            // E8M0 bytes of 1.0
+
+// Memory to LDS: lane L's 16 (or 4) bytes at offset off + k0 of the resource land at `to` +
+// 16 L (4 L).
+__device__ __forceinline__ void load16_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t off, uint32_t k0)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) uint8_t*)to, 16, off, (int)k0, 0, 0);
+}
+__device__ __forceinline__ void load4_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t off)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) uint8_t*)to, 4, off, 0, 0, 0);
+}
 
 // A lane's fragment of one operand row for 64 of K: the row's 16-byte LDS chunks at byte
 // offsets c0 and c1.
@@ -38,25 +60,232 @@ __device__ __forceinline__ i32x8 frag(const uint8_t* rowp, uint32_t c0, uint32_t
     return i32x8{(int)v0.x, (int)v0.y, (int)v0.z, (int)v0.w, (int)v1.x, (int)v1.y, (int)v1.z, (int)v1.w};
 }
 
-__device__ __forceinline__ f32x16 mfma64(i32x8 w, i32x8 a, f32x16 c)
+__device__ __forceinline__ f32x4 mfma128(i32x8 w, i32x8 a, f32x4 c)
 {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, a, c, 0, 0, 0, kUnitScale, 0, kUnitScale);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 0, 0, 0, kUnitScale, 0, kUnitScale);
 }
 
 }  // namespace
 
-// WM x WN waves; a wave computes MT x NT tiles of 32 tokens x 32 features.
-template <int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 1) void block_gemm_kernel(
+// A workgroup barrier behind this wave's LDS reads and writes.  __syncthreads would also wait
+// for every load into LDS in flight, those of the stages to come among them; the stage loop
+// waits for the ones it needs by count.
+__device__ __forceinline__ void meet()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// What a wave needs in its stage loop.
+template <int D>
+struct TileCtx {
+    uint8_t* buf[D];                              // the LDS stage buffers
+    float* scl;                                   // staged token scales: [2 pairs][2 stages][slots]
+    __amdgpu_buffer_rsrc_t ra, rw, rsa, rsw;      // operand rows, token and weight scales
+    uint32_t abase, wbase, ac0, ac1, wc0, wc1, K; // loader: row offsets and the two chunk offsets of each
+    uint32_t lds_a, lds_w, lds_s;                 // loader: LDS offsets of the wave's first rows, scale slots
+    uint32_t srow, sslot;                         // scale loader: global offset of the row, LDS slot
+    uint32_t arow, wrow, c0, c1;                  // fragments: LDS offsets of the lane's rows, chunks
+    uint32_t scl_at;                              // slot of the lane's first token scale
+};
+
+// The tile of WM x WN waves, each 16 MT tokens x 16 NT features, with D stage buffers.
+template <int WM, int WN, int MT, int NT, int D>
+struct Tile {
+    static constexpr int TM = 16 * MT * WM, TN = 16 * NT * WN;
+    static constexpr int kWaves = WM * WN;
+    static constexpr int kStage = (TM + TN) * kBK;
+    static constexpr int kLoadsA = TM / 8 / kWaves, kLoadsW = TN / 8 / kWaves;   // 8-row loads of a wave
+    static constexpr int kSlots = 64 * kWaves;              // scale slots (those past TM are not read)
+    static constexpr int kTiles = MT * NT;
+    static constexpr int kLag = 2;                          // products in flight before their scaled add
+    // Scales: with two buffers, those of two stages at a time go through registers to LDS
+    // (half the requests); with four, each stage's go into its buffer with the operands, a
+    // wave's token slots and then its weights' scale, so that no register waits for memory
+    // over several stages.
+    static constexpr bool kDmaScales = D == 4;
+    static constexpr int kBuf = kStage + (kDmaScales ? 8 * kSlots : 0);
+    // While stage s + 1 is awaited, the loads of stages s + 2 .. s + D - 1 may be in flight.
+    static constexpr int kInFlight = (D - 2) * (kLoadsA + kLoadsW + 2);
+    static_assert(D == 2 || D == 4, "stage buffers");
+    static_assert(TM % (8 * kWaves) == 0 && TN % (8 * kWaves) == 0 && TM <= kSlots, "loads");
+    static_assert(TN % 128 == 0 && 128 % (16 * NT) == 0, "a wave's features lie in one scale block");
+    static_assert(2 * kStage >= TM * TN * 2, "the epilogue stages the tile in two buffers");
+    static_assert((MT == 2 || MT % 4 == 0) && kTiles % 4 == 0, "scale reads, ring of products");
+
+    struct State {
+        f32x4 acc[MT][NT];
+        f32x4 p[4];                               // products on their way to acc
+        i32x8 fw[NT], fa[2];
+        float raw[MT], sc[MT];                    // next and present token scales (sc: times the weights')
+        float wsc[D];                             // the weights' scale of the stages
+        float ld[D];                              // token scales on their way to LDS
+    };
+
+    static __device__ __forceinline__ float load_f32(__amdgpu_buffer_rsrc_t r, uint32_t off)
+    {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
+    }
+    // Part `part` of NT of the operand loads of stage s into buffer b = s % D.  Offsets are
+    // made here, from registers that live across the stages; a stage past the last reads
+    // nothing (its columns are past K).
+    static __device__ __forceinline__ void issue_operands(const TileCtx<D>& cx, int b, uint32_t s, int part)
+    {
+        const uint32_t k0 = s * kBK;
+#pragma unroll
+        for (int j = part * (kLoadsA + kLoadsW) / NT; j < (part + 1) * (kLoadsA + kLoadsW) / NT; ++j) {
+            const bool tok = j < kLoadsA;
+            const int i = tok ? j : j - kLoadsA;
+            const uint32_t c = tok ? (i & 1 ? cx.ac1 : cx.ac0) : (i & 1 ? cx.wc1 : cx.wc0);
+            const uint32_t off = c + k0 < cx.K ? (tok ? cx.abase : cx.wbase) + c : kOutOfRange;
+            load16_to_lds(tok ? cx.ra : cx.rw, cx.buf[b] + (tok ? cx.lds_a : cx.lds_w) + 8 * i * kBK,
+                          off + 8u * i * cx.K, k0);
+        }
+    }
+    // Its scales.
+    static __device__ __forceinline__ void issue_scales(const TileCtx<D>& cx, State& t, int b, uint32_t s)
+    {
+        const uint32_t k0 = s * kBK;
+        if constexpr (kDmaScales) {
+            uint8_t* const to = cx.buf[b] + kStage + cx.lds_s;
+            load4_to_lds(cx.rsa, to, k0 < cx.K ? cx.srow + 4 * s : kOutOfRange);
+            load4_to_lds(cx.rsw, to + 4 * kSlots, 4 * s);
+            return;
+        }
+        t.wsc[b] = load_f32(cx.rsw, 4 * s);
+        if (b % 2 == 0) {
+            t.ld[b] = load_f32(cx.rsa, k0 < cx.K ? cx.srow + 4 * s : kOutOfRange);
+            t.ld[b + 1] = load_f32(cx.rsa, k0 + kBK < cx.K ? cx.srow + 4 * s + 4 : kOutOfRange);
+        }
+    }
+    // The token scales of stages s, s + 1 (s even, buffer b) to LDS.
+    static __device__ __forceinline__ void store_scales(const TileCtx<D>& cx, const State& t, int b, uint32_t s)
+    {
+        float* const to = cx.scl + (s & 2) * kSlots + cx.sslot;
+        to[0] = t.ld[b];
+        to[kSlots] = t.ld[b + 1];
+    }
+    // The scales of stage s (buffer b).
+    static __device__ __forceinline__ void read_scales(const TileCtx<D>& cx, State& t, int b, uint32_t s)
+    {
+        if constexpr (kDmaScales) {
+            const float* const from = reinterpret_cast<const float*>(cx.buf[b] + kStage);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                t.raw[i] = from[cx.scl_at + i];
+            t.wsc[b] = from[kSlots + cx.sslot];
+            return;
+        }
+        const float* const from = cx.scl + (s & 3) * kSlots + cx.scl_at;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            t.raw[i] = from[i];
+    }
+    static __device__ __forceinline__ i32x8 token_frag(const TileCtx<D>& cx, int b, int mt)
+    {
+        return frag(cx.buf[b] + cx.arow + 16 * mt * kBK, cx.c0, cx.c1);
+    }
+    static __device__ __forceinline__ i32x8 weight_frag(const TileCtx<D>& cx, int b, int nt)
+    {
+        return frag(cx.buf[b] + cx.wrow + 16 * nt * kBK, cx.c0, cx.c1);
+    }
+    // The scaled add of product I of a stage (of the stage before, for I < 0).
+    template <int I>
+    static __device__ __forceinline__ void add(State& t)
+    {
+        constexpr int i = (I + kTiles) % kTiles, mt = i / NT, nt = i % NT;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            t.acc[mt][nt][e] = __builtin_fmaf(t.sc[mt], t.p[i & 3][e], t.acc[mt][nt][e]);
+    }
+    // Products I .. END - 1, each followed by the scaled add of the one kLag before it, in
+    // this order (the scheduler would put dependent ones together).  In the stage's last
+    // token tile a weight fragment is replaced by the next stage's (buffer b) after its use.
+    template <int I, int END>
+    static __device__ __forceinline__ void products(const TileCtx<D>& cx, State& t, int b, uint32_t s)
+    {
+        if constexpr (I < END) {
+            t.p[I & 3] = mfma128(t.fw[I % NT], t.fa[I / NT % 2], f32x4{});
+            if constexpr (I / NT == MT - 1) {
+                t.fw[I % NT] = weight_frag(cx, b, I % NT);
+                if constexpr (D == 4)
+                    issue_operands(cx, (b + D - 1) % D, s, I % NT);
+            }
+            if constexpr (I >= kLag)
+                add<I - kLag>(t);
+            __builtin_amdgcn_sched_barrier(0);
+            products<I + 1, END>(cx, t, b, s);
+        }
+    }
+    template <int M>
+    static __device__ __forceinline__ void token_tiles(const TileCtx<D>& cx, State& t, int b)
+    {
+        if constexpr (M < MT - 1) {
+            t.fa[(M + 1) % 2] = token_frag(cx, b, M + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            products<M * NT, (M + 1) * NT>(cx, t, 0, 0);
+            token_tiles<M + 1>(cx, t, b);
+        }
+    }
+    // Stage s in buffer B = s % D.
+    template <int B>
+    static __device__ __forceinline__ void stage(const TileCtx<D>& cx, State& t, uint32_t s)
+    {
+        constexpr int kNext = (B + 1) % D;
+        __builtin_amdgcn_s_setprio(1);
+        add<-2>(t);
+        add<-1>(t);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+            t.sc[mt] = t.raw[mt] * t.wsc[B];
+        token_tiles<0>(cx, t, B);
+        __builtin_amdgcn_s_setprio(0);
+        // every fragment of this stage is in registers: wait for the next one's loads, meet
+        // the others, and load a later one into this buffer
+        __builtin_amdgcn_s_waitcnt(vmcnt_at_most(kInFlight));
+        if (!kDmaScales && B % 2 == 1)
+            store_scales(cx, t, kNext, s + 1);
+        if constexpr (D == 2) {
+            __syncthreads();
+#pragma unroll
+            for (int part = 0; part < NT; ++part)
+                issue_operands(cx, B, s + D, part);
+        } else {
+            meet();                               // (the operand loads go between the products)
+        }
+        issue_scales(cx, t, B, s + D);
+        read_scales(cx, t, kNext, s + 1);
+        t.fa[0] = token_frag(cx, kNext, 0);
+        products<(MT - 1) * NT, kTiles>(cx, t, kNext, s + D);
+    }
+};
+
+// The tile kernel: WM x WN waves, K in stages of 128 (one scale block) through D LDS buffers.
+// LDS rows are 128 bytes with 16-byte chunk c of row r at chunk c ^ ((r >> 1) & 7), so that
+// the fragment reads of 16 rows hit distinct banks; operand bytes go there straight from
+// memory.  A stage: products of all but the last token tile, each token fragment read one
+// tile ahead; wait for the next stage's loads, barrier; products of the last token tile,
+// while the next stage's first fragments are read (a weight fragment right after its last
+// use) and a later stage's loads go out into the buffer just left.  So the barrier never
+// finds a wave without matrix work behind it, and the scaled adds run two products late.
+// D = 2 for the tiles of 64 KB and 32 KB stages that share a CU or fill it; D = 4 where a CU
+// holds one workgroup with little work per stage, which would wait for memory each time (128
+// x 128, 1024 rows x 4096 x 4096: 25.5 us with 8 waves and D = 4, 28.7 with 4 and D = 2).
+template <int WM, int WN, int MT, int NT, int D>
+__global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
     const float* __restrict__ sw, uint16_t* __restrict__ y, const int32_t* __restrict__ offs, int G, int64_t N,
     int64_t K, uint32_t ntn)
 {
-    constexpr int MT = TM / WM / 32, NT = TN / WN / 32;
-    constexpr int kStage = (TM + TN) * kBK;
-    constexpr int kLoads = (TM + TN) / 8 / (WM * WN);       // 8-row loads of a wave per stage
-    static_assert(128 % (32 * NT) == 0 && TN % 128 == 0, "a wave's features lie in one scale block");
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][kStage];
+    typedef Tile<WM, WN, MT, NT, D> W;
+    constexpr int TM = W::TM, TN = W::TN, kWaves = W::kWaves;
+    // separate arrays: what is loaded into one does not hold up reads of another
+    __shared__ __attribute__((aligned(16))) uint8_t lds0[W::kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds1[W::kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds2[D == 4 ? W::kBuf : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t lds3[D == 4 ? W::kBuf : 16];
+    __shared__ __attribute__((aligned(16))) float scl[W::kDmaScales ? 4 : 4 * W::kSlots];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -72,132 +301,298 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void block_gemm_kernel(
     const int cols = (int)min((int64_t)TN, N - n0);
     const uint32_t kb_n = (uint32_t)((K + kBK - 1) / kBK);
     const uint32_t nb_n = (uint32_t)((N + 127) / 128);
+    const int wm = wave % WM, wn = wave / WM;
+    const uint32_t r = (uint32_t)(lane & 15), h = (uint32_t)(lane >> 4);
+
+    // loader: instruction i of wave w fills token rows 8 (kLoadsA w + i) .. + 7 (and feature
+    // rows alike); lane L takes row L / 8 of them and LDS chunk L % 8, the row's chunk
+    // (L % 8) ^ ((row >> 1) & 7), which is the same for every other i.  Token scales: slot
+    // 64 w + L, which is token tile slot % MT of row slot / MT % 16 of wave row slot / (16 MT)
+    const uint32_t l8 = (uint32_t)(lane >> 3), l16 = (uint32_t)(lane >> 4), lc = (uint32_t)(lane & 7);
+    const uint32_t ag = (uint32_t)(W::kLoadsA * wave), wg = (uint32_t)(W::kLoadsW * wave);   // first 8-row groups
+    const uint32_t slot = (uint32_t)tid;
+    const uint32_t srow = slot / (16 * MT) * (16 * MT) + slot % MT * 16 + slot / MT % 16;
+    const uint32_t nb = min((uint32_t)(n0 + 16 * NT * wn) / 128, nb_n - 1);
+    TileCtx<D> cx;
+    cx.buf[0] = lds0;
+    cx.buf[1] = lds1;
+    if constexpr (D == 4) {
+        cx.buf[2] = lds2;
+        cx.buf[3] = lds3;
+    }
+    cx.scl = scl;
+    cx.ra = strip_rsrc(a + row0 * K, (uint64_t)rows * (uint64_t)K);
+    cx.rw = strip_rsrc(w + ((int64_t)g * N + n0) * K, (uint64_t)cols * (uint64_t)K);
+    cx.rsa = strip_rsrc(sa + row0 * kb_n, (uint64_t)rows * kb_n * 4);
+    cx.rsw = strip_rsrc(sw + ((int64_t)g * nb_n + nb) * kb_n, (uint64_t)kb_n * 4);
+    cx.K = (uint32_t)K;
+    cx.abase = (8 * ag + l8) * cx.K;
+    cx.wbase = (8 * wg + l8) * cx.K;
+    cx.ac0 = 16 * (lc ^ ((4 * ag + l16) & 7));
+    cx.ac1 = 16 * (lc ^ ((4 * ag + 4 + l16) & 7));
+    cx.wc0 = 16 * (lc ^ ((4 * wg + l16) & 7));
+    cx.wc1 = 16 * (lc ^ ((4 * wg + 4 + l16) & 7));
+    cx.lds_a = 8 * ag * kBK;
+    cx.lds_w = (TM + 8 * wg) * kBK;
+    cx.lds_s = 256 * (uint32_t)wave;
+    cx.srow = srow * kb_n * 4;
+    cx.sslot = slot;
+    cx.arow = (uint32_t)(16 * MT * wm + r) * kBK;
+    cx.wrow = (uint32_t)(TM + 16 * NT * wn + r) * kBK;
+    cx.c0 = 16 * (h ^ ((r >> 1) & 7));
+    cx.c1 = 16 * ((4 + h) ^ ((r >> 1) & 7));
+    cx.scl_at = (16 * (uint32_t)wm + r) * MT;
+
+    typename W::State t;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+        t.sc[mt] = 0.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            t.acc[mt][nt] = f32x4{};
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        t.p[i] = f32x4{};
+#pragma unroll
+    for (int b = 0; b < D; ++b) {
+        W::issue_scales(cx, t, b, b);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            W::issue_operands(cx, b, b, nt);
+        __builtin_amdgcn_sched_barrier(0);        // (the waits count the loads in this order)
+    }
+    // with scales in registers everything is awaited: loads into LDS and loads into registers
+    // do not return in one order (measured: counting over both let a stage start early), so
+    // only a kernel whose loads all go to LDS may wait by count
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most(W::kDmaScales ? W::kInFlight + W::kLoadsA + W::kLoadsW + 2 : 0));
+    if constexpr (!W::kDmaScales) {
+        asm volatile("" : "+v"(t.wsc[0]), "+v"(t.wsc[1]));   // loaded by now, not in the loop's way
+        W::store_scales(cx, t, 0, 0);
+    }
+    meet();
+    W::read_scales(cx, t, 0, 0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+        t.fw[nt] = W::weight_frag(cx, 0, nt);
+    t.fa[0] = W::token_frag(cx, 0, 0);
+    // D stages at a time; the loads and reads for a stage past the end find zeros, which add
+    // nothing (leaving the loop between its stages made the compiler copy the accumulators)
+    for (uint32_t s = 0; s < kb_n; s += D) {
+        W::template stage<0>(cx, t, s);
+        W::template stage<1>(cx, t, s + 1);
+        if constexpr (D == 4) {
+            W::template stage<2>(cx, t, s + 2);
+            W::template stage<3>(cx, t, s + 3);
+        }
+    }
+    W::template add<-2>(t);
+    W::template add<-1>(t);
+
+    // epilogue through LDS: lane (r, h) of tile (mt, nt) holds token 16 (MT wm + mt) + r and
+    // features 16 (NT wn + nt) + 4 h + (0..3); a token's row is 2 TN bytes there with 16-byte
+    // chunk c at chunk c ^ (token % 16), then whole row segments go out, 16 bytes a lane
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0));  // no load into LDS is left
+    __syncthreads();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const f32x4& v = t.acc[mt][nt];
+            const bf16x2 p0 = {(__bf16)v[0], (__bf16)v[1]};
+            const bf16x2 p1 = {(__bf16)v[2], (__bf16)v[3]};
+            const uint32_t c = (uint32_t)(2 * (NT * wn + nt)) + (h >> 1);
+            const uint32_t row = (uint32_t)(16 * (MT * wm + mt)) + r;
+            *reinterpret_cast<u32x2*>((row < TM / 2 ? lds0 : lds1) + row % (TM / 2) * (2 * TN) + 16 * (c ^ r) +
+                                      8 * (h & 1)) =
+                u32x2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
+        }
+    __syncthreads();
+    const __amdgpu_buffer_rsrc_t ry = strip_rsrc(y + row0 * N, (uint64_t)rows * (uint64_t)N * 2);
+    constexpr int kChunks = TN / 8;               // 16-byte chunks of a row
+    constexpr int kRows = 64 * kWaves / kChunks;  // rows per pass
+    const uint32_t c = (uint32_t)tid % kChunks;
+#pragma unroll
+    for (int i = 0; i < TM / kRows; ++i) {
+        const uint32_t row = (uint32_t)tid / kChunks + kRows * i;
+        const uint8_t* const from =
+            (row < TM / 2 ? lds0 : lds1) + row % (TM / 2) * (2 * TN) + 16 * (c ^ (row & 15));
+        const uint32_t off = (int)(8 * c) < cols ? (row * (uint32_t)N + (uint32_t)n0) * 2 + 16 * c : kOutOfRange;
+        __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(from), ry, (int)off, 0, 2);
+    }
+}
+
+// The kernel for few rows per expert, where the weights are the traffic: a workgroup owns
+// 16 MT tokens x 16 NT features and its W waves share K, each a run of blocks whose operands
+// go from memory straight into the fragments' registers (a lane's two 16-byte chunks of a
+// row; four lanes cover 64 contiguous bytes), kAhead blocks ahead.  The waves' sums meet in
+// LDS and are added in wave order.
+template <int MT, int NT, int W>
+__global__ __launch_bounds__(64 * W) void block_gemm_rows_kernel(
+    const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
+    const float* __restrict__ sw, uint16_t* __restrict__ y, const int32_t* __restrict__ offs, int G, int64_t N,
+    int64_t K, uint32_t ntm)
+{
+    constexpr int TM = 16 * MT, TN = 16 * NT, kAhead = 3;
+    constexpr int kRow = TN + 4;                  // floats of a token's row in LDS
+    __shared__ __attribute__((aligned(16))) float part[W][TM][kRow];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // feature tile by feature tile, token tiles inside: the token tiles of an expert follow
+    // each other on one XCD and share the weights in its L2
+    const uint32_t lin = xcd_remap(blockIdx.x, gridDim.x);
+    int g;
+    int64_t row0;
+    int rows;
+    if (!find_tile<TM>(offs, G, lin % ntm, g, row0, rows))
+        return;                                   // uniform over the workgroup
+    const int64_t n0 = (int64_t)TN * (lin / ntm);
+    const int cols = (int)min((int64_t)TN, N - n0);
+    const uint32_t kb_n = (uint32_t)((K + kBK - 1) / kBK);
+    const uint32_t nb_n = (uint32_t)((N + 127) / 128);
+    const uint32_t kb0 = kb_n * wave / W, kb1 = kb_n * (wave + 1) / W;
+    const uint32_t r = (uint32_t)(lane & 15), h = (uint32_t)(lane >> 4);
 
     const __amdgpu_buffer_rsrc_t ra = strip_rsrc(a + row0 * K, (uint64_t)rows * (uint64_t)K);
     const __amdgpu_buffer_rsrc_t rw = strip_rsrc(w + ((int64_t)g * N + n0) * K, (uint64_t)cols * (uint64_t)K);
     const __amdgpu_buffer_rsrc_t rsa = strip_rsrc(sa + row0 * kb_n, (uint64_t)rows * kb_n * 4);
+    const __amdgpu_buffer_rsrc_t rsw = strip_rsrc(sw + ((int64_t)g * nb_n + n0 / 128) * kb_n, (uint64_t)kb_n * 4);
 
-    // loader: instruction i of wave w fills rows 8 (kLoads w + i) .. + 7 of the stage (tokens,
-    // then features); lane L takes row L / 8 of them and LDS chunk L % 8
-    uint32_t loff[kLoads], lcol[kLoads];
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const uint32_t lrow = (uint32_t)(8 * (kLoads * wave + i) + (lane >> 3));
-        const uint32_t r = lrow < TM ? lrow : lrow - TM;
-        lcol[i] = 16 * ((uint32_t)(lane & 7) ^ ((lrow >> 1) & 7));
-        loff[i] = r * (uint32_t)K + lcol[i];
-    }
-    auto issue = [&](uint32_t s, int buf) {
-        typedef __attribute__((address_space(3))) uint8_t lds_u8;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int row8 = 8 * (kLoads * wave + i);
-            const uint32_t off = lcol[i] + s * kBK < (uint32_t)K ? loff[i] : kOutOfRange;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(row8 < TM ? ra : rw, (lds_u8*)lds[buf] + row8 * kBK, 16, off,
-                                                     (int)(s * kBK), 0, 0);
-        }
+    struct Block {
+        i32x8 w[NT], a[MT];
+        float sa[MT], sw;
     };
-
-    const int wm = wave % WM, wn = wave / WM;
-    const uint32_t r = (uint32_t)(lane & 31), h = (uint32_t)(lane >> 5);
-    const uint32_t sw8 = (r >> 1) & 7;            // the swizzle of rows r + 32 x
-    // scales: a lane's tokens, and the wave's block of features
-    const uint32_t nb = min((uint32_t)(n0 + 32 * NT * wn) / 128, nb_n - 1);
-    const float* const swp = sw + ((int64_t)g * nb_n + nb) * kb_n;
-    uint32_t soff[MT];
-    float sc[MT], sc_next[MT];
+    auto chunk = [&](__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t k) {
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             rs, (int)(k < (uint32_t)K ? off + k : kOutOfRange), 0, 0));
+    };
+    auto row_of = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, uint32_t kb) {
+        // (a block of another wave's run, or past the last, reads nothing)
+        const uint32_t k = kb < kb1 ? kb * kBK + 16 * h : kOutOfRange;
+        const u32x4 v0 = chunk(rs, row * (uint32_t)K, k), v1 = chunk(rs, row * (uint32_t)K, k + 64);
+        return i32x8{(int)v0.x, (int)v0.y, (int)v0.z, (int)v0.w, (int)v1.x, (int)v1.y, (int)v1.z, (int)v1.w};
+    };
+    auto load = [&](Block& b, uint32_t kb) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-        soff[mt] = (uint32_t)(32 * (MT * wm + mt) + r) * kb_n * 4;
-    auto load_scales = [&](uint32_t s, float (&to)[MT]) {
-        const float b = swp[s];
+        for (int nt = 0; nt < NT; ++nt)
+            b.w[nt] = row_of(rw, 16 * nt + r, kb);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
-            to[mt] = b * __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsa, (int)soff[mt], (int)(4 * s), 0));
+            b.a[mt] = row_of(ra, 16 * mt + r, kb);
+        b.sw = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+            rsw, (int)(kb < kb1 ? 4 * kb : kOutOfRange), 0, 0));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+            b.sa[mt] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+                rsa, (int)(kb < kb1 ? ((16 * mt + r) * kb_n + kb) * 4 : kOutOfRange), 0, 0));
     };
-
-    f32x16 acc[MT][NT];
+    f32x4 acc[MT][NT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-            acc[mt][nt] = f32x16{};
-
-    issue(0, 0);
-    load_scales(0, sc);
-    for (uint32_t s = 0; s < kb_n; ++s) {
-        const int buf = s & 1;
-        __builtin_amdgcn_s_waitcnt(0x0F70);       // vmcnt(0): this lane's loads of stage s are in LDS
-        __syncthreads();                          // everybody's are, and the other buffer is read
-        if (s + 1 < kb_n) {
-            issue(s + 1, buf ^ 1);
-            load_scales(s + 1, sc_next);
+            acc[mt][nt] = f32x4{};
+    Block blk[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        load(blk[u], kb0 + u);
+    for (uint32_t kb = kb0; kb < kb1; kb += kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            Block& b = blk[u];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const f32x4 p = mfma128(b.w[nt], b.a[mt], f32x4{});
+                    const float sc = b.sa[mt] * b.sw;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[mt][nt][i] = __builtin_fmaf(sc, p[i], acc[mt][nt][i]);
+                }
+            load(b, kb + kAhead + u);
         }
-        i32x8 fw[2][NT];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t c0 = 16 * ((4 * j + h) ^ sw8), c1 = 16 * ((4 * j + 2 + h) ^ sw8);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                fw[j][nt] = frag(lds[buf] + (TM + 32 * (NT * wn + nt) + r) * kBK, c0, c1);
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-            i32x8 fa[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                fa[j] = frag(lds[buf] + (32 * (MT * wm + mt) + r) * kBK, 16 * ((4 * j + h) ^ sw8),
-                             16 * ((4 * j + 2 + h) ^ sw8));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                f32x16 p = mfma64(fw[0][nt], fa[0], f32x16{});
-                p = mfma64(fw[1][nt], fa[1], p);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    acc[mt][nt][i] = __builtin_fmaf(sc[mt], p[i], acc[mt][nt][i]);
-            }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            sc[mt] = sc_next[mt];
     }
-
-    // lane (r, h) of tile (mt, nt) holds token 32 (MT wm + mt) + r and features
-    // 32 (NT wn + nt) + 8 q + 4 h + (0..3) in values 4q .. 4q + 3; N is a multiple of 8
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        const int m = 32 * (MT * wm + mt) + (int)r;
-        if (m >= rows)
-            continue;
-        uint16_t* const yrow = y + (row0 + m) * N + n0;
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
+            *reinterpret_cast<f32x4*>(&part[wave][16 * mt + r][16 * nt + 4 * h]) = acc[mt][nt];
+    __syncthreads();
+    for (int i = tid; i < TM * TN / 4; i += 64 * W) {
+        const int m = i / (TN / 4), n = i % (TN / 4) * 4;
+        f32x4 v = *reinterpret_cast<const f32x4*>(&part[0][m][n]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int n = 32 * (NT * wn + nt) + 8 * q + 4 * (int)h;
-                const f32x16& v = acc[mt][nt];
-                const bf16x2 p0 = {(__bf16)v[4 * q + 0], (__bf16)v[4 * q + 1]};
-                const bf16x2 p1 = {(__bf16)v[4 * q + 2], (__bf16)v[4 * q + 3]};
-                if (n < cols)
-                    *reinterpret_cast<u32x2*>(yrow + n) =
-                        u32x2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
-            }
+        for (int q = 1; q < W; ++q)
+            v += *reinterpret_cast<const f32x4*>(&part[q][m][n]);
+        const bf16x2 p0 = {(__bf16)v[0], (__bf16)v[1]};
+        const bf16x2 p1 = {(__bf16)v[2], (__bf16)v[3]};
+        if (m < rows && n < cols)
+            *reinterpret_cast<u32x2*>(y + (row0 + m) * N + n0 + n) =
+                u32x2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
     }
 }
+
+namespace {
+
+// Workgroups of TM x TN tiles that a call can need: every token tile holds a row.
+int64_t tiles(int64_t M_cap, int32_t G, int64_t N, int TM, int TN)
+{
+    const int64_t mt = (M_cap + TM - 1) / TM + G;
+    return (mt < M_cap ? mt : M_cap) * ((N + TN - 1) / TN);
+}
+
+}  // namespace
 
 hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, uint16_t* y,
                              const int32_t* offs, int32_t G, int64_t M_cap, int64_t N, int64_t K, hipStream_t stream)
 {
-    constexpr int TM = 64, TN = 128;
-    uint32_t ntn = (uint32_t)((N + TN - 1) / TN);
-    const int64_t grid = ((M_cap + TM - 1) / TM + G) * ntn;
-    if (grid > 0x7FFFFFFF)
-        return hipErrorInvalidValue;
     int g = G;
     int64_t n = N, k = K;
+    uint32_t nt = 0;                              // feature tiles (tile kernel), token tiles (rows kernel)
     void* args[] = {(void*)&a, (void*)&sa, (void*)&w, (void*)&sw, (void*)&y, (void*)&offs, (void*)&g,
-                    (void*)&n, (void*)&k, (void*)&ntn};
-    return launch_kernel((const void*)block_gemm_kernel<TM, TN, 1, 4>, dim3((unsigned)grid), dim3(256), args, stream);
+                    (void*)&n, (void*)&k, (void*)&nt};
+    auto launch = [&](const void* kernel, int64_t grid, int threads) {
+        return grid > 0x7FFFFFFF ? hipErrorInvalidValue
+                                 : launch_kernel(kernel, dim3((unsigned)grid), dim3((unsigned)threads), args, stream);
+    };
+    auto tile = [&](const void* kernel, int TM, int TN, int threads) {
+        nt = (uint32_t)((N + TN - 1) / TN);
+        return launch(kernel, tiles(M_cap, G, N, TM, TN), threads);
+    };
+    auto rows = [&](const void* kernel, int TN) {
+        nt = (uint32_t)tiles(M_cap, G, 1, 16, 1);
+        return launch(kernel, tiles(M_cap, G, N, 16, TN), 256);
+    };
+    // The choice goes by the rows an expert has on average and by the number of workgroups
+    // (256 CUs).  Measured in us, the chosen one first:
+    //   256 x 256, from 192 rows per expert on: 8 experts, 2048 rows x 4096 x 7168: 116, 128 x
+    //     128: 134; 32768 rows: 965, 1070; but 1 expert, 1024 rows x 4096 x 4096 (64 tiles): 55
+    //     against 25.5
+    //   128 x 128, from 12 rows on: two buffers and 4 waves where CUs share workgroups (32
+    //     experts, 2048 rows: 231, 8 waves and four buffers 242), the latter for fewer tiles (3
+    //     experts, 1501 rows x 1352 x 1744: 16.3, 17.7)
+    //   32 x 128 below (32 experts, 128 rows: 157, 128 x 128 165; 1 expert, 200 rows x 4096 x
+    //     7168: 21.5, 33.4)
+    //   rows kernel, for at most a row per expert on average or a few rows and few tiles: 256
+    //     experts, 64 rows x 4096 x 2048: 97, 32 x 128 149; 1 expert, 16 rows x 2112 x 7168:
+    //     14.6, 18.8 (64 rows: 19.4, 8.7); 64 features a workgroup, or 32 to have enough of
+    //     them (1 row x 7168 x 2048: 6.4, 8.7)
+    if (M_cap >= 192 * (int64_t)G && tiles(M_cap, G, N, 256, 256) >= 192)
+        return tile((const void*)block_gemm_tile_kernel<2, 4, 8, 4, 2>, 256, 256, 512);
+    if (M_cap >= 12 * (int64_t)G && tiles(M_cap, G, N, 128, 128) >= 128) {
+        if (tiles(M_cap, G, N, 128, 128) >= 512)
+            return tile((const void*)block_gemm_tile_kernel<2, 2, 4, 4, 2>, 128, 128, 256);
+        return tile((const void*)block_gemm_tile_kernel<2, 4, 4, 2, 4>, 128, 128, 512);
+    }
+    if (M_cap <= G || (M_cap <= 16 * (int64_t)G && tiles(M_cap, G, N, 32, 128) < 128)) {
+        if (tiles(M_cap, G, N, 16, 64) >= 512)
+            return rows((const void*)block_gemm_rows_kernel<1, 4, 4>, 64);
+        return rows((const void*)block_gemm_rows_kernel<1, 2, 4>, 32);
+    }
+    return tile((const void*)block_gemm_tile_kernel<1, 4, 2, 2, 4>, 32, 128, 256);
 }
 
 }  // namespace mxfp4

@@ -63,6 +63,19 @@ def test_product(counts, N, K):
     check(counts, N, K)
 
 
+@pytest.mark.parametrize("counts,N,K", [
+    ([2500, 0, 700], 4104, 400),                  # large tiles, ragged in all three directions
+    ([1100], 12288, 144),
+    ([70, 0, 64, 33, 129, 1, 90, 128], 7176, 272),     # medium tiles, many of them
+    ([301, 300, 280], 1544, 528),                 # medium tiles, few of them
+    ([1, 0, 2, 1, 0, 1, 3, 0] * 10, 1032, 656),   # about a row per expert
+    ([1] * 300, 520, 240),                        # more experts than a wave has lanes
+    ([0] * 130 + [9] + [0] * 70 + [40], 264, 144),
+])
+def test_every_kernel(counts, N, K):
+    check(counts, N, K, seed=N)
+
+
 @pytest.mark.parametrize("M", [1, 2, 8, 15, 31, 32, 33, 47, 48, 96, 192, 255, 256, 320])
 def test_row_counts(M):
     check([M], 384, 512, slack=0, seed=M)
