@@ -36,12 +36,18 @@ __device__ __forceinline__ float exp_f32(float x)
     return __builtin_isfinite(r) ? r : e;         // exp(+-inf), exp(NaN) as they are
 }
 
-__device__ __forceinline__ float sigmoid_f32(float x) { return 1.0f / (1.0f + exp_f32(-x)); }
+// The router's exp, without that correction: its relative error is |x| 2^-24 and the
+// instruction's, 4e-7 at |x| = 8, under what may decide a choice among FP32 scores anyway,
+// for a third of the score's instructions less.
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269502162933349609375f); }
+// (the hardware reciprocal: one unit in the last place; below 2^-126 it gives 0)
+__device__ __forceinline__ float sigmoid_fast(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x)); }
+__device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x)); }
 
-// FP32 -> order key: larger key, larger value; NaN gives 1 (below -inf), never 0.
+// FP32 -> order key: larger key, larger value; NaN gives 1 (below -inf), never 0.  (No sum
+// of a score, which is +0 or more, and a bias is -0.)
 __device__ __forceinline__ uint32_t order_key(float c)
 {
-    c += 0.0f;                                    // -0 and +0 are equal
     const uint32_t b = __float_as_uint(c);
     const uint32_t k = (int32_t)b < 0 ? ~b : b | 0x80000000u;
     return c == c ? k : 1u;
@@ -51,30 +57,89 @@ __device__ __forceinline__ float key_value(uint32_t k)
     return k <= 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float((int32_t)k < 0 ? k & 0x7FFFFFFFu : ~k);
 }
 
-__device__ __forceinline__ float wave_sum(float v)
+// ---- reductions over a wave, by DPP ----
+// (two quad permutations, the mirrors of 8 and 16 lanes, then lane 15 of a row to the next
+// and lane 31 to the upper half: lane 63 has everything.)
+constexpr int kRowMirror = 0x140, kRowHalfMirror = 0x141, kRowBcast15 = 0x142, kRowBcast31 = 0x143;
+
+// Lanes that a broadcast does not reach take 0, the identity of both reductions below (keys
+// and sums), so that the compiler folds the move into the operation.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v)
 {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-        v += __shfl_xor(v, d, 64);
-    return v;
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
-__device__ __forceinline__ float wave_max(float v)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_rows(uint32_t v)
 {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-        v = fmaxf(v, __shfl_xor(v, d, 64));
-    return v;
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
 }
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v)
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-        v = max(v, (uint32_t)__shfl_xor((int)v, d, 64));
-    return uniform(v);
+    v = max(v, dpp<kQuadSwap1>(v));
+    v = max(v, dpp<kQuadSwap2>(v));
+    v = max(v, dpp<kRowHalfMirror>(v));
+    v = max(v, dpp<kRowMirror>(v));
+    v = max(v, dpp_rows<kRowBcast15, 0xA>(v));
+    v = max(v, dpp_rows<kRowBcast31, 0xC>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ float wave_sum(float f)
+{
+    auto add = [&](uint32_t o) { f += __uint_as_float(o); };
+    add(dpp<kQuadSwap1>(__float_as_uint(f)));
+    add(dpp<kQuadSwap2>(__float_as_uint(f)));
+    add(dpp<kRowHalfMirror>(__float_as_uint(f)));
+    add(dpp<kRowMirror>(__float_as_uint(f)));
+    add(dpp_rows<kRowBcast15, 0xA>(__float_as_uint(f)));
+    add(dpp_rows<kRowBcast31, 0xC>(__float_as_uint(f)));
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), 63));
+}
+// What lane ^ D holds, for a value that is the same in every aligned run of D lanes.
+template <int D>
+__device__ __forceinline__ uint32_t across(uint32_t v)
+{
+    if constexpr (D == 1)
+        return dpp<kQuadSwap1>(v);
+    else if constexpr (D == 2)
+        return dpp<kQuadSwap2>(v);
+    else if constexpr (D == 4)
+        return dpp<kRowHalfMirror>(v);
+    else if constexpr (D == 8)
+        return dpp<kRowMirror>(v);
+    else
+        return (uint32_t)__shfl_xor((int)v, D, 64);
+}
+// The two largest keys of the 1 << l_log lanes of a group, from each lane's two largest.
+template <int D = 1>
+__device__ __forceinline__ void group_top2(uint32_t& k1, uint32_t& k2, int l_log)
+{
+    if constexpr (D < 64) {
+        if (D >> l_log)
+            return;                               // (uniform)
+        const uint32_t o1 = across<D>(k1), o2 = across<D>(k2);
+        k2 = max(max(k2, o2), min(k1, o1));
+        k1 = max(k1, o1);
+        group_top2<2 * D>(k1, k2, l_log);
+    }
+}
+
+// value[lane] = mask has the lane ? 0 : value, the mask on the scalar unit.
+__device__ __forceinline__ void clear_lanes(uint32_t& v, uint64_t mask)
+{
+    asm("v_cndmask_b32 %0, %0, 0, %1" : "+v"(v) : "s"(mask));
 }
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ f32x4 load_logit4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ f32x4 load_logit4(const uint16_t* p)
+{
+    const u32x2 u = *reinterpret_cast<const u32x2*>(p);
+    return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                 __uint_as_float(u.y & 0xFFFF0000u)};
+}
 
 // What a softmax row is normalised by: p_e = exp(l_e - m) * inv.  A row of -inf only has
 // p = 0 everywhere; a row with NaN or +inf has NaN everywhere.
@@ -82,253 +147,615 @@ struct RowNorm {
     float m, inv;
 };
 __device__ __forceinline__ float softmax_of(float l, RowNorm n) { return exp_f32(l - n.m) * n.inv; }
-__device__ __forceinline__ RowNorm row_norm(float m, float sum)
+// The maximum from its key (0 for a row of -inf or NaN only), the factor from the sum (NaN if
+// a logit is NaN, which the maximum leaves out).
+__device__ __forceinline__ float norm_top(uint32_t key)
 {
+    const float m = key_value(key);
+    return m == -__builtin_inff() || !(m == m) ? 0.0f : m;
+}
+__device__ __forceinline__ float norm_inv(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+// The norm of a row spread over a wave, and its scores in place of the logits.
+template <int V, bool FAST = false>
+__device__ __forceinline__ RowNorm softmax_row(float (&l)[V])
+{
+    float top = l[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+        top = fmaxf(top, l[i]);
     RowNorm n;
-    n.m = m == -__builtin_inff() ? 0.0f : m;
-    n.inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    n.m = norm_top(wave_max(order_key(top)));
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        sum += l[i] = FAST ? exp_fast(l[i] - n.m) : exp_f32(l[i] - n.m);
+    n.inv = norm_inv(wave_sum(sum));
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        l[i] *= n.inv;
     return n;
 }
 
 }  // namespace
 
-// One wave per token.  Each group has L lanes (64 / n_group rounded down to a power of
-// two) and each of them VPL consecutive experts of it, so lane order is expert order
-// and what a group needs is exchanged inside its lanes.
-template <int VPL, typename T>
+// One wave per token, several in turn.  Each group has L = 1 << l_log lanes (64 / n_group
+// rounded down to a power of two) and each of them VPL consecutive experts of it, so lane
+// order is expert order and what a group needs is exchanged inside its lanes.  A selection
+// is one wave maximum (six DPP steps); the lane and slot that hold it are found on the
+// scalar unit from one ballot per slot.  VEC: VPL is a multiple of 4, groups are too and
+// rows aligned, so a lane's logits are 16-byte (BF16: 8-byte) loads.
+template <int VPL, bool VEC, typename T>
 __global__ __launch_bounds__(kThreads) void route_kernel(
     const T* __restrict__ logits, const float* __restrict__ bias, const uint8_t* __restrict__ row_mask,
-    int32_t* __restrict__ ids, float* __restrict__ weights, int64_t n_tokens, int E, int n_group, int topk_group,
-    int group_best, int k, int sigmoid, int renorm, float scale, int L)
+    int32_t* __restrict__ ids, float* __restrict__ weights, int64_t n_tokens, int E, int n_group, int gs,
+    int topk_group, int group_best, int k, int sigmoid, int renorm, float scale, int l_log)
 {
-    __shared__ float s_lds[kThreads / 64][64 * VPL];
+    __shared__ __attribute__((aligned(16))) float s_lds[kThreads / 64][64 * VPL];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + wave;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / 64);
+    int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + wave;
     if (t >= n_tokens)
         return;
-    const int gs = E / n_group;
-    const int g = lane / L, r = lane & (L - 1);
+    const int g = lane >> l_log, r = lane & ((1 << l_log) - 1);
     const int e0 = g * gs + r * VPL;              // the lane's first expert
-    const int nv = g < n_group ? min(VPL, gs - r * VPL) : 0;
-    const T* const row = logits + t * E;
+    const int nv = g < n_group ? gs - r * VPL : 0;       // the experts it has, at most VPL of them
 
-    float s[VPL];
+    // (slots without an expert read another one's)
+    auto load_row = [&](float (&v)[VPL], const auto* row) {
+        if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-        s[i] = i < nv ? load_logit(row + e0 + i) : -__builtin_inff();
-    if (sigmoid) {
+            for (int i = 0; i < VPL; i += 4) {
+                const f32x4 q = load_logit4(row + (i < nv ? e0 + i : 0));
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[i + j] = q[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                v[i] = load_logit(row + (i < nv ? e0 + i : 0));
+        }
+    };
+    float b[VPL] = {}, next[VPL];
+    if (bias)
+        load_row(b, bias);
+    load_row(next, logits + t * E);
+    for (; t < n_tokens; t += step) {
+        float s[VPL];
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            s[i] = sigmoid_f32(s[i]);
-    } else {
-        float m = -__builtin_inff();
+            s[i] = next[i];
+        if (t + step < n_tokens)
+            load_row(next, logits + (t + step) * E);
+        if (sigmoid) {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            m = fmaxf(m, s[i]);
-        m = wave_max(m);
-        const float m0 = m == -__builtin_inff() ? 0.0f : m;
-        float sum = 0.0f;
+            for (int i = 0; i < VPL; ++i)
+                s[i] = sigmoid_fast(s[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                s[i] = i < nv ? s[i] : -__builtin_inff();
+            softmax_row<VPL, true>(s);
+        }
+        uint32_t key[VPL];
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            s[i] = exp_f32(s[i] - m0);
-            sum += s[i];
+            key[i] = order_key(s[i] + b[i]) & (i < nv ? ~0u : 0u);
+            s_lds[wave][lane * VPL + i] = s[i];
         }
-        const RowNorm n = row_norm(m, wave_sum(sum));
+        if (topk_group < n_group) {
+            uint32_t k1 = 0, k2 = 0;              // the two largest keys of the lane, then of the group
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            s[i] *= n.inv;
-    }
-    uint32_t key[VPL];
+            for (int i = 0; i < VPL; ++i) {
+                k2 = max(k2, min(k1, key[i]));
+                k1 = max(k1, key[i]);
+            }
+            group_top2(k1, k2, l_log);
+            const float v = group_best == 2 ? key_value(k1) + key_value(k2) : key_value(k1);
+            const uint32_t gk = order_key(v);     // (at most that of +inf: gk + 1 is larger)
+            int rank = 0;
+            for (int h = 0; h < n_group; ++h) {
+                const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)gk, h << l_log);
+                rank += o + (h < g) > gk;         // a group before this one wins ties
+            }
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        key[i] = i < nv ? order_key(s[i] + (bias ? bias[e0 + i] : 0.0f)) : 0u;
-        s_lds[wave][lane * VPL + i] = s[i];
-    }
-    if (topk_group < n_group) {
-        uint32_t k1 = 0, k2 = 0;                  // the two largest keys of the group
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            k2 = max(k2, min(k1, key[i]));
-            k1 = max(k1, key[i]);
+            for (int i = 0; i < VPL; ++i)
+                key[i] = rank < topk_group ? key[i] : 0u;
         }
-        for (int d = 1; d < L; d <<= 1) {
-            const uint32_t o1 = (uint32_t)__shfl_xor((int)k1, d, 64), o2 = (uint32_t)__shfl_xor((int)k2, d, 64);
-            k2 = max(max(k2, o2), min(k1, o1));
-            k1 = max(k1, o1);
+        int mine = 0;                             // lane j: place of selection j in s_lds
+        for (int j = 0; j < k; ++j) {
+            uint32_t lm = key[0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i)
+                lm = max(lm, key[i]);
+            const uint32_t best = wave_max(lm);
+            // the first lane that holds it, and its first slot that does, on the scalar unit
+            uint64_t has[VPL], any = 0;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                has[i] = __ballot(key[i] == best);
+                any |= has[i];
+            }
+            const uint64_t first = any & (0 - any);
+            uint32_t slots = 0;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                slots |= (has[i] & first) != 0 ? 1u << i : 0u;
+            const uint32_t slot = slots & (0 - slots);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                clear_lanes(key[i], slot == 1u << i ? first : 0);
+            const int at = (int)__builtin_ctzll(any) * VPL + __builtin_ctz(slots);
+            mine = lane == j ? at : mine;
         }
-        const float v = group_best == 2 ? key_value(k1) + key_value(k2) : key_value(k1);
-        const uint32_t gk = order_key(v);
-        int rank = 0;
-        for (int h = 0; h < n_group; ++h) {
-            const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)gk, h * L);
-            rank += o > gk || (o == gk && h < g);
+        const float sj = lane < k ? s_lds[wave][mine] : 0.0f;
+        float w = scale * sj;
+        if (renorm)
+            w = scale * (sj / (wave_sum(sj) + 1e-20f));
+        const int from = mine / VPL;
+        int e = (from >> l_log) * gs + (from & ((1 << l_log) - 1)) * VPL + mine % VPL;
+        if (row_mask && !row_mask[t]) {
+            e = -1;
+            w = 0.0f;
         }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            key[i] = rank < topk_group ? key[i] : 0u;
-    }
-    int mine = 0;                                 // lane j: place of selection j in s_lds
-    for (int j = 0; j < k; ++j) {
-        uint32_t lm = key[0];
-#pragma unroll
-        for (int i = 1; i < VPL; ++i)
-            lm = max(lm, key[i]);
-        const uint32_t best = wave_max_u32(lm);
-        const int src = __builtin_ctzll(__ballot(lm == best));
-        int slot = 0;
-#pragma unroll
-        for (int i = VPL - 1; i >= 0; --i)
-            slot = key[i] == best ? i : slot;
-        slot = __builtin_amdgcn_readlane(slot, src);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            key[i] = lane == src && i == slot ? 0u : key[i];
-        mine = lane == j ? src * VPL + slot : mine;
-    }
-    const float sj = lane < k ? s_lds[wave][mine] : 0.0f;
-    float w = scale * sj;
-    if (renorm)
-        w = scale * (sj / (wave_sum(sj) + 1e-20f));
-    const int from = mine / VPL;
-    int e = (from / L) * gs + (from & (L - 1)) * VPL + mine % VPL;
-    if (row_mask && !row_mask[t]) {
-        e = -1;
-        w = 0.0f;
-    }
-    if (lane < k) {
-        ids[t * k + lane] = e;
-        weights[t * k + lane] = w;
+        if (lane < k) {
+            ids[t * k + lane] = e;
+            weights[t * k + lane] = w;
+        }
     }
 }
 
-// One wave per token; lane j < k holds selection j.  The selected experts' ds are placed in
-// a row of LDS (zero elsewhere), from which every lane takes its experts'.
-template <typename T>
+// ---- four tokens per wave -------------------------------------------------------------
+// Up to 256 experts and 8 choices: 16 lanes (a DPP row) per token, VPL consecutive experts
+// per lane.  A candidate is one number, the bits of a double in [2, 4) with the order key in
+// the top 32 bits of its mantissa and the expert below (the complements of its lane and of
+// its slot there, so that the lower expert is the larger number): no two are equal, the larger one is
+// the better choice, and v_max_f64 / v_min_f64 sort them without carrying an index along.
+// Each lane sorts its candidates (the best 8 of them), then k times the row's best head is
+// taken (four DPP steps) and its lane moves on in its list, which lies in LDS.
+
+__device__ __forceinline__ double f64_max(double a, double b)
+{
+    double d;                                     // (fmax would first quiet its operands)
+    asm("v_max_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+    return d;
+}
+__device__ __forceinline__ double f64_min(double a, double b)
+{
+    double d;
+    asm("v_min_f64 %0, %1, %2" : "=v"(d) : "v"(a), "v"(b));
+    return d;
+}
+__device__ __forceinline__ double candidate(uint32_t key, uint32_t low)
+{
+    const uint32_t hi = __builtin_amdgcn_alignbit(0x40000u, key, 12), lo = key << 20 | low;
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double with_low(double c, uint32_t low)
+{
+    return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, c) | low);
+}
+__device__ __forceinline__ void order2(double& a, double& b)
+{
+    const double hi = f64_max(a, b);
+    b = f64_min(a, b);
+    a = hi;
+}
+__device__ __forceinline__ void sort4(double* v)
+{
+    order2(v[0], v[1]), order2(v[2], v[3]);
+    order2(v[0], v[2]), order2(v[1], v[3]);
+    order2(v[1], v[2]);
+}
+__device__ __forceinline__ void sort8(double* v)          // Batcher's odd-even merge of two sorted halves
+{
+    sort4(v), sort4(v + 4);
+    order2(v[0], v[4]), order2(v[1], v[5]), order2(v[2], v[6]), order2(v[3], v[7]);
+    order2(v[2], v[4]), order2(v[3], v[5]);
+    order2(v[1], v[2]), order2(v[3], v[4]), order2(v[5], v[6]);
+}
+// The best min(V, 8) of V candidates, in order, in the first places.
+template <int V>
+__device__ __forceinline__ void sort_best(double (&v)[V])
+{
+    if constexpr (V == 4) {
+        sort4(v);
+    } else if constexpr (V == 8) {
+        sort8(v);
+    } else {
+        sort8(v), sort8(v + 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = f64_max(v[i], v[15 - i]);      // the best 8, a bitonic sequence
+        order2(v[0], v[4]), order2(v[1], v[5]), order2(v[2], v[6]), order2(v[3], v[7]);
+        order2(v[0], v[2]), order2(v[1], v[3]), order2(v[4], v[6]), order2(v[5], v[7]);
+        order2(v[0], v[1]), order2(v[2], v[3]), order2(v[4], v[5]), order2(v[6], v[7]);
+    }
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 | dpp<CTRL>((uint32_t)u));
+}
+__device__ __forceinline__ double row_best(double v)
+{
+    v = f64_max(v, dpp<kQuadSwap1>(v));
+    v = f64_max(v, dpp<kQuadSwap2>(v));
+    v = f64_max(v, dpp<kRowHalfMirror>(v));
+    return f64_max(v, dpp<kRowMirror>(v));
+}
+__device__ __forceinline__ float row_sum(float f)
+{
+    f += __uint_as_float(dpp<kQuadSwap1>(__float_as_uint(f)));
+    f += __uint_as_float(dpp<kQuadSwap2>(__float_as_uint(f)));
+    f += __uint_as_float(dpp<kRowHalfMirror>(__float_as_uint(f)));
+    return f + __uint_as_float(dpp<kRowMirror>(__float_as_uint(f)));
+}
+__device__ __forceinline__ uint32_t row_max(uint32_t v)
+{
+    v = max(v, dpp<kQuadSwap1>(v));
+    v = max(v, dpp<kQuadSwap2>(v));
+    v = max(v, dpp<kRowHalfMirror>(v));
+    return max(v, dpp<kRowMirror>(v));
+}
+// How many of the row's other groups come before this lane's: the groups have L lanes each
+// and fill the row, so rotations by L lanes show each of them.
+template <int L, int N = L>
+__device__ __forceinline__ int group_rank(uint32_t gk, uint32_t g)
+{
+    if constexpr (N < 16) {
+        constexpr int kRor = 0x120 + N;
+        const uint32_t before = dpp<kRor>(g) < g;          // it wins ties
+        return (dpp<kRor>(gk) + before > gk) + group_rank<L, N + L>(gk, g);
+    }
+    return 0;
+}
+
+template <int VPL, bool VEC, typename T>
+__global__ __launch_bounds__(kThreads) void route_quad_kernel(
+    const T* __restrict__ logits, const float* __restrict__ bias, const uint8_t* __restrict__ row_mask,
+    int32_t* __restrict__ ids, float* __restrict__ weights, int64_t n_tokens, int E, int n_group, int gs,
+    int topk_group, int group_best, int k, int sigmoid, int renorm, float scale, int l_log)
+{
+    constexpr int kList = VPL < 8 ? VPL : 8;
+    __shared__ __attribute__((aligned(16))) float s_lds[kThreads / 64][64 * VPL];
+    __shared__ double list[kThreads / 64][kList + 1][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15;                      // lane of the row
+    const int64_t step = (int64_t)gridDim.x * kThreads / 16;
+    int64_t t0 = ((int64_t)blockIdx.x * (kThreads / 64) + wave) * 4;
+    if (t0 >= n_tokens)
+        return;
+    const int e0 = r * VPL;                       // the lane's first expert
+    const int nv = E - e0;                        // the experts it has, at most VPL of them
+    const uint32_t g = (uint32_t)r >> l_log;
+    const uint32_t low = (uint32_t)(15 - r) * VPL;        // (VPL is a power of two)
+
+    // (slots without an expert read another one's, rows without a token the last one's)
+    auto load_row = [&](float (&v)[VPL], const auto* row) {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < VPL; i += 4) {
+                const f32x4 q = load_logit4(row + (i < nv ? e0 + i : 0));
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[i + j] = q[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                v[i] = load_logit(row + (i < nv ? e0 + i : 0));
+        }
+    };
+    auto row_at = [&](int64_t t) { return logits + min(t + (lane >> 4), n_tokens - 1) * E; };
+    float b[VPL] = {}, next[VPL];
+    if (bias)
+        load_row(b, bias);
+    load_row(next, row_at(t0));
+    list[wave][kList][lane] = 0.0;                // below every candidate
+    for (; t0 < n_tokens; t0 += step) {
+        float s[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            s[i] = next[i];
+        if (t0 + step < n_tokens)
+            load_row(next, row_at(t0 + step));
+        if (sigmoid) {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                s[i] = sigmoid_fast(s[i]);
+        } else {
+            float top = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                s[i] = i < nv ? s[i] : -__builtin_inff();
+                top = fmaxf(top, s[i]);
+            }
+            const float m = norm_top(row_max(order_key(top)));
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                sum += s[i] = exp_fast(s[i] - m);
+            const float inv = norm_inv(row_sum(sum));
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                s[i] *= inv;
+        }
+        uint32_t key[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            key[i] = order_key(s[i] + b[i]) & (i < nv ? ~0u : 0u);
+            s_lds[wave][i * 64 + lane] = s[i];
+        }
+        if (topk_group < n_group) {
+            uint32_t k1 = 0, k2 = 0;              // the two largest keys of the lane, then of the group
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                k2 = max(k2, min(k1, key[i]));
+                k1 = max(k1, key[i]);
+            }
+            group_top2(k1, k2, l_log);
+            const float v = group_best == 2 ? key_value(k1) + key_value(k2) : key_value(k1);
+            const uint32_t gk = order_key(v);     // (at most that of +inf: gk + 1 is larger)
+            const int rank = l_log == 0   ? group_rank<1>(gk, g)
+                             : l_log == 1 ? group_rank<2>(gk, g)
+                             : l_log == 2 ? group_rank<4>(gk, g)
+                                          : group_rank<8>(gk, g);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                key[i] = rank < topk_group ? key[i] : 0u;
+        }
+        double c[VPL];
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            c[i] = candidate(key[i], (uint32_t)(VPL - 1 - i));
+        sort_best(c);
+#pragma unroll
+        for (int i = 0; i < kList; ++i)
+            c[i] = with_low(c[i], low);
+#pragma unroll
+        for (int i = 1; i < kList; ++i)
+            list[wave][i][lane] = c[i];
+        double head = c[0];
+        const double* rest = &list[wave][1][lane];
+        uint32_t mine = 0;                        // lane j of the row: the low bits of choice j
+        for (int j = 0; j < k; ++j) {
+            const double best = row_best(head);
+            if (__builtin_bit_cast(uint64_t, head) == __builtin_bit_cast(uint64_t, best)) {
+                head = *rest;
+                rest += 64;
+            }
+            mine = r == j ? (uint32_t)__builtin_bit_cast(uint64_t, best) : mine;
+        }
+        const int64_t t = t0 + (lane >> 4);
+        int e = 16 * VPL - 1 - (int)(mine & (16 * VPL - 1));
+        const float sj = r < k ? s_lds[wave][e % VPL * 64 + (lane & 48) + e / VPL] : 0.0f;
+        float w = scale * sj;
+        if (renorm)
+            w = scale * (sj / (row_sum(sj) + 1e-20f));
+        if (t < n_tokens && r < k) {
+            if (row_mask && !row_mask[t]) {
+                e = -1;
+                w = 0.0f;
+            }
+            ids[t * k + r] = e;
+            weights[t * k + r] = w;
+        }
+    }
+}
+
+// ---- backward ---------------------------------------------------------------------------
+
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) { return LANES == 16 ? row_sum(v) : wave_sum(v); }
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) { return LANES == 16 ? row_max(v) : wave_max(v); }
+
+__device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ void store_logit4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ void store_logit4(uint16_t* p, f32x4 v)
+{
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    const bf16x4 b = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+    *reinterpret_cast<u32x2*>(p) = __builtin_bit_cast(u32x2, b);
+}
+
+// LANES lanes per token, 4 Q experts per lane in runs of four (LANES x 4 consecutive experts
+// per load); lane j < k holds selection j.  The selected experts' ds are placed in a row of
+// LDS that is zero elsewhere, from which every lane takes its experts'.  Reading and writing
+// the logits is what bounds it (16384 tokens x 256 experts, FP32: 34.6 MB).
+template <int LANES, int Q, bool VEC, typename T>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const T* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ dweights,
     T* __restrict__ dlogits, int64_t n_tokens, int E, int k, int sigmoid, int renorm, float scale)
 {
-    constexpr int kV = 16;                        // E <= 1024
-    __shared__ float ds_lds[kThreads / 64][64 * kV];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + wave;
-    if (t >= n_tokens)
-        return;
-    const T* const row = logits + t * E;
-    float p[kV];
+    __shared__ __attribute__((aligned(16))) float ds_lds[kThreads / LANES][LANES * 4 * Q];
+    const int r = threadIdx.x % LANES;
+    float* const ds_row = ds_lds[threadIdx.x / LANES];
+    const int64_t t = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+    const bool live = t < n_tokens;               // (a row of lanes without a token does the last one's, unstored)
+    const int64_t tr = live ? t : n_tokens - 1;
+    const T* const row = logits + tr * E;
+    int id = r < k ? ids[tr * k + r] : -1;
+    id = (uint32_t)id < (uint32_t)E ? id : -1;
+    const float dw = id >= 0 ? dweights[tr * k + r] : 0.0f;
+    const float lj = load_logit(row + max(id, 0));
+    float p[Q][4];
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int e = i * 64 + lane;
-        p[i] = e < E ? load_logit(row + e) : -__builtin_inff();
-        if (e < E)
-            ds_lds[wave][e] = 0.0f;
+    for (int q = 0; q < Q; ++q) {
+        const int e = (q * LANES + r) * 4;
+        if (VEC) {
+            const f32x4 v = load_logit4(row + (e < E ? e : 0));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                p[q][j] = e < E ? v[j] : -__builtin_inff();
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float v = load_logit(row + min(e + j, E - 1));
+                p[q][j] = e + j < E ? v : -__builtin_inff();
+            }
+        }
+        *reinterpret_cast<f32x4*>(ds_row + e) = f32x4{};
     }
     RowNorm n{0.0f, 1.0f};
-    if (!sigmoid) {
-        float m = -__builtin_inff();
+    if (sigmoid) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i)
-            m = fmaxf(m, p[i]);
-        m = wave_max(m);
-        const float m0 = m == -__builtin_inff() ? 0.0f : m;
-        float sum = 0.0f;
+        for (int q = 0; q < Q; ++q)
 #pragma unroll
-        for (int i = 0; i < kV; ++i)
-            sum += exp_f32(p[i] - m0);
-        n = row_norm(m, wave_sum(sum));
+            for (int j = 0; j < 4; ++j)
+                p[q][j] = sigmoid_f32(p[q][j]);
+    } else {
+        float top = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                top = fmaxf(top, p[q][j]);
+        n.m = norm_top(lanes_max<LANES>(order_key(top)));
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sum += p[q][j] = exp_f32(p[q][j] - n.m);
+        n.inv = norm_inv(lanes_sum<LANES>(sum));
     }
-    int id = -1;
-    float dw = 0.0f, sj = 0.0f;
-    if (lane < k) {
-        id = ids[t * k + lane];
-        if ((uint32_t)id < (uint32_t)E) {
-            dw = dweights[t * k + lane];
-            const float l = load_logit(row + id);
-            sj = sigmoid ? sigmoid_f32(l) : softmax_of(l, n);
-        } else {
-            id = -1;
-        }
-    }
+    const float sj = id < 0 ? 0.0f : sigmoid ? sigmoid_f32(lj) : softmax_of(lj, n);
     float ds = scale * dw;
     if (renorm) {
-        const float D = wave_sum(sj) + 1e-20f;
-        ds = scale * ((dw - wave_sum(dw * sj) / D) / D);
+        const float D = lanes_sum<LANES>(sj) + 1e-20f;
+        ds = scale * ((dw - lanes_sum<LANES>(dw * sj) / D) / D);
     }
     if (id >= 0)
-        ds_lds[wave][id] = ds;
+        ds_row[id] = ds;
     else
         ds = 0.0f;
-    const float dot = sigmoid ? 0.0f : wave_sum(ds * sj);
-    __builtin_amdgcn_wave_barrier();
+    const float dot = sigmoid ? 0.0f : lanes_sum<LANES>(ds * sj);
+    __builtin_amdgcn_wave_barrier();              // (one wave writes and reads the row)
+    T* const out = dlogits + tr * E;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int e = i * 64 + lane;
-        if (e < E) {
-            const float d = ds_lds[wave][e];
-            const float q = sigmoid ? sigmoid_f32(p[i]) : softmax_of(p[i], n);
-            const float out = sigmoid ? d * (q * (1.0f - q)) : q * (d - dot);
-            if constexpr (sizeof(T) == 4)
-                dlogits[t * E + e] = out;
-            else
-                dlogits[t * E + e] = __builtin_bit_cast(uint16_t, (__bf16)out);
+    for (int q = 0; q < Q; ++q) {
+        const int e = (q * LANES + r) * 4;
+        const f32x4 d = *reinterpret_cast<const f32x4*>(ds_row + e);
+        f32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float s = p[q][j] * n.inv;
+            v[j] = sigmoid ? d[j] * (s * (1.0f - s)) : s * (d[j] - dot);
+        }
+        if (VEC) {
+            if (live && e < E)
+                store_logit4(out + e, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (live && e + j < E)
+                    store_logit(out + e + j, v[j]);
         }
     }
 }
 
 template <typename T>
-static const void* route_kernel_for(int vpl)
+static const void* route_kernel_for(int vpl, bool vec)
 {
     switch (vpl) {
-    case 1: return (const void*)route_kernel<1, T>;
-    case 2: return (const void*)route_kernel<2, T>;
-    case 4: return (const void*)route_kernel<4, T>;
-    case 8: return (const void*)route_kernel<8, T>;
-    case 16: return (const void*)route_kernel<16, T>;
-    default: return (const void*)route_kernel<kMaxRouteV, T>;
+    case 1: return (const void*)route_kernel<1, false, T>;
+    case 2: return (const void*)route_kernel<2, false, T>;
+    case 4: return vec ? (const void*)route_kernel<4, true, T> : (const void*)route_kernel<4, false, T>;
+    case 8: return vec ? (const void*)route_kernel<8, true, T> : (const void*)route_kernel<8, false, T>;
+    case 16: return vec ? (const void*)route_kernel<16, true, T> : (const void*)route_kernel<16, false, T>;
+    default: return (const void*)route_kernel<kMaxRouteV, false, T>;
     }
 }
+template <typename T>
+static const void* route_quad_kernel_for(int vpl, bool vec)
+{
+    switch (vpl) {
+    case 4: return vec ? (const void*)route_quad_kernel<4, true, T> : (const void*)route_quad_kernel<4, false, T>;
+    case 8: return vec ? (const void*)route_quad_kernel<8, true, T> : (const void*)route_quad_kernel<8, false, T>;
+    default: return vec ? (const void*)route_quad_kernel<16, true, T> : (const void*)route_quad_kernel<16, false, T>;
+    }
+}
+
+template <bool VEC, typename T>
+static const void* route_backward_for(int lanes, int q)
+{
+    if (lanes == 16)
+        return q == 1   ? (const void*)route_backward_kernel<16, 1, VEC, T>
+               : q == 2 ? (const void*)route_backward_kernel<16, 2, VEC, T>
+                        : (const void*)route_backward_kernel<16, 4, VEC, T>;
+    return q == 1   ? (const void*)route_backward_kernel<64, 1, VEC, T>
+           : q == 2 ? (const void*)route_backward_kernel<64, 2, VEC, T>
+                    : (const void*)route_backward_kernel<64, 4, VEC, T>;
+}
+
+// Workgroups of the router at most: the 8 a CU holds at a time; they take tokens in turn.
+constexpr int64_t kRouteGroups = 2048;
 
 hipError_t launch_route(const void* logits, bool f32, const float* bias, const uint8_t* row_mask, int32_t* ids,
                         float* weights, int64_t T, int32_t E, int32_t n_group, int32_t topk_group,
                         int32_t group_best, int32_t k, bool sigmoid, bool renorm, float scale, hipStream_t stream)
 {
-    const int64_t grid = (T + kThreads / 64 - 1) / (kThreads / 64);
-    if (grid > 0x7FFFFFFF)
-        return hipErrorInvalidValue;
-    int L = 1;
-    while (2 * L * n_group <= 64)
-        L *= 2;
-    const int need = (E / n_group + L - 1) / L;   // experts per lane
-    int vpl = 1;
-    while (vpl < need)
+    int gs = E / n_group, l_log = 0, vpl = 4;
+    while (16 * vpl < E)
         vpl *= 2;
-    if (vpl > kMaxRouteV)
-        return hipErrorInvalidValue;
+    // four tokens per wave if a row of 16 lanes holds the experts, and whole lanes a group
+    const int per_group = gs / vpl;               // lanes
+    const bool groups_fit = topk_group == n_group || (gs % vpl == 0 && per_group * n_group == 16 &&
+                                                      (per_group & (per_group - 1)) == 0);
+    const bool quad = vpl <= 16 && k <= 8 && groups_fit;
+    const int tokens = kThreads / 64 * (quad ? 4 : 1);     // of a workgroup at a time
+    if (quad) {
+        while (2 << l_log <= per_group)
+            ++l_log;
+    } else {
+        while (2 * n_group << l_log <= 64)
+            ++l_log;
+        const int need = (gs + (1 << l_log) - 1) >> l_log;     // experts per lane
+        vpl = 1;
+        while (vpl < need)
+            vpl *= 2;
+        if (vpl > kMaxRouteV)
+            return hipErrorInvalidValue;
+    }
+    const int64_t need_groups = (T + tokens - 1) / tokens;
+    const int64_t grid = need_groups < kRouteGroups ? need_groups : kRouteGroups;
     int64_t t = T;
     int e = E, ng = n_group, tg = topk_group, gb = group_best, kk = k, sg = sigmoid, rn = renorm;
     float sc = scale;
     void* args[] = {(void*)&logits, (void*)&bias, (void*)&row_mask, (void*)&ids, (void*)&weights, (void*)&t, (void*)&e,
-                    (void*)&ng, (void*)&tg, (void*)&gb, (void*)&kk, (void*)&sg, (void*)&rn, (void*)&sc, (void*)&L};
-    return launch_kernel(f32 ? route_kernel_for<float>(vpl) : route_kernel_for<uint16_t>(vpl), dim3((unsigned)grid),
-                         dim3(kThreads), args, stream);
+                    (void*)&ng, (void*)&gs, (void*)&tg, (void*)&gb, (void*)&kk, (void*)&sg, (void*)&rn, (void*)&sc,
+                    (void*)&l_log};
+    const bool vec = quad ? E % 4 == 0 : gs % 4 == 0;      // rows (and a lane's part of them) are aligned
+    const void* kernel;
+    if (quad)
+        kernel = f32 ? route_quad_kernel_for<float>(vpl, vec) : route_quad_kernel_for<uint16_t>(vpl, vec);
+    else
+        kernel = f32 ? route_kernel_for<float>(vpl, vec) : route_kernel_for<uint16_t>(vpl, vec);
+    return launch_kernel(kernel, dim3((unsigned)grid), dim3(kThreads), args, stream);
 }
 
 hipError_t launch_route_backward(const void* logits, bool f32, const int32_t* ids, const float* dweights,
                                  void* dlogits, int64_t T, int32_t E, int32_t k, bool sigmoid, bool renorm,
                                  float scale, hipStream_t stream)
 {
-    const int64_t grid = (T + kThreads / 64 - 1) / (kThreads / 64);
-    if (grid > 0x7FFFFFFF)
-        return hipErrorInvalidValue;
+    const int lanes = E <= 256 && k <= 16 ? 16 : 64;
+    int q = 1;
+    while (4 * lanes * q < E)
+        q *= 2;
+    const int per = kThreads / lanes;             // tokens of a workgroup
+    const int64_t grid = (T + per - 1) / per;
     int64_t t = T;
     int e = E, kk = k, sg = sigmoid, rn = renorm;
     float sc = scale;
     void* args[] = {(void*)&logits, (void*)&ids, (void*)&dweights, (void*)&dlogits, (void*)&t, (void*)&e,
                     (void*)&kk, (void*)&sg, (void*)&rn, (void*)&sc};
-    return launch_kernel(f32 ? (const void*)route_backward_kernel<float> : (const void*)route_backward_kernel<uint16_t>,
-                         dim3((unsigned)grid), dim3(kThreads), args, stream);
+    const void* kernel = E % 4 == 0 ? (f32 ? route_backward_for<true, float>(lanes, q) : route_backward_for<true, uint16_t>(lanes, q))
+                                    : (f32 ? route_backward_for<false, float>(lanes, q) : route_backward_for<false, uint16_t>(lanes, q));
+    return launch_kernel(kernel, dim3((unsigned)grid), dim3(kThreads), args, stream);
 }
 
 }  // namespace mxfp4
