@@ -16,8 +16,9 @@
 // 8-byte one), a row a multiple of 8 lanes, so a block's amax is exchanged over 8 lanes (FP8)
 // or 2 (MXFP4) by DPP.  Where a row is a multiple of 64 lanes a wave has one token, whose
 // positions are scalar loads; else rows follow each other without a gap (32768 rows of 128
-// elements to 8 places: 21.4 us with a wave per row, 10.8 without).  What bounds it is the writing:
-// 8192 rows of 7168 to 8 places each take 118-125 us for 602 MB.
+// elements to 8 places: 21.4 us with a wave per row, 10.8 without).  What bounds it is the writing,
+// streamed past the caches: 8192 rows of 7168 to 8 places each take 110 us for 602 MB, 125
+// with ordinary stores.
 #include "common.h"
 
 namespace mxfp4 {
@@ -138,7 +139,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(
                 const int64_t row = !in ? -1 : kInPlace ? t : (int64_t)pos[t * k + j];
                 if (row < 0 || row >= M_cap)
                     continue;
-                *reinterpret_cast<u32x2*>(y + (row * K + e0) / 2) = codes;
+                store_stream(reinterpret_cast<u32x2*>(y + (row * K + e0) / 2), codes);
                 if (!(lane & 1))
                     static_cast<uint8_t*>(y_scales)[(row * K + e0) / 32] = (uint8_t)s;
             }
@@ -149,7 +150,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(
                 const int64_t row = !in ? -1 : kInPlace ? t : (int64_t)pos[t * k + j];
                 if (row < 0 || row >= M_cap)
                     continue;
-                *reinterpret_cast<u32x4*>(y + row * K + e0) = q.bytes;
+                store_stream(reinterpret_cast<u32x4*>(y + row * K + e0), q.bytes);
                 if (!(lane & 7))
                     static_cast<float*>(y_scales)[row * kb + e0 / 128] = q.scale;
             }

@@ -14,7 +14,7 @@
 // Selection works on order keys: the FP32 bits of c made monotone as unsigned integers,
 // NaN below every number, and 0 for what is excluded, so that a comparison is one integer
 // maximum and any input gives k distinct valid indices.
-#include "strips.h"
+#include "lanes.h"
 
 namespace mxfp4 {
 
@@ -57,44 +57,6 @@ __device__ __forceinline__ float key_value(uint32_t k)
     return k <= 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float((int32_t)k < 0 ? k & 0x7FFFFFFFu : ~k);
 }
 
-// ---- reductions over a wave, by DPP ----
-// (two quad permutations, the mirrors of 8 and 16 lanes, then lane 15 of a row to the next
-// and lane 31 to the upper half: lane 63 has everything.)
-constexpr int kRowMirror = 0x140, kRowHalfMirror = 0x141, kRowBcast15 = 0x142, kRowBcast31 = 0x143;
-
-// Lanes that a broadcast does not reach take 0, the identity of both reductions below (keys
-// and sums), so that the compiler folds the move into the operation.
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v)
-{
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
-}
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t dpp_rows(uint32_t v)
-{
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ uint32_t wave_max(uint32_t v)
-{
-    v = max(v, dpp<kQuadSwap1>(v));
-    v = max(v, dpp<kQuadSwap2>(v));
-    v = max(v, dpp<kRowHalfMirror>(v));
-    v = max(v, dpp<kRowMirror>(v));
-    v = max(v, dpp_rows<kRowBcast15, 0xA>(v));
-    v = max(v, dpp_rows<kRowBcast31, 0xC>(v));
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-__device__ __forceinline__ float wave_sum(float f)
-{
-    auto add = [&](uint32_t o) { f += __uint_as_float(o); };
-    add(dpp<kQuadSwap1>(__float_as_uint(f)));
-    add(dpp<kQuadSwap2>(__float_as_uint(f)));
-    add(dpp<kRowHalfMirror>(__float_as_uint(f)));
-    add(dpp<kRowMirror>(__float_as_uint(f)));
-    add(dpp_rows<kRowBcast15, 0xA>(__float_as_uint(f)));
-    add(dpp_rows<kRowBcast31, 0xC>(__float_as_uint(f)));
-    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), 63));
-}
 // What lane ^ D holds, for a value that is the same in every aligned run of D lanes.
 template <int D>
 __device__ __forceinline__ uint32_t across(uint32_t v)
@@ -385,20 +347,6 @@ __device__ __forceinline__ double row_best(double v)
     v = f64_max(v, dpp<kQuadSwap2>(v));
     v = f64_max(v, dpp<kRowHalfMirror>(v));
     return f64_max(v, dpp<kRowMirror>(v));
-}
-__device__ __forceinline__ float row_sum(float f)
-{
-    f += __uint_as_float(dpp<kQuadSwap1>(__float_as_uint(f)));
-    f += __uint_as_float(dpp<kQuadSwap2>(__float_as_uint(f)));
-    f += __uint_as_float(dpp<kRowHalfMirror>(__float_as_uint(f)));
-    return f + __uint_as_float(dpp<kRowMirror>(__float_as_uint(f)));
-}
-__device__ __forceinline__ uint32_t row_max(uint32_t v)
-{
-    v = max(v, dpp<kQuadSwap1>(v));
-    v = max(v, dpp<kQuadSwap2>(v));
-    v = max(v, dpp<kRowHalfMirror>(v));
-    return max(v, dpp<kRowMirror>(v));
 }
 // How many of the row's other groups come before this lane's: the groups have L lanes each
 // and fill the row, so rotations by L lanes show each of them.
