@@ -450,12 +450,27 @@ def _score(score) -> int:
     return kinds.get(score, score)
 
 
-def _at(t) -> int | None:
-    """_ptr, with an address that nothing reads for a tensor without elements (torch gives
-    those none, and NULL is an error)."""
-    if t is None or isinstance(t, int):
-        return t
-    return t.data_ptr() or 16
+def _take(what: str, args):
+    """_need's checks in one pass, and the tensors' addresses.  A tensor without elements gets
+    one that nothing reads (torch gives those none, and NULL is an error)."""
+    at, host = [], None
+    for t, nbytes, name, dtypes in args:
+        if t is None or isinstance(t, int):
+            at.append(t)
+            continue
+        have = t.nbytes
+        if have < nbytes:
+            raise ValueError(f"{what}: {name} holds {have} bytes, the launch needs {nbytes}")
+        if _dtype_name(t.dtype) not in dtypes:
+            raise ValueError(f"{what}: {name} has dtype {t.dtype}, expected one of {', '.join(dtypes)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+        if not t.is_cuda:
+            host = host or name
+        at.append(t.data_ptr() or 16)
+    if host:
+        raise ValueError(f"{what}: {host} must be a GPU tensor")
+    return at
 
 
 def _logits_dims(logits, ids, T, E, k, f32):
@@ -477,12 +492,13 @@ def mxfp4_route_topk(logits, ids, weights, bias=None, row_mask=None, n_group=1, 
     the k chosen experts; score "softmax" or "sigmoid" (see the header)."""
     T, E, k, f32 = _logits_dims(logits, ids, T, E, k, logits_f32)
     t, e, n = max(T, 0), max(E, 0), max(T, 0) * max(k, 0)
-    _need("mxfp4_route_topk", [(logits, (4 if f32 else 2) * t * e, "logits", _F32 if f32 else _B16),
-                               (bias, 4 * e, "bias", _F32), (row_mask, t, "row_mask", ("uint8", "bool")),
-                               (ids, 4 * n, "ids", _I32), (weights, 4 * n, "weights", _F32)])
-    _check(load_library().mxfp4_route_topk(_at(logits), f32, _at(bias), _at(row_mask), _at(ids), _at(weights),
-                                           T, E, int(n_group), int(topk_group), int(group_best), k, _score(score),
-                                           bool(renorm), float(scale), _stream(stream)), "mxfp4_route_topk")
+    at = _take("mxfp4_route_topk", [(logits, (4 if f32 else 2) * t * e, "logits", _F32 if f32 else _B16),
+                                    (bias, 4 * e, "bias", _F32), (row_mask, t, "row_mask", ("uint8", "bool")),
+                                    (ids, 4 * n, "ids", _I32), (weights, 4 * n, "weights", _F32)])
+    l, b, mask, i, w = at
+    _check(load_library().mxfp4_route_topk(l, f32, b, mask, i, w, T, E, int(n_group), int(topk_group),
+                                           int(group_best), k, _score(score), bool(renorm), float(scale),
+                                           _stream(stream)), "mxfp4_route_topk")
 
 
 def mxfp4_route_topk_backward(logits, ids, dweights, dlogits, score="softmax", renorm=True, scale=1.0, T=None, E=None,
@@ -492,11 +508,11 @@ def mxfp4_route_topk_backward(logits, ids, dweights, dlogits, score="softmax", r
     T, E, k, f32 = _logits_dims(logits, ids, T, E, k, logits_f32)
     t, e, n = max(T, 0), max(E, 0), max(T, 0) * max(k, 0)
     el, kinds = (4, _F32) if f32 else (2, _B16)
-    _need("mxfp4_route_topk_backward", [(logits, el * t * e, "logits", kinds), (ids, 4 * n, "ids", _I32),
-                                        (dweights, 4 * n, "dweights", _F32), (dlogits, el * t * e, "dlogits", kinds)])
-    _check(load_library().mxfp4_route_topk_backward(_at(logits), f32, _at(ids), _at(dweights), _at(dlogits), T, E,
-                                                    k, _score(score), bool(renorm), float(scale), _stream(stream)),
-           "mxfp4_route_topk_backward")
+    at = _take("mxfp4_route_topk_backward", [(logits, el * t * e, "logits", kinds), (ids, 4 * n, "ids", _I32),
+                                             (dweights, 4 * n, "dweights", _F32),
+                                             (dlogits, el * t * e, "dlogits", kinds)])
+    _check(load_library().mxfp4_route_topk_backward(at[0], f32, *at[1:], T, E, k, _score(score), bool(renorm),
+                                                    float(scale), _stream(stream)), "mxfp4_route_topk_backward")
 
 
 def mxfp4_expert_map_workspace(T: int, k: int, G: int) -> int:
@@ -519,12 +535,12 @@ def mxfp4_expert_map(ids, offs, pos, workspace, src=None, first_expert=0, T=None
         M_cap = int(T) * int(k) if src is None or isinstance(src, int) else src.numel()
     T, k, G, M_cap = int(T), int(k), int(G), int(M_cap)
     n = max(T, 0) * max(k, 0)
-    _need("mxfp4_expert_map",
-          [(ids, 4 * n, "ids", _I32), (offs, 4 * (G + 1), "group_offsets", _I32), (pos, 4 * n, "pos", _I32),
-           (src, 4 * max(M_cap, 0), "src", _I32),
-           (workspace, max(mxfp4_expert_map_workspace(T, k, G), 0), "workspace", ("int32", "uint8", "float32"))])
-    _check(load_library().mxfp4_expert_map(_at(ids), _at(offs), _at(pos), _at(src), _at(workspace), T, k,
-                                           int(first_expert), G, M_cap, _stream(stream)), "mxfp4_expert_map")
+    need = mxfp4_expert_map_workspace(T, k, G)
+    at = _take("mxfp4_expert_map", [(ids, 4 * n, "ids", _I32), (offs, 4 * (G + 1), "group_offsets", _I32),
+                                    (pos, 4 * n, "pos", _I32), (src, 4 * max(M_cap, 0), "src", _I32),
+                                    (workspace, max(need, 0), "workspace", ("int32", "uint8", "float32"))])
+    _check(load_library().mxfp4_expert_map(*at, T, k, int(first_expert), G, M_cap, _stream(stream)),
+           "mxfp4_expert_map")
 
 
 def _token_dims(rows, pos, out, T, k, M_cap, K):
@@ -545,10 +561,9 @@ def mxfp4_dispatch_rows(x, pos, codes, scales, T=None, k=None, M_cap=None, K=Non
     order, each row quantized once and written to its places pos [T, k]."""
     T, k, M_cap, K = _token_dims(x, pos, codes, T, k, M_cap, K)
     t, m, w = max(T, 0), max(M_cap, 0), max(K, 0)
-    _need("mxfp4_dispatch_rows", [(x, 2 * t * w, "x", _B16), (pos, 4 * t * max(k, 0), "pos", _I32),
-                                  (codes, m * w // 2, "codes", _U8), (scales, m * w // 32, "scales", _U8)])
-    _check(load_library().mxfp4_dispatch_rows(_at(x), _at(pos), _at(codes), _at(scales), T, k, M_cap, K,
-                                              _stream(stream)), "mxfp4_dispatch_rows")
+    at = _take("mxfp4_dispatch_rows", [(x, 2 * t * w, "x", _B16), (pos, 4 * t * max(k, 0), "pos", _I32),
+                                       (codes, m * w // 2, "codes", _U8), (scales, m * w // 32, "scales", _U8)])
+    _check(load_library().mxfp4_dispatch_rows(*at, T, k, M_cap, K, _stream(stream)), "mxfp4_dispatch_rows")
 
 
 def mxfp4_dispatch_fp8_rows(x, pos, y, y_scales, T=None, k=None, M_cap=None, K=None, stream=None):
@@ -556,10 +571,10 @@ def mxfp4_dispatch_fp8_rows(x, pos, y, y_scales, T=None, k=None, M_cap=None, K=N
     expert order, each row quantized once and written to its places pos [T, k]."""
     T, k, M_cap, K = _token_dims(x, pos, y, T, k, M_cap, K)
     t, m, w = max(T, 0), max(M_cap, 0), max(K, 0)
-    _need("mxfp4_dispatch_fp8_rows", [(x, 2 * t * w, "x", _B16), (pos, 4 * t * max(k, 0), "pos", _I32),
-                                      (y, m * w, "y", _FP8), (y_scales, 4 * m * ((w + 127) // 128), "y_scales", _F32)])
-    _check(load_library().mxfp4_dispatch_fp8_rows(_at(x), _at(pos), _at(y), _at(y_scales), T, k, M_cap, K,
-                                                  _stream(stream)), "mxfp4_dispatch_fp8_rows")
+    at = _take("mxfp4_dispatch_fp8_rows", [(x, 2 * t * w, "x", _B16), (pos, 4 * t * max(k, 0), "pos", _I32),
+                                           (y, m * w, "y", _FP8),
+                                           (y_scales, 4 * m * ((w + 127) // 128), "y_scales", _F32)])
+    _check(load_library().mxfp4_dispatch_fp8_rows(*at, T, k, M_cap, K, _stream(stream)), "mxfp4_dispatch_fp8_rows")
 
 
 def mxfp4_bf16_to_fp8_rows_f32(x, y, y_scales, offs, G=None, M_cap=None, K=None, stream=None):
@@ -567,11 +582,10 @@ def mxfp4_bf16_to_fp8_rows_f32(x, y, y_scales, offs, G=None, M_cap=None, K=None,
     [0, offs[G]) (the quantizer of mxfp4_dispatch_fp8_rows)."""
     G, M_cap, K = _dims(x, offs, G, M_cap, K)
     m, w = max(M_cap, 0), max(K, 0)
-    _need("mxfp4_bf16_to_fp8_rows_f32", [(x, 2 * m * w, "x", _B16), (y, m * w, "y", _FP8),
-                                         (y_scales, 4 * m * ((w + 127) // 128), "y_scales", _F32),
-                                         (offs, 4 * (G + 1), "group_offsets", _I32)])
-    _check(load_library().mxfp4_bf16_to_fp8_rows_f32(_at(x), _at(y), _at(y_scales), _at(offs), G, M_cap, K,
-                                                     _stream(stream)), "mxfp4_bf16_to_fp8_rows_f32")
+    at = _take("mxfp4_bf16_to_fp8_rows_f32", [(x, 2 * m * w, "x", _B16), (y, m * w, "y", _FP8),
+                                              (y_scales, 4 * m * ((w + 127) // 128), "y_scales", _F32),
+                                              (offs, 4 * (G + 1), "group_offsets", _I32)])
+    _check(load_library().mxfp4_bf16_to_fp8_rows_f32(*at, G, M_cap, K, _stream(stream)), "mxfp4_bf16_to_fp8_rows_f32")
 
 
 def mxfp4_fp8_block_gemm(a, a_scales, w, w_scales, y, offs, G=None, M_cap=None, N=None, K=None, stream=None):
@@ -588,11 +602,10 @@ def mxfp4_fp8_block_gemm(a, a_scales, w, w_scales, y, offs, G=None, M_cap=None, 
     G, M_cap, N, K = int(G), int(M_cap), int(N), int(K)
     g, m, n, k = max(G, 0), max(M_cap, 0), max(N, 0), max(K, 0)
     nb, kb = (n + 127) // 128, (k + 127) // 128
-    _need("mxfp4_fp8_block_gemm", [(a, m * k, "a", _FP8), (a_scales, 4 * m * kb, "a_scales", _F32),
-                                   (w, g * n * k, "w", _FP8), (w_scales, 4 * g * nb * kb, "w_scales", _F32),
-                                   (y, 2 * m * n, "y", _B16), (offs, 4 * (G + 1), "group_offsets", _I32)])
-    _check(load_library().mxfp4_fp8_block_gemm(_at(a), _at(a_scales), _at(w), _at(w_scales), _at(y), _at(offs),
-                                               G, M_cap, N, K, _stream(stream)), "mxfp4_fp8_block_gemm")
+    at = _take("mxfp4_fp8_block_gemm", [(a, m * k, "a", _FP8), (a_scales, 4 * m * kb, "a_scales", _F32),
+                                        (w, g * n * k, "w", _FP8), (w_scales, 4 * g * nb * kb, "w_scales", _F32),
+                                        (y, 2 * m * n, "y", _B16), (offs, 4 * (G + 1), "group_offsets", _I32)])
+    _check(load_library().mxfp4_fp8_block_gemm(*at, G, M_cap, N, K, _stream(stream)), "mxfp4_fp8_block_gemm")
 
 
 def mxfp4_combine_rows(y, pos, out, weights=None, base=None, T=None, k=None, M_cap=None, K=None, stream=None):
@@ -601,11 +614,10 @@ def mxfp4_combine_rows(y, pos, out, weights=None, base=None, T=None, k=None, M_c
     T, k, M_cap, K = _token_dims(y, pos, y, T, k, M_cap, K)
     t, w = max(T, 0), max(K, 0)
     n = t * max(k, 0)
-    _need("mxfp4_combine_rows", [(y, 2 * max(M_cap, 0) * w, "y", _B16), (pos, 4 * n, "pos", _I32),
-                                 (weights, 4 * n, "weights", _F32), (base, 2 * t * w, "base", _B16),
-                                 (out, 2 * t * w, "out", _B16)])
-    _check(load_library().mxfp4_combine_rows(_at(y), _at(pos), _at(weights), _at(base), _at(out), T, k, M_cap, K,
-                                             _stream(stream)), "mxfp4_combine_rows")
+    at = _take("mxfp4_combine_rows", [(y, 2 * max(M_cap, 0) * w, "y", _B16), (pos, 4 * n, "pos", _I32),
+                                      (weights, 4 * n, "weights", _F32), (base, 2 * t * w, "base", _B16),
+                                      (out, 2 * t * w, "out", _B16)])
+    _check(load_library().mxfp4_combine_rows(*at, T, k, M_cap, K, _stream(stream)), "mxfp4_combine_rows")
 
 
 def mxfp4_combine_rows_backward(dout, y, pos, weights, dy, dweights, T=None, k=None, M_cap=None, K=None, stream=None):
@@ -614,11 +626,10 @@ def mxfp4_combine_rows_backward(dout, y, pos, weights, dy, dweights, T=None, k=N
     T, k, M_cap, K = _token_dims(dout, pos, y, T, k, M_cap, K)
     t, m, w = max(T, 0), max(M_cap, 0), max(K, 0)
     n = t * max(k, 0)
-    _need("mxfp4_combine_rows_backward", [(dout, 2 * t * w, "dout", _B16), (y, 2 * m * w, "y", _B16),
-                                          (pos, 4 * n, "pos", _I32), (weights, 4 * n, "weights", _F32),
-                                          (dy, 2 * m * w, "dy", _B16), (dweights, 4 * n, "dweights", _F32)])
-    _check(load_library().mxfp4_combine_rows_backward(_at(dout), _at(y), _at(pos), _at(weights), _at(dy),
-                                                      _at(dweights), T, k, M_cap, K, _stream(stream)),
+    at = _take("mxfp4_combine_rows_backward", [(dout, 2 * t * w, "dout", _B16), (y, 2 * m * w, "y", _B16),
+                                               (pos, 4 * n, "pos", _I32), (weights, 4 * n, "weights", _F32),
+                                               (dy, 2 * m * w, "dy", _B16), (dweights, 4 * n, "dweights", _F32)])
+    _check(load_library().mxfp4_combine_rows_backward(*at, T, k, M_cap, K, _stream(stream)),
            "mxfp4_combine_rows_backward")
 
 
