@@ -99,7 +99,7 @@ struct Tile {
     static constexpr int kLoadsA = TM / 8 / kWaves, kLoadsW = TN / 8 / kWaves;   // 8-row loads of a wave
     static constexpr int kSlots = 64 * kWaves;              // scale slots (those past TM are not read)
     static constexpr int kTiles = MT * NT;
-    static constexpr int kLag = 2;                          // products in flight before their scaled add
+    static constexpr int kLag = 3;                          // products in flight before their scaled add
     // Scales: with two buffers, those of two stages at a time go through registers to LDS
     // (half the requests); with four, each stage's go into its buffer with the operands, a
     // wave's token slots and then its weights' scale, so that no register waits for memory
@@ -209,8 +209,7 @@ struct Tile {
             t.p[I & 3] = mfma128(t.fw[I % NT], t.fa[I / NT % 2], f32x4{});
             if constexpr (I / NT == MT - 1) {
                 t.fw[I % NT] = weight_frag(cx, b, I % NT);
-                if constexpr (D == 4)
-                    issue_operands(cx, (b + D - 1) % D, s, I % NT);
+                issue_operands(cx, (b + D - 1) % D, s, I % NT);
             }
             if constexpr (I >= kLag)
                 add<I - kLag>(t);
@@ -233,30 +232,25 @@ struct Tile {
     static __device__ __forceinline__ void stage(const TileCtx<D>& cx, State& t, uint32_t s)
     {
         constexpr int kNext = (B + 1) % D;
-        __builtin_amdgcn_s_setprio(1);
+        add<-3>(t);
         add<-2>(t);
         add<-1>(t);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
             t.sc[mt] = t.raw[mt] * t.wsc[B];
         token_tiles<0>(cx, t, B);
-        __builtin_amdgcn_s_setprio(0);
         // every fragment of this stage is in registers: wait for the next one's loads, meet
         // the others, and load a later one into this buffer
         __builtin_amdgcn_s_waitcnt(vmcnt_at_most(kInFlight));
         if (!kDmaScales && B % 2 == 1)
             store_scales(cx, t, kNext, s + 1);
-        if constexpr (D == 2) {
+        if constexpr (D == 2)
             __syncthreads();
-#pragma unroll
-            for (int part = 0; part < NT; ++part)
-                issue_operands(cx, B, s + D, part);
-        } else {
-            meet();                               // (the operand loads go between the products)
-        }
-        issue_scales(cx, t, B, s + D);
-        read_scales(cx, t, kNext, s + 1);
+        else
+            meet();
         t.fa[0] = token_frag(cx, kNext, 0);
+        read_scales(cx, t, kNext, s + 1);
+        issue_scales(cx, t, B, s + D);
         products<(MT - 1) * NT, kTiles>(cx, t, kNext, s + D);
     }
 };
@@ -386,6 +380,7 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
             W::template stage<3>(cx, t, s + 3);
         }
     }
+    W::template add<-3>(t);
     W::template add<-2>(t);
     W::template add<-1>(t);
 
