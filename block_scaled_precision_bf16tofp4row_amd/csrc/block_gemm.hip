@@ -11,7 +11,7 @@
 // v_mfma_f32_32x32x64 per block, 16 results each, measured 1490 us where this form, in the
 // first version of the same tile, took 1225.)
 //
-// What bounds it (32768 rows x 7168 x 4096, 8 experts, 960-980 us, 1.96-2.0 PFLOP/s; this
+// What bounds it (32768 rows x 7168 x 4096, 8 experts, 890-940 us, 2.05-2.15 PFLOP/s; this
 // library's UE8M0-scaled product of that size, where the matrix cores apply the scales,
 // takes 802, the vendor library's per-tensor-scaled FP8 product 710): the matrix
 // instructions fill 2048 cycles of a 256 x 256 tile's stage, the scaled adds half as many
@@ -262,10 +262,13 @@ struct Tile {
 // tile ahead; wait for the next stage's loads, barrier; products of the last token tile,
 // while the next stage's first fragments are read (a weight fragment right after its last
 // use) and a later stage's loads go out into the buffer just left.  So the barrier never
-// finds a wave without matrix work behind it, and the scaled adds run two products late.
+// finds a wave without matrix work behind it.  The scaled adds run three products late and
+// the operand loads go out one or two at a time between the last tile's products (256 x 256,
+// 32768 rows x 7168 x 4096: 890-940 us; adds two late 925-960; all loads in a burst behind
+// the barrier as well 970-990).
 // D = 2 for the tiles of 64 KB and 32 KB stages that share a CU or fill it; D = 4 where a CU
 // holds one workgroup with little work per stage, which would wait for memory each time (128
-// x 128, 1024 rows x 4096 x 4096: 25.5 us with 8 waves and D = 4, 28.7 with 4 and D = 2).
+// x 128, 1024 rows x 4096 x 4096: 25.5 us with 8 waves and D = 4, 26.8 with 4 and D = 2).
 template <int WM, int WN, int MT, int NT, int D>
 __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
@@ -563,14 +566,14 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
     };
     // The choice goes by the rows an expert has on average and by the number of workgroups
     // (256 CUs).  Measured in us, the chosen one first:
-    //   256 x 256, from 192 rows per expert on: 8 experts, 2048 rows x 4096 x 7168: 116, 128 x
-    //     128: 134; 32768 rows: 965, 1070; but 1 expert, 1024 rows x 4096 x 4096 (64 tiles): 55
+    //   256 x 256, from 192 rows per expert on: 8 experts, 2048 rows x 4096 x 7168: 110, 128 x
+    //     128: 132; 32768 rows: 920, 1096; but 1 expert, 1024 rows x 4096 x 4096 (64 tiles): 52
     //     against 25.5
     //   128 x 128, from 12 rows on: two buffers and 4 waves where CUs share workgroups (32
-    //     experts, 2048 rows: 231, 8 waves and four buffers 242), the latter for fewer tiles (3
-    //     experts, 1501 rows x 1352 x 1744: 16.3, 17.7)
-    //   32 x 128 below (32 experts, 128 rows: 157, 128 x 128 165; 1 expert, 200 rows x 4096 x
-    //     7168: 21.5, 33.4)
+    //     experts, 2048 rows: 231, 8 waves and four buffers 243), the latter for fewer tiles (3
+    //     experts, 1501 rows x 1352 x 1744: 16.3, 17.6)
+    //   32 x 128 below (32 experts, 128 rows: 156, 128 x 128 164; 1 expert, 200 rows x 4096 x
+    //     7168: 21.7, 33.1)
     //   rows kernel, for at most a row per expert on average or a few rows and few tiles: 256
     //     experts, 64 rows x 4096 x 2048: 97, 32 x 128 149; 1 expert, 16 rows x 2112 x 7168:
     //     14.6, 18.8 (64 rows: 19.4, 8.7); 64 features a workgroup, or 32 to have enough of
