@@ -44,17 +44,19 @@ __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp
 __device__ __forceinline__ float sigmoid_fast(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x)); }
 __device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x)); }
 
-// FP32 -> order key: larger key, larger value; NaN gives 1 (below -inf), never 0.  (No sum
-// of a score, which is +0 or more, and a bias is -0.)
+// FP32 -> order key: larger key, larger value.  Numbers take 0x00FFFFFE (-inf) to 0xFFFFFFFF
+// (+inf); the sum that puts +inf there lets every NaN wrap to less than -inf, and the maximum
+// makes them one.  No key is 0.  (No sum of a score, which is +0 or more, and a bias is -0.)
+constexpr uint32_t kKeyOffset = 0x807FFFFFu, kKeyNaN = 0x00FFFFFDu;
 __device__ __forceinline__ uint32_t order_key(float c)
 {
     const uint32_t b = __float_as_uint(c);
-    const uint32_t k = (int32_t)b < 0 ? ~b : b | 0x80000000u;
-    return c == c ? k : 1u;
+    return max((b ^ ((uint32_t)((int32_t)b >> 31) & 0x7FFFFFFFu)) + kKeyOffset, kKeyNaN);
 }
 __device__ __forceinline__ float key_value(uint32_t k)
 {
-    return k <= 1u ? __uint_as_float(0x7FC00000u) : __uint_as_float((int32_t)k < 0 ? k & 0x7FFFFFFFu : ~k);
+    const uint32_t b = k - kKeyOffset;
+    return __uint_as_float(k <= kKeyNaN ? 0x7FC00000u : b ^ ((uint32_t)((int32_t)b >> 31) & 0x7FFFFFFFu));
 }
 
 // What lane ^ D holds, for a value that is the same in every aligned run of D lanes.
@@ -215,11 +217,11 @@ __global__ __launch_bounds__(kThreads) void route_kernel(
             }
             group_top2(k1, k2, l_log);
             const float v = group_best == 2 ? key_value(k1) + key_value(k2) : key_value(k1);
-            const uint32_t gk = order_key(v);     // (at most that of +inf: gk + 1 is larger)
+            const uint32_t gk = order_key(v);
             int rank = 0;
             for (int h = 0; h < n_group; ++h) {
                 const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)gk, h << l_log);
-                rank += o + (h < g) > gk;         // a group before this one wins ties
+                rank += o > gk - (h < g);         // a group before this one wins ties (no key is 0)
             }
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
@@ -294,6 +296,11 @@ __device__ __forceinline__ double candidate(uint32_t key, uint32_t low)
     const uint32_t hi = __builtin_amdgcn_alignbit(0x40000u, key, 12), lo = key << 20 | low;
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
+__device__ __forceinline__ uint32_t key_of(double c)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, c);
+    return __builtin_amdgcn_alignbit((uint32_t)(u >> 32), (uint32_t)u, 20);
+}
 __device__ __forceinline__ double with_low(double c, uint32_t low)
 {
     return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, c) | low);
@@ -355,8 +362,8 @@ __device__ __forceinline__ int group_rank(uint32_t gk, uint32_t g)
 {
     if constexpr (N < 16) {
         constexpr int kRor = 0x120 + N;
-        const uint32_t before = dpp<kRor>(g) < g;          // it wins ties
-        return (dpp<kRor>(gk) + before > gk) + group_rank<L, N + L>(gk, g);
+        const uint32_t before = dpp<kRor>(g) < g;          // it wins ties (no key is 0)
+        return (dpp<kRor>(gk) > gk - before) + group_rank<L, N + L>(gk, g);
     }
     return 0;
 }
@@ -368,26 +375,23 @@ __global__ __launch_bounds__(kThreads) void route_quad_kernel(
     int topk_group, int group_best, int k, int sigmoid, int renorm, float scale, int l_log)
 {
     constexpr int kList = VPL < 8 ? VPL : 8;
-    __shared__ __attribute__((aligned(16))) float s_lds[kThreads / 64][64 * VPL];
     __shared__ double list[kThreads / 64][kList + 1][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15;                      // lane of the row
-    const int64_t step = (int64_t)gridDim.x * kThreads / 16;
-    int64_t t0 = ((int64_t)blockIdx.x * (kThreads / 64) + wave) * 4;
-    if (t0 >= n_tokens)
+    const int64_t t = ((int64_t)blockIdx.x * (kThreads / 64) + wave) * 4 + (lane >> 4);
+    if (t - (lane >> 4) >= n_tokens)
         return;
     const int e0 = r * VPL;                       // the lane's first expert
     const int nv = E - e0;                        // the experts it has, at most VPL of them
-    const uint32_t g = (uint32_t)r >> l_log;
-    const uint32_t low = (uint32_t)(15 - r) * VPL;        // (VPL is a power of two)
+    const T* const row = logits + min(t, n_tokens - 1) * E;
 
     // (slots without an expert read another one's, rows without a token the last one's)
-    auto load_row = [&](float (&v)[VPL], const auto* row) {
+    auto load_row = [&](float (&v)[VPL], const auto* from) {
         if constexpr (VEC) {
 #pragma unroll
             for (int i = 0; i < VPL; i += 4) {
-                const f32x4 q = load_logit4(row + (i < nv ? e0 + i : 0));
+                const f32x4 q = load_logit4(from + (i < nv ? e0 + i : 0));
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     v[i + j] = q[j];
@@ -395,102 +399,85 @@ __global__ __launch_bounds__(kThreads) void route_quad_kernel(
         } else {
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                v[i] = load_logit(row + (i < nv ? e0 + i : 0));
+                v[i] = load_logit(from + (i < nv ? e0 + i : 0));
         }
     };
-    auto row_at = [&](int64_t t) { return logits + min(t + (lane >> 4), n_tokens - 1) * E; };
-    float b[VPL] = {}, next[VPL];
+    float s[VPL], b[VPL] = {}, m = 0.0f, inv = 1.0f;
+    load_row(s, row);
     if (bias)
         load_row(b, bias);
-    load_row(next, row_at(t0));
+    const bool chosen = row_mask == nullptr || row_mask[min(t, n_tokens - 1)] != 0;
     list[wave][kList][lane] = 0.0;                // below every candidate
-    for (; t0 < n_tokens; t0 += step) {
-        float s[VPL];
+    if (sigmoid) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            s[i] = next[i];
-        if (t0 + step < n_tokens)
-            load_row(next, row_at(t0 + step));
-        if (sigmoid) {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                s[i] = sigmoid_fast(s[i]);
-        } else {
-            float top = -__builtin_inff(), sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                s[i] = i < nv ? s[i] : -__builtin_inff();
-                top = fmaxf(top, s[i]);
-            }
-            const float m = norm_top(row_max(order_key(top)));
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                sum += s[i] = exp_fast(s[i] - m);
-            const float inv = norm_inv(row_sum(sum));
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                s[i] *= inv;
-        }
-        uint32_t key[VPL];
+            s[i] = sigmoid_fast(s[i]);
+    } else {
+        float top = -__builtin_inff(), sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            key[i] = order_key(s[i] + b[i]) & (i < nv ? ~0u : 0u);
-            s_lds[wave][i * 64 + lane] = s[i];
+            s[i] = i < nv ? s[i] : -__builtin_inff();
+            top = fmaxf(top, s[i]);
         }
-        if (topk_group < n_group) {
-            uint32_t k1 = 0, k2 = 0;              // the two largest keys of the lane, then of the group
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                k2 = max(k2, min(k1, key[i]));
-                k1 = max(k1, key[i]);
-            }
-            group_top2(k1, k2, l_log);
-            const float v = group_best == 2 ? key_value(k1) + key_value(k2) : key_value(k1);
-            const uint32_t gk = order_key(v);     // (at most that of +inf: gk + 1 is larger)
-            const int rank = l_log == 0   ? group_rank<1>(gk, g)
-                             : l_log == 1 ? group_rank<2>(gk, g)
-                             : l_log == 2 ? group_rank<4>(gk, g)
-                                          : group_rank<8>(gk, g);
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                key[i] = rank < topk_group ? key[i] : 0u;
-        }
-        double c[VPL];
+        m = norm_top(row_max(order_key(top)));
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            c[i] = candidate(key[i], (uint32_t)(VPL - 1 - i));
-        sort_best(c);
+            sum += s[i] = exp_fast(s[i] - m);
+        inv = norm_inv(row_sum(sum));
 #pragma unroll
-        for (int i = 0; i < kList; ++i)
-            c[i] = with_low(c[i], low);
+        for (int i = 0; i < VPL; ++i)
+            s[i] *= inv;
+    }
+    double c[VPL];
 #pragma unroll
-        for (int i = 1; i < kList; ++i)
-            list[wave][i][lane] = c[i];
-        double head = c[0];
-        const double* rest = &list[wave][1][lane];
-        uint32_t mine = 0;                        // lane j of the row: the low bits of choice j
-        for (int j = 0; j < k; ++j) {
-            const double best = row_best(head);
-            if (__builtin_bit_cast(uint64_t, head) == __builtin_bit_cast(uint64_t, best)) {
-                head = *rest;
-                rest += 64;
-            }
-            mine = r == j ? (uint32_t)__builtin_bit_cast(uint64_t, best) : mine;
+    for (int i = 0; i < VPL; ++i)
+        c[i] = candidate(order_key(s[i] + b[i]), (uint32_t)(VPL - 1 - i));
+    if (E < 16 * VPL) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            c[i] = i < nv ? c[i] : candidate(0, 0);
+    }
+    sort_best(c);
+#pragma unroll
+    for (int i = 0; i < kList; ++i)
+        c[i] = with_low(c[i], (uint32_t)(15 - r) * VPL);       // (VPL is a power of two)
+#pragma unroll
+    for (int i = 1; i < kList; ++i)
+        list[wave][i][lane] = c[i];
+    double head = c[0];
+    if (topk_group < n_group) {
+        uint32_t k1 = key_of(c[0]), k2 = key_of(c[1]);
+        group_top2(k1, k2, l_log);
+        const uint32_t gk = order_key(group_best == 2 ? key_value(k1) + key_value(k2) : key_value(k1));
+        const uint32_t g = (uint32_t)r >> l_log;
+        const int rank = l_log == 0   ? group_rank<1>(gk, g)
+                         : l_log == 1 ? group_rank<2>(gk, g)
+                         : l_log == 2 ? group_rank<4>(gk, g)
+                                      : group_rank<8>(gk, g);
+        head = rank < topk_group ? head : 0.0;    // a lane's experts are of one group
+    }
+    const double* rest = &list[wave][1][lane];
+    uint32_t mine = 0;                            // lane j of the row: the low bits of choice j
+    for (int j = 0; j < k; ++j) {
+        const double best = row_best(head);
+        if (__builtin_bit_cast(uint64_t, head) == __builtin_bit_cast(uint64_t, best)) {
+            head = *rest;
+            rest += 64;
         }
-        const int64_t t = t0 + (lane >> 4);
-        int e = 16 * VPL - 1 - (int)(mine & (16 * VPL - 1));
-        const float sj = r < k ? s_lds[wave][e % VPL * 64 + (lane & 48) + e / VPL] : 0.0f;
-        float w = scale * sj;
-        if (renorm)
-            w = scale * (sj / (row_sum(sj) + 1e-20f));
-        if (t < n_tokens && r < k) {
-            if (row_mask && !row_mask[t]) {
-                e = -1;
-                w = 0.0f;
-            }
-            ids[t * k + r] = e;
-            weights[t * k + r] = w;
-        }
+        mine = r == j ? (uint32_t)__builtin_bit_cast(uint64_t, best) : mine;
+    }
+    const int e = 16 * VPL - 1 - (int)(mine & (16 * VPL - 1));
+    float sj = 0.0f;                              // its score once more, from the cached logit
+    if (r < k) {
+        const float l = load_logit(row + e);
+        sj = sigmoid ? sigmoid_fast(l) : exp_fast(l - m) * inv;
+    }
+    float w = scale * sj;
+    if (renorm)
+        w = scale * (sj / (row_sum(sj) + 1e-20f));
+    if (t < n_tokens && r < k) {
+        ids[t * k + r] = chosen ? e : -1;
+        weights[t * k + r] = chosen ? w : 0.0f;
     }
 }
 
@@ -640,7 +627,8 @@ static const void* route_backward_for(int lanes, int q)
                     : (const void*)route_backward_kernel<64, 4, VEC, T>;
 }
 
-// Workgroups of the router at most: the 8 a CU holds at a time; they take tokens in turn.
+// Workgroups of the router at most with a wave per token: the 8 a CU holds at a time; they
+// take tokens in turn.
 constexpr int64_t kRouteGroups = 2048;
 
 hipError_t launch_route(const void* logits, bool f32, const float* bias, const uint8_t* row_mask, int32_t* ids,
@@ -670,7 +658,9 @@ hipError_t launch_route(const void* logits, bool f32, const float* bias, const u
             return hipErrorInvalidValue;
     }
     const int64_t need_groups = (T + tokens - 1) / tokens;
-    const int64_t grid = need_groups < kRouteGroups ? need_groups : kRouteGroups;
+    const int64_t grid = quad || need_groups < kRouteGroups ? need_groups : kRouteGroups;
+    if (grid > 0x7FFFFFFF)
+        return hipErrorInvalidValue;
     int64_t t = T;
     int e = E, ng = n_group, tg = topk_group, gb = group_best, kk = k, sg = sigmoid, rn = renorm;
     float sc = scale;
