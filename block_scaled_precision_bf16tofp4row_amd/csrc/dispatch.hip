@@ -96,7 +96,8 @@ __device__ __forceinline__ Place place_of(uint32_t row_lanes)
 {
     // rows of whole waves: the wave's number by the waves of a row, on the scalar unit
     const uint32_t per = kWhole ? row_lanes / 64 : row_lanes;
-    const uint64_t u = kWhole ? (uint64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint64_t u = kWhole ? (uint64_t)blockIdx.x * (kThreads / 64) + wave
                               : (uint64_t)blockIdx.x * kThreads + threadIdx.x;
     uint64_t t;
     if (gridDim.x < (1u << 24))                   // 32 bits hold every u

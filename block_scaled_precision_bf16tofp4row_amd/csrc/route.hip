@@ -14,6 +14,13 @@
 // Selection works on order keys: the FP32 bits of c made monotone as unsigned integers,
 // NaN below every number, and 0 for what is excluded, so that a comparison is one integer
 // maximum and any input gives k distinct valid indices.
+//
+// What bounds it: 32768 tokens x 256 experts in 8 groups, FP32 logits, 8 choices: 12.8 us for
+// 36 MB, which a copy moves in 7.0; the vector unit is busy for 80 % of the time (600
+// instructions per four tokens, half of them the scores and keys, a fifth the sort), with half
+// the bytes (BF16, softmax) it is 11.4 us.  32768 x 64, softmax: 5.6 us.  Few tokens are a
+// launch: 3.6 us for one, 4.2 for 128.  The gradient is its bytes: 16384 x 256, FP32: 8.0 us
+// for 35 MB (6.8 copied).
 #include "lanes.h"
 
 namespace mxfp4 {
@@ -274,10 +281,12 @@ __global__ __launch_bounds__(kThreads) void route_kernel(
 // Up to 256 experts and 8 choices: 16 lanes (a DPP row) per token, VPL consecutive experts
 // per lane.  A candidate is one number, the bits of a double in [2, 4) with the order key in
 // the top 32 bits of its mantissa and the expert below (the complements of its lane and of
-// its slot there, so that the lower expert is the larger number): no two are equal, the larger one is
-// the better choice, and v_max_f64 / v_min_f64 sort them without carrying an index along.
-// Each lane sorts its candidates (the best 8 of them), then k times the row's best head is
-// taken (four DPP steps) and its lane moves on in its list, which lies in LDS.
+// its slot there, so that the lower expert is the larger number): no two are equal, the larger
+// one is the better choice, and v_max_f64 / v_min_f64 sort them without carrying an index
+// along.  Each lane sorts its candidates (the best 8 of them), the groups are ranked on the
+// lists' heads, then k times the row's best head is taken (four DPP steps) and its lane moves
+// on in its list, which lies in LDS.  Against one token per wave: 32768 x 256 in 8 groups 12.8
+// and 31.5 us, 32768 x 64 5.6 and 12.7, 128 x 256 4.2 both.
 
 __device__ __forceinline__ double f64_max(double a, double b)
 {
@@ -680,6 +689,8 @@ hipError_t launch_route_backward(const void* logits, bool f32, const int32_t* id
                                  void* dlogits, int64_t T, int32_t E, int32_t k, bool sigmoid, bool renorm,
                                  float scale, hipStream_t stream)
 {
+    // a row of 16 lanes per token where it holds the choices and 16 experts a lane: 32768 x 60,
+    // BF16: 4.7 us, a wave per token 11.7; 16384 x 256, FP32: 8.0 and 8.6
     const int lanes = E <= 256 && k <= 16 ? 16 : 64;
     int q = 1;
     while (4 * lanes * q < E)
@@ -691,8 +702,11 @@ hipError_t launch_route_backward(const void* logits, bool f32, const int32_t* id
     float sc = scale;
     void* args[] = {(void*)&logits, (void*)&ids, (void*)&dweights, (void*)&dlogits, (void*)&t, (void*)&e,
                     (void*)&kk, (void*)&sg, (void*)&rn, (void*)&sc};
-    const void* kernel = E % 4 == 0 ? (f32 ? route_backward_for<true, float>(lanes, q) : route_backward_for<true, uint16_t>(lanes, q))
-                                    : (f32 ? route_backward_for<false, float>(lanes, q) : route_backward_for<false, uint16_t>(lanes, q));
+    const void* kernel;
+    if (E % 4 == 0)
+        kernel = f32 ? route_backward_for<true, float>(lanes, q) : route_backward_for<true, uint16_t>(lanes, q);
+    else
+        kernel = f32 ? route_backward_for<false, float>(lanes, q) : route_backward_for<false, uint16_t>(lanes, q);
     return launch_kernel(kernel, dim3((unsigned)grid), dim3(kThreads), args, stream);
 }
 
