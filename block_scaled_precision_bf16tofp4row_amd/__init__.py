@@ -201,14 +201,19 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = _device = None                      # torch's, once it has initialised the GPU
+
+
 def _current_stream() -> int:
     """The raw current stream of the current device.  torch.cuda.current_stream() builds a
     Stream object around it, which costs more than a small call's launch."""
+    global _raw_stream, _device
+    if _raw_stream is not None:
+        return _raw_stream(_device())
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None or not torch.cuda.is_initialized():
-        return torch.cuda.current_stream().cuda_stream
-    return raw(torch._C._cuda_getDevice())
+    if hasattr(torch._C, "_cuda_getCurrentRawStream") and torch.cuda.is_initialized():
+        _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _stream(stream) -> int | None:
@@ -235,7 +240,7 @@ def _need(what: str, args):
         have = t.nbytes
         if have < nbytes:
             raise ValueError(f"{what}: {name} holds {have} bytes, the launch needs {nbytes}")
-        if _dtype_name(t.dtype) not in dtypes:
+        if _dtype_name[t.dtype] not in dtypes:
             raise ValueError(f"{what}: {name} has dtype {t.dtype}, expected one of {', '.join(dtypes)}")
         if not t.is_contiguous():
             raise ValueError(f"{what}: {name} must be contiguous")
@@ -244,14 +249,13 @@ def _need(what: str, args):
             raise ValueError(f"{what}: {name} must be a GPU tensor")
 
 
-_dtype_names: dict = {}
+class _DtypeNames(dict):
+    def __missing__(self, dtype):
+        name = self[dtype] = str(dtype).replace("torch.", "")
+        return name
 
 
-def _dtype_name(dtype) -> str:
-    name = _dtype_names.get(dtype)
-    if name is None:
-        name = _dtype_names[dtype] = str(dtype).replace("torch.", "")
-    return name
+_dtype_name = _DtypeNames()
 
 
 _U8 = ("uint8",)
@@ -441,27 +445,31 @@ def mxfp4_nvfp4_quantize_rows_sr(x, codes, scales, tensor_amax, offs, seed, G=No
 _F32 = ("float32",)
 _I32 = ("int32",)
 _B16 = ("bfloat16", "int16", "uint16")
+_MASK = ("uint8", "bool")
+_WORK = ("int32", "uint8", "float32")
+
+
+_SCORES = {"softmax": MXFP4_SCORE_SOFTMAX, "sigmoid": MXFP4_SCORE_SIGMOID}
 
 
 def _score(score) -> int:
-    kinds = {"softmax": MXFP4_SCORE_SOFTMAX, "sigmoid": MXFP4_SCORE_SIGMOID}
-    if isinstance(score, str) and score not in kinds:
+    if isinstance(score, str) and score not in _SCORES:
         raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
-    return kinds.get(score, score)
+    return _SCORES.get(score, score)
 
 
 def _take(what: str, args):
     """_need's checks in one pass, and the tensors' addresses.  A tensor without elements gets
-    one that nothing reads (torch gives those none, and NULL is an error)."""
+    one that nothing reads (torch gives those none, and NULL is an error).  A negative size
+    needs no bytes here; the library refuses it."""
     at, host = [], None
     for t, nbytes, name, dtypes in args:
         if t is None or isinstance(t, int):
             at.append(t)
             continue
-        have = t.nbytes
-        if have < nbytes:
-            raise ValueError(f"{what}: {name} holds {have} bytes, the launch needs {nbytes}")
-        if _dtype_name(t.dtype) not in dtypes:
+        if t.nbytes < nbytes:
+            raise ValueError(f"{what}: {name} holds {t.nbytes} bytes, the launch needs {nbytes}")
+        if _dtype_name[t.dtype] not in dtypes:
             raise ValueError(f"{what}: {name} has dtype {t.dtype}, expected one of {', '.join(dtypes)}")
         if not t.is_contiguous():
             raise ValueError(f"{what}: {name} must be contiguous")
@@ -475,14 +483,14 @@ def _take(what: str, args):
 
 def _logits_dims(logits, ids, T, E, k, f32):
     """T, E, k and whether the logits are FP32, from the tensors where they are not given."""
-    if T is None:
-        T = logits.shape[0]
-    if E is None:
-        E = logits.shape[1]
+    if T is None or E is None:
+        shape = logits.shape
+        T = shape[0] if T is None else T
+        E = shape[1] if E is None else E
     if k is None:
         k = ids.shape[1]
     if f32 is None:
-        f32 = isinstance(logits, int) or _dtype_name(logits.dtype) == "float32"
+        f32 = isinstance(logits, int) or _dtype_name[logits.dtype] == "float32"
     return int(T), int(E), int(k), bool(f32)
 
 
@@ -491,11 +499,10 @@ def mxfp4_route_topk(logits, ids, weights, bias=None, row_mask=None, n_group=1, 
     """logits [T, E] (float32 or bfloat16) -> ids [T, k] int32 and weights [T, k] float32 of
     the k chosen experts; score "softmax" or "sigmoid" (see the header)."""
     T, E, k, f32 = _logits_dims(logits, ids, T, E, k, logits_f32)
-    t, e, n = max(T, 0), max(E, 0), max(T, 0) * max(k, 0)
-    at = _take("mxfp4_route_topk", [(logits, (4 if f32 else 2) * t * e, "logits", _F32 if f32 else _B16),
-                                    (bias, 4 * e, "bias", _F32), (row_mask, t, "row_mask", ("uint8", "bool")),
-                                    (ids, 4 * n, "ids", _I32), (weights, 4 * n, "weights", _F32)])
-    l, b, mask, i, w = at
+    n = 4 * T * k
+    l, b, mask, i, w = _take("mxfp4_route_topk", (
+        (logits, (4 if f32 else 2) * T * E, "logits", _F32 if f32 else _B16), (bias, 4 * E, "bias", _F32),
+        (row_mask, T, "row_mask", _MASK), (ids, n, "ids", _I32), (weights, n, "weights", _F32)))
     _check(load_library().mxfp4_route_topk(l, f32, b, mask, i, w, T, E, int(n_group), int(topk_group),
                                            int(group_best), k, _score(score), bool(renorm), float(scale),
                                            _stream(stream)), "mxfp4_route_topk")
@@ -506,11 +513,10 @@ def mxfp4_route_topk_backward(logits, ids, dweights, dlogits, score="softmax", r
     """The weights' gradient dweights [T, k] -> dlogits [T, E], of the logits' type (see the
     header)."""
     T, E, k, f32 = _logits_dims(logits, ids, T, E, k, logits_f32)
-    t, e, n = max(T, 0), max(E, 0), max(T, 0) * max(k, 0)
-    el, kinds = (4, _F32) if f32 else (2, _B16)
-    at = _take("mxfp4_route_topk_backward", [(logits, el * t * e, "logits", kinds), (ids, 4 * n, "ids", _I32),
-                                             (dweights, 4 * n, "dweights", _F32),
-                                             (dlogits, el * t * e, "dlogits", kinds)])
+    kinds = _F32 if f32 else _B16
+    rows, n = (4 if f32 else 2) * T * E, 4 * T * k
+    at = _take("mxfp4_route_topk_backward", ((logits, rows, "logits", kinds), (ids, n, "ids", _I32),
+                                             (dweights, n, "dweights", _F32), (dlogits, rows, "dlogits", kinds)))
     _check(load_library().mxfp4_route_topk_backward(at[0], f32, *at[1:], T, E, k, _score(score), bool(renorm),
                                                     float(scale), _stream(stream)), "mxfp4_route_topk_backward")
 
@@ -525,30 +531,29 @@ def mxfp4_expert_map(ids, offs, pos, workspace, src=None, first_expert=0, T=None
     none) and, if given, the slot src [M_cap] of every row (see the header).  M_cap defaults
     to src's size, or T k without it; workspace may be None where
     mxfp4_expert_map_workspace(T, k, G) is 0."""
-    if T is None:
-        T = ids.shape[0]
-    if k is None:
-        k = ids.shape[1]
+    if T is None or k is None:
+        shape = ids.shape
+        T = shape[0] if T is None else T
+        k = shape[1] if k is None else k
     if G is None:
         G = offs.numel() - 1
     if M_cap is None:
         M_cap = int(T) * int(k) if src is None or isinstance(src, int) else src.numel()
     T, k, G, M_cap = int(T), int(k), int(G), int(M_cap)
-    n = max(T, 0) * max(k, 0)
-    need = mxfp4_expert_map_workspace(T, k, G)
-    at = _take("mxfp4_expert_map", [(ids, 4 * n, "ids", _I32), (offs, 4 * (G + 1), "group_offsets", _I32),
-                                    (pos, 4 * n, "pos", _I32), (src, 4 * max(M_cap, 0), "src", _I32),
-                                    (workspace, max(need, 0), "workspace", ("int32", "uint8", "float32"))])
+    n = 4 * T * k
+    at = _take("mxfp4_expert_map", ((ids, n, "ids", _I32), (offs, 4 * (G + 1), "group_offsets", _I32),
+                                    (pos, n, "pos", _I32), (src, 4 * M_cap, "src", _I32),
+                                    (workspace, mxfp4_expert_map_workspace(T, k, G), "workspace", _WORK)))
     _check(load_library().mxfp4_expert_map(*at, T, k, int(first_expert), G, M_cap, _stream(stream)),
            "mxfp4_expert_map")
 
 
 def _token_dims(rows, pos, out, T, k, M_cap, K):
     """T and k from pos, K and M_cap from the token rows and the expert rows, where not given."""
-    if T is None:
-        T = pos.shape[0]
-    if k is None:
-        k = pos.shape[1]
+    if T is None or k is None:
+        shape = pos.shape
+        T = shape[0] if T is None else T
+        k = shape[1] if k is None else k
     if K is None:
         K = rows.shape[1]
     if M_cap is None:
@@ -560,9 +565,8 @@ def mxfp4_dispatch_rows(x, pos, codes, scales, T=None, k=None, M_cap=None, K=Non
     """BF16 token rows x [T, K] -> MXFP4 codes [M_cap, K/2] and scales [M_cap, K/32] in expert
     order, each row quantized once and written to its places pos [T, k]."""
     T, k, M_cap, K = _token_dims(x, pos, codes, T, k, M_cap, K)
-    t, m, w = max(T, 0), max(M_cap, 0), max(K, 0)
-    at = _take("mxfp4_dispatch_rows", [(x, 2 * t * w, "x", _B16), (pos, 4 * t * max(k, 0), "pos", _I32),
-                                       (codes, m * w // 2, "codes", _U8), (scales, m * w // 32, "scales", _U8)])
+    at = _take("mxfp4_dispatch_rows", ((x, 2 * T * K, "x", _B16), (pos, 4 * T * k, "pos", _I32),
+                                       (codes, M_cap * K // 2, "codes", _U8), (scales, M_cap * K // 32, "scales", _U8)))
     _check(load_library().mxfp4_dispatch_rows(*at, T, k, M_cap, K, _stream(stream)), "mxfp4_dispatch_rows")
 
 
@@ -570,10 +574,9 @@ def mxfp4_dispatch_fp8_rows(x, pos, y, y_scales, T=None, k=None, M_cap=None, K=N
     """BF16 token rows x [T, K] -> E4M3 y [M_cap, K] and FP32 y_scales [M_cap, ceil(K/128)] in
     expert order, each row quantized once and written to its places pos [T, k]."""
     T, k, M_cap, K = _token_dims(x, pos, y, T, k, M_cap, K)
-    t, m, w = max(T, 0), max(M_cap, 0), max(K, 0)
-    at = _take("mxfp4_dispatch_fp8_rows", [(x, 2 * t * w, "x", _B16), (pos, 4 * t * max(k, 0), "pos", _I32),
-                                           (y, m * w, "y", _FP8),
-                                           (y_scales, 4 * m * ((w + 127) // 128), "y_scales", _F32)])
+    at = _take("mxfp4_dispatch_fp8_rows", ((x, 2 * T * K, "x", _B16), (pos, 4 * T * k, "pos", _I32),
+                                           (y, M_cap * K, "y", _FP8),
+                                           (y_scales, 4 * M_cap * ((K + 127) // 128), "y_scales", _F32)))
     _check(load_library().mxfp4_dispatch_fp8_rows(*at, T, k, M_cap, K, _stream(stream)), "mxfp4_dispatch_fp8_rows")
 
 
@@ -581,10 +584,9 @@ def mxfp4_bf16_to_fp8_rows_f32(x, y, y_scales, offs, G=None, M_cap=None, K=None,
     """BF16 x [M_cap, K] -> E4M3 y [M_cap, K] + FP32 y_scales [M_cap, ceil(K/128)] for the rows
     [0, offs[G]) (the quantizer of mxfp4_dispatch_fp8_rows)."""
     G, M_cap, K = _dims(x, offs, G, M_cap, K)
-    m, w = max(M_cap, 0), max(K, 0)
-    at = _take("mxfp4_bf16_to_fp8_rows_f32", [(x, 2 * m * w, "x", _B16), (y, m * w, "y", _FP8),
-                                              (y_scales, 4 * m * ((w + 127) // 128), "y_scales", _F32),
-                                              (offs, 4 * (G + 1), "group_offsets", _I32)])
+    at = _take("mxfp4_bf16_to_fp8_rows_f32", ((x, 2 * M_cap * K, "x", _B16), (y, M_cap * K, "y", _FP8),
+                                              (y_scales, 4 * M_cap * ((K + 127) // 128), "y_scales", _F32),
+                                              (offs, 4 * (G + 1), "group_offsets", _I32)))
     _check(load_library().mxfp4_bf16_to_fp8_rows_f32(*at, G, M_cap, K, _stream(stream)), "mxfp4_bf16_to_fp8_rows_f32")
 
 
@@ -593,18 +595,17 @@ def mxfp4_fp8_block_gemm(a, a_scales, w, w_scales, y, offs, G=None, M_cap=None, 
     [G, ceil(N/128), ceil(K/128)]) -> BF16 y [M_cap, N] (see the header)."""
     if G is None:
         G = offs.numel() - 1
-    if M_cap is None:
-        M_cap = a.shape[0]
-    if K is None:
-        K = a.shape[1]
+    if M_cap is None or K is None:
+        shape = a.shape
+        M_cap = shape[0] if M_cap is None else M_cap
+        K = shape[1] if K is None else K
     if N is None:
         N = w.shape[-2]
     G, M_cap, N, K = int(G), int(M_cap), int(N), int(K)
-    g, m, n, k = max(G, 0), max(M_cap, 0), max(N, 0), max(K, 0)
-    nb, kb = (n + 127) // 128, (k + 127) // 128
-    at = _take("mxfp4_fp8_block_gemm", [(a, m * k, "a", _FP8), (a_scales, 4 * m * kb, "a_scales", _F32),
-                                        (w, g * n * k, "w", _FP8), (w_scales, 4 * g * nb * kb, "w_scales", _F32),
-                                        (y, 2 * m * n, "y", _B16), (offs, 4 * (G + 1), "group_offsets", _I32)])
+    nb, kb = (N + 127) // 128, (K + 127) // 128
+    at = _take("mxfp4_fp8_block_gemm", ((a, M_cap * K, "a", _FP8), (a_scales, 4 * M_cap * kb, "a_scales", _F32),
+                                        (w, G * N * K, "w", _FP8), (w_scales, 4 * G * nb * kb, "w_scales", _F32),
+                                        (y, 2 * M_cap * N, "y", _B16), (offs, 4 * (G + 1), "group_offsets", _I32)))
     _check(load_library().mxfp4_fp8_block_gemm(*at, G, M_cap, N, K, _stream(stream)), "mxfp4_fp8_block_gemm")
 
 
@@ -612,11 +613,10 @@ def mxfp4_combine_rows(y, pos, out, weights=None, base=None, T=None, k=None, M_c
     """out [T, K] = base [T, K] + sum over a token's rows of weights [T, k] * y[pos] (BF16 rows,
     FP32 sum; without weights the plain sum, without base from zero)."""
     T, k, M_cap, K = _token_dims(y, pos, y, T, k, M_cap, K)
-    t, w = max(T, 0), max(K, 0)
-    n = t * max(k, 0)
-    at = _take("mxfp4_combine_rows", [(y, 2 * max(M_cap, 0) * w, "y", _B16), (pos, 4 * n, "pos", _I32),
-                                      (weights, 4 * n, "weights", _F32), (base, 2 * t * w, "base", _B16),
-                                      (out, 2 * t * w, "out", _B16)])
+    n, rows = 4 * T * k, 2 * T * K
+    at = _take("mxfp4_combine_rows", ((y, 2 * M_cap * K, "y", _B16), (pos, n, "pos", _I32),
+                                      (weights, n, "weights", _F32), (base, rows, "base", _B16),
+                                      (out, rows, "out", _B16)))
     _check(load_library().mxfp4_combine_rows(*at, T, k, M_cap, K, _stream(stream)), "mxfp4_combine_rows")
 
 
@@ -624,11 +624,10 @@ def mxfp4_combine_rows_backward(dout, y, pos, weights, dy, dweights, T=None, k=N
     """The gradients of mxfp4_combine_rows: dy [M_cap, K] (BF16, the rows that have a slot) and
     dweights [T, k] (float32) from dout [T, K]."""
     T, k, M_cap, K = _token_dims(dout, pos, y, T, k, M_cap, K)
-    t, m, w = max(T, 0), max(M_cap, 0), max(K, 0)
-    n = t * max(k, 0)
-    at = _take("mxfp4_combine_rows_backward", [(dout, 2 * t * w, "dout", _B16), (y, 2 * m * w, "y", _B16),
-                                               (pos, 4 * n, "pos", _I32), (weights, 4 * n, "weights", _F32),
-                                               (dy, 2 * m * w, "dy", _B16), (dweights, 4 * n, "dweights", _F32)])
+    n, tokens, rows = 4 * T * k, 2 * T * K, 2 * M_cap * K
+    at = _take("mxfp4_combine_rows_backward", ((dout, tokens, "dout", _B16), (y, rows, "y", _B16),
+                                               (pos, n, "pos", _I32), (weights, n, "weights", _F32),
+                                               (dy, rows, "dy", _B16), (dweights, n, "dweights", _F32)))
     _check(load_library().mxfp4_combine_rows_backward(*at, T, k, M_cap, K, _stream(stream)),
            "mxfp4_combine_rows_backward")
 
