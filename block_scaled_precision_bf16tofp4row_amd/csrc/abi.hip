@@ -84,7 +84,7 @@ constexpr int32_t kMaxChoices = 64;
 // A call over the k choices of T tokens, rows of K elements, outputs or inputs of M_cap rows.
 mxfp4_status check_tokens(int64_t T, int32_t k, int64_t M_cap, int64_t K, int64_t k_multiple)
 {
-    if (T < 0 || k < 1 || k > kMaxChoices || M_cap < 0 || K <= 0 || K % k_multiple != 0)
+    if (T < 0 || k < 1 || k > kMaxChoices || M_cap < 0 || K <= 0 || K > INT32_MAX || K % k_multiple != 0)
         return MXFP4_ERR_SHAPE;
     if (T > INT32_MAX / k || M_cap > INT32_MAX)      // positions are int32
         return MXFP4_ERR_SHAPE;
@@ -489,6 +489,8 @@ mxfp4_status mxfp4_bf16_to_fp8_rows_f32(const uint16_t* x_bf16, uint8_t* y_e4m3,
     if (!x_bf16 || !y_e4m3 || !y_scales || !group_offsets)
         return MXFP4_ERR_NULL;
     mxfp4_status st = check_shape(G, M_cap, K, 16);
+    if (st == MXFP4_OK && K > INT32_MAX)             // lanes of a row are counted in 32 bits
+        st = MXFP4_ERR_SHAPE;
     if (st != MXFP4_OK)
         return st;
     if (!aligned(x_bf16, 16) || !aligned(y_e4m3, 16) || !aligned(y_scales, 16) || !aligned(group_offsets, 4))

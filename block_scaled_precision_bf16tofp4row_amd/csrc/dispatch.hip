@@ -122,7 +122,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(
     const uint32_t lane = at.lane;                // its lowest 3 bits are the hardware lane's
     const int64_t e0 = 16 * (int64_t)lane;
     // (lanes without elements stay for the exchange)
-    const bool in = t < (kInPlace ? (int64_t)offs[G] : n_tokens) && e0 < K;     // K is a multiple of 16
+    const bool in = t < n_tokens && (!kInPlace || t < offs[G]) && e0 < K;       // K is a multiple of 16
     u32x4 v0 = {0, 0, 0, 0}, v1 = {0, 0, 0, 0};
     if (in) {
         const u32x4* const p = reinterpret_cast<const u32x4*>(x + t * K + e0);

@@ -235,8 +235,8 @@ mxfp4_status mxfp4_fp8_grouped_gemm_wgrad(const uint8_t* dyT_e4m3, const uint8_t
  *     mxfp4_dispatch_fp8_rows    token rows -> E4M3 rows with FP32 scales, in expert order
  *     mxfp4_fp8_block_gemm       expert product of those with 128x128-scaled weights
  *     mxfp4_combine_rows         expert rows -> tokens       (backward: dy, dweights)
- * A slot is choice j < k of token t, number t k + j; T k is at most 2^31 - 1 and k at most
- * 64 (else MXFP4_ERR_SHAPE).  T == 0 enqueues nothing (but mxfp4_expert_map, which writes
+ * A slot is choice j < k of token t, number t k + j; T k and a row's K are at most 2^31 - 1
+ * and k at most 64 (else MXFP4_ERR_SHAPE).  T == 0 enqueues nothing (but mxfp4_expert_map, which writes
  * the zero offsets).  Pointers called optional may be NULL; all others, their alignment
  * (16 bytes) and the errors are as above. */
 

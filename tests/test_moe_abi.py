@@ -198,3 +198,13 @@ def test_empty_tensors_are_no_null_pointers():
     mx.mxfp4_dispatch_fp8_rows(e(b, 0, 64), e(i, 0, 2), e(u, 0, 64), e(f, 0, 1), stream=0)
     mx.mxfp4_combine_rows(e(b, 0, 64), e(i, 0, 2), e(b, 0, 64), stream=0)
     mx.mxfp4_combine_rows_backward(e(b, 0, 64), e(b, 0, 64), e(i, 0, 2), e(f, 0, 2), e(b, 0, 64), e(f, 0, 2), stream=0)
+
+
+def test_rows_longer_than_their_counters(lib):
+    """A row's lanes are counted in 32 bits: longer rows are refused, not wrapped."""
+    for K in (1 << 31, 1 << 37):
+        for call in (functools.partial(_disp, lib, "mxfp4_dispatch_rows"),
+                     functools.partial(_disp, lib, "mxfp4_dispatch_fp8_rows"), functools.partial(_comb, lib),
+                     functools.partial(_comb_back, lib)):
+            assert call(T=1, k=1, cap=1, K=K) == SHAPE, (call, K)
+        assert _rows(lib, M=1, K=K) == SHAPE, K
