@@ -373,15 +373,26 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
     for (int nt = 0; nt < NT; ++nt)
         t.fw[nt] = W::weight_frag(cx, 0, nt);
     t.fa[0] = W::token_frag(cx, 0, 0);
-    // D stages at a time; the loads and reads for a stage past the end find zeros, which add
-    // nothing (leaving the loop between its stages made the compiler copy the accumulators)
-    for (uint32_t s = 0; s < kb_n; s += D) {
+    // D stages at a time, then the rest one by one (leaving the loop between its stages made
+    // the compiler copy the accumulators; running whole turns over zeros took 16.3 us where
+    // this takes 15.5, 1501 rows x 1352 x 1744); the loads and reads for a stage past the last
+    // find zeros
+    uint32_t s = 0;
+    for (; s + D <= kb_n; s += D) {
         W::template stage<0>(cx, t, s);
         W::template stage<1>(cx, t, s + 1);
         if constexpr (D == 4) {
             W::template stage<2>(cx, t, s + 2);
             W::template stage<3>(cx, t, s + 3);
         }
+    }
+    if (s < kb_n)
+        W::template stage<0>(cx, t, s);
+    if constexpr (D == 4) {
+        if (s + 1 < kb_n)
+            W::template stage<1>(cx, t, s + 1);
+        if (s + 2 < kb_n)
+            W::template stage<2>(cx, t, s + 2);
     }
     W::template add<-3>(t);
     W::template add<-2>(t);
@@ -571,7 +582,7 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
     //     against 25.5
     //   128 x 128, from 12 rows on: two buffers and 4 waves where CUs share workgroups (32
     //     experts, 2048 rows: 231, 8 waves and four buffers 243), the latter for fewer tiles (3
-    //     experts, 1501 rows x 1352 x 1744: 16.3, 17.6)
+    //     experts, 1501 rows x 1352 x 1744: 15.5, 17.7)
     //   32 x 128 below (32 experts, 128 rows: 156, 128 x 128 164; 1 expert, 200 rows x 4096 x
     //     7168: 21.7, 33.1)
     //   rows kernel, for at most a row per expert on average or a few rows and few tiles: 256
