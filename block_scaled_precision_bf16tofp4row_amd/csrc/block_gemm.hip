@@ -288,7 +288,12 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     uint32_t mtile, ntile;
-    tile_of(group_interleave(blockIdx.x, gridDim.x, kGroupM * ntn), gridDim.x, ntn, mtile, ntile);
+    // Workgroups go round-robin over the 8 XCDs, so with pairs of token tiles an XCD has every
+    // second token tile and every fourth feature tile of a stretch: 8 x 4 of 256 workgroups,
+    // all of them on one expert or a few neighbours, and an expert with few rows spread over
+    // all XCDs.  (Groups of 4 dealt to one XCD each, as the other GEMM has them: 2048 rows over
+    // 32 experts 225 us, here 213; 65536 rows x 7168 x 2048 975, 955; 32768 rows 905, 892.)
+    tile_of<2>(blockIdx.x, gridDim.x, ntn, mtile, ntile);
     int g;
     int64_t row0;
     int rows;

@@ -43,14 +43,13 @@ __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offs, int 
     return false;
 }
 
-// Workgroup -> (token tile, feature tile).  The tiles of one XCD run in this order:
-// groups of kGroupM token tiles, every feature tile of a group before the next group,
-// the group's token tiles innermost, so the workgroups one XCD holds at a time share a
-// few operand tiles of each kind in its L2.
+// Position -> (token tile, feature tile): groups of GM token tiles, every feature tile of a
+// group before the next group, the group's token tiles innermost, so that neighbours share a
+// few operand tiles of each kind.
 constexpr uint32_t kGroupM = 4;
 
-// Workgroup -> position in that order for the fast kernel.  Workgroups are dealt
-// round-robin over the 8 XCDs; XCD x takes tile groups x, x + 8, x + 16, ... (a group is
+// Workgroup -> position in that order for the forward expert GEMM's fast kernel.  Workgroups
+// are dealt round-robin over the 8 XCDs; XCD x takes tile groups x, x + 8, x + 16, ... (a group is
 // kGroupM token tiles across all feature tiles), so that an XCD's workgroups share a
 // group's operand tiles in its L2 while the eight XCDs work on neighbouring groups, that
 // is on the same expert's weights at the same time.  The remainder past the last whole
@@ -64,14 +63,15 @@ __device__ __forceinline__ uint32_t group_interleave(uint32_t bid, uint32_t nblo
     const uint32_t x = bid & 7, slot = bid >> 3;
     return (x + 8 * (slot / gsz)) * gsz + slot % gsz;
 }
+template <uint32_t GM = kGroupM>
 __device__ __forceinline__ void tile_of(uint32_t lin, uint32_t nblocks, uint32_t ntn, uint32_t& mtile,
                                         uint32_t& ntile)
 {
     const uint32_t ntm = nblocks / ntn;
-    const uint32_t grp = lin / (kGroupM * ntn);
-    const uint32_t gm = min(kGroupM, ntm - grp * kGroupM);
-    const uint32_t idx = lin - grp * kGroupM * ntn;
-    mtile = grp * kGroupM + idx % gm;
+    const uint32_t grp = lin / (GM * ntn);
+    const uint32_t gm = min(GM, ntm - grp * GM);
+    const uint32_t idx = lin - grp * GM * ntn;
+    mtile = grp * GM + idx % gm;
     ntile = idx / gm;
 }
 
