@@ -1,4 +1,4 @@
-// lanes.h -- reductions over a wave and over its rows of 16 lanes, by DPP.
+// lanes.h -- sums and maxima over a wave and over its rows of 16 lanes, by DPP.
 #pragma once
 
 #include "strips.h"
@@ -41,6 +41,16 @@ __device__ __forceinline__ float wave_sum(float f)
     add(dpp_rows<kRowBcast15, 0xA>(__float_as_uint(f)));
     add(dpp_rows<kRowBcast31, 0xC>(__float_as_uint(f)));
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), 63));
+}
+// The sum over lanes 0 .. own: shifts by 1, 2, 4 and 8 within the rows of 16, then as above.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v)
+{
+    v += dpp_rows<0x111, 0xF>(v);
+    v += dpp_rows<0x112, 0xF>(v);
+    v += dpp_rows<0x114, 0xF>(v);
+    v += dpp_rows<0x118, 0xF>(v);
+    v += dpp_rows<kRowBcast15, 0xA>(v);
+    return v + dpp_rows<kRowBcast31, 0xC>(v);
 }
 // Over the 16 lanes of a row, the result in all of them.
 __device__ __forceinline__ float row_sum(float f)
