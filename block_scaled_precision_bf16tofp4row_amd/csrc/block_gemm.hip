@@ -16,12 +16,11 @@
 // takes 802, the vendor library's per-tensor-scaled FP8 product 710): the matrix
 // instructions fill 2048 cycles of a 256 x 256 tile's stage, the scaled adds half as many
 // vector cycles beside them, the fragment reads 1536 LDS cycles and the loads 512.  With few
-// rows it is the weights' bytes: 128 rows over 32 experts x 4096 x 7168 take 157 us, 6.0 TB/s.
+// rows it is the weights' bytes: 128 rows over 32 experts x 4096 x 7168 take 147 us, 6.4 TB/s.
 //
-// Two kernels.  The tile kernel stages both operands in LDS and serves everything from a few
-// rows per expert on; the rows kernel reads fragments straight from memory and splits K over
-// its waves, for a row or so per expert, or so few tiles that a tile's walk along K is the
-// time.  Buffer loads take the bounds: rows past the expert's and features past N are
+// Two kernels.  The tile kernel stages both operands in LDS; the rows kernel reads fragments
+// straight from memory and splits K over its waves, where there are so few tiles that a
+// tile's walk along K is the time.  Buffer loads take the bounds: rows past the expert's and features past N are
 // outside the ranges and read as zero, and a lane whose bytes are past K gets an offset
 // outside every range.
 #include "tiles.h"
@@ -88,6 +87,7 @@ struct TileCtx {
     uint32_t srow, sslot;                         // scale loader: global offset of the row, LDS slot
     uint32_t arow, wrow, c0, c1;                  // fragments: LDS offsets of the lane's rows, chunks
     uint32_t scl_at;                              // slot of the lane's first token scale
+    uint32_t turn, blocks;                        // the block of K that stage 0 takes, and their number
 };
 
 // The tile of WM x WN waves, each 16 MT tokens x 16 NT features, with D stage buffers.
@@ -99,16 +99,21 @@ struct Tile {
     static constexpr int kLoadsA = TM / 8 / kWaves, kLoadsW = TN / 8 / kWaves;   // 8-row loads of a wave
     static constexpr int kSlots = 64 * kWaves;              // scale slots (those past TM are not read)
     static constexpr int kTiles = MT * NT;
+    // Where rows are a multiple of 4096 bytes apart, a stage's 128-byte pieces of all rows lie
+    // in few memory channels.  The tile for few rows, which lives on the weights' stream, then
+    // starts each feature tile and expert at another block of K and goes round (64 rows over
+    // 128 experts x 4096 x 4096: 138 us, 160 all from the start; at 7168 deep it would cost 5 %).
+    static constexpr bool kTurn = TM == 32;
     static constexpr int kLag = 3;                          // products in flight before their scaled add
     // Scales: with two buffers, those of two stages at a time go through registers to LDS
-    // (half the requests); with four, each stage's go into its buffer with the operands, a
+    // (half the requests); with more, each stage's go into its buffer with the operands, a
     // wave's token slots and then its weights' scale, so that no register waits for memory
     // over several stages.
-    static constexpr bool kDmaScales = D == 4;
+    static constexpr bool kDmaScales = D > 2;
     static constexpr int kBuf = kStage + (kDmaScales ? 8 * kSlots : 0);
     // While stage s + 1 is awaited, the loads of stages s + 2 .. s + D - 1 may be in flight.
     static constexpr int kInFlight = (D - 2) * (kLoadsA + kLoadsW + 2);
-    static_assert(D == 2 || D == 4, "stage buffers");
+    static_assert(D >= 2 && D <= 4, "stage buffers");
     static_assert(TM % (8 * kWaves) == 0 && TN % (8 * kWaves) == 0 && TM <= kSlots, "loads");
     static_assert(TN % 128 == 0 && 128 % (16 * NT) == 0, "a wave's features lie in one scale block");
     static_assert(2 * kStage >= TM * TN * 2, "the epilogue stages the tile in two buffers");
@@ -127,12 +132,20 @@ struct Tile {
     {
         return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
     }
+    // The block of K that stage s takes.
+    static __device__ __forceinline__ uint32_t block_of(const TileCtx<D>& cx, uint32_t s)
+    {
+        if constexpr (!kTurn)
+            return s;
+        const uint32_t b = s + cx.turn;
+        return s < cx.blocks ? b < cx.blocks ? b : b - cx.blocks : cx.blocks;
+    }
     // Part `part` of NT of the operand loads of stage s into buffer b = s % D.  Offsets are
     // made here, from registers that live across the stages; a stage past the last reads
     // nothing (its columns are past K).
     static __device__ __forceinline__ void issue_operands(const TileCtx<D>& cx, int b, uint32_t s, int part)
     {
-        const uint32_t k0 = s * kBK;
+        const uint32_t k0 = block_of(cx, s) * kBK;
 #pragma unroll
         for (int j = part * (kLoadsA + kLoadsW) / NT; j < (part + 1) * (kLoadsA + kLoadsW) / NT; ++j) {
             const bool tok = j < kLoadsA;
@@ -146,13 +159,14 @@ struct Tile {
     // Its scales.
     static __device__ __forceinline__ void issue_scales(const TileCtx<D>& cx, State& t, int b, uint32_t s)
     {
-        const uint32_t k0 = s * kBK;
         if constexpr (kDmaScales) {
+            const uint32_t kb = block_of(cx, s);
             uint8_t* const to = cx.buf[b] + kStage + cx.lds_s;
-            load4_to_lds(cx.rsa, to, k0 < cx.K ? cx.srow + 4 * s : kOutOfRange);
-            load4_to_lds(cx.rsw, to + 4 * kSlots, 4 * s);
+            load4_to_lds(cx.rsa, to, kb * kBK < cx.K ? cx.srow + 4 * kb : kOutOfRange);
+            load4_to_lds(cx.rsw, to + 4 * kSlots, 4 * kb);
             return;
         }
+        const uint32_t k0 = s * kBK;
         t.wsc[b] = load_f32(cx.rsw, 4 * s);
         if (b % 2 == 0) {
             t.ld[b] = load_f32(cx.rsa, k0 < cx.K ? cx.srow + 4 * s : kOutOfRange);
@@ -268,7 +282,10 @@ struct Tile {
 // the barrier as well 970-990).
 // D = 2 for the tiles of 64 KB and 32 KB stages that share a CU or fill it; D = 4 where a CU
 // holds one workgroup with little work per stage, which would wait for memory each time (128
-// x 128, 1024 rows x 4096 x 4096: 25.5 us with 8 waves and D = 4, 26.8 with 4 and D = 2).
+// x 128, 1024 rows x 4096 x 4096: 25.5 us with 8 waves and D = 4, 26.8 with 4 and D = 2); D =
+// 3 for the 32 x 128 tile where there is more than one per CU: two then fit its LDS, and one
+// works while the other starts or ends (64 rows over 256 experts x 4096 x 2048: 80 us, D = 4
+// 83, D = 2 87; 128 rows over 32 experts x 4096 x 7168: 146, 148, 179).
 template <int WM, int WN, int MT, int NT, int D>
 __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
@@ -280,8 +297,8 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
     // separate arrays: what is loaded into one does not hold up reads of another
     __shared__ __attribute__((aligned(16))) uint8_t lds0[W::kBuf];
     __shared__ __attribute__((aligned(16))) uint8_t lds1[W::kBuf];
-    __shared__ __attribute__((aligned(16))) uint8_t lds2[D == 4 ? W::kBuf : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t lds3[D == 4 ? W::kBuf : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t lds2[D > 2 ? W::kBuf : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t lds3[D > 3 ? W::kBuf : 16];
     __shared__ __attribute__((aligned(16))) float scl[W::kDmaScales ? 4 : 4 * W::kSlots];
 
     const int tid = threadIdx.x;
@@ -318,16 +335,18 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
     TileCtx<D> cx;
     cx.buf[0] = lds0;
     cx.buf[1] = lds1;
-    if constexpr (D == 4) {
+    if constexpr (D > 2)
         cx.buf[2] = lds2;
+    if constexpr (D > 3)
         cx.buf[3] = lds3;
-    }
     cx.scl = scl;
     cx.ra = strip_rsrc(a + row0 * K, (uint64_t)rows * (uint64_t)K);
     cx.rw = strip_rsrc(w + ((int64_t)g * N + n0) * K, (uint64_t)cols * (uint64_t)K);
     cx.rsa = strip_rsrc(sa + row0 * kb_n, (uint64_t)rows * kb_n * 4);
     cx.rsw = strip_rsrc(sw + ((int64_t)g * nb_n + nb) * kb_n, (uint64_t)kb_n * 4);
     cx.K = (uint32_t)K;
+    cx.blocks = kb_n;
+    cx.turn = K % 4096 == 0 ? (ntile + 5 * (uint32_t)g) % kb_n : 0;
     cx.abase = (8 * ag + l8) * cx.K;
     cx.wbase = (8 * wg + l8) * cx.K;
     cx.ac0 = 16 * (lc ^ ((4 * ag + l16) & 7));
@@ -386,19 +405,19 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
     for (; s + D <= kb_n; s += D) {
         W::template stage<0>(cx, t, s);
         W::template stage<1>(cx, t, s + 1);
-        if constexpr (D == 4) {
+        if constexpr (D > 2)
             W::template stage<2>(cx, t, s + 2);
+        if constexpr (D > 3)
             W::template stage<3>(cx, t, s + 3);
-        }
     }
     if (s < kb_n)
         W::template stage<0>(cx, t, s);
-    if constexpr (D == 4) {
+    if constexpr (D > 2)
         if (s + 1 < kb_n)
             W::template stage<1>(cx, t, s + 1);
+    if constexpr (D > 3)
         if (s + 2 < kb_n)
             W::template stage<2>(cx, t, s + 2);
-    }
     W::template add<-3>(t);
     W::template add<-2>(t);
     W::template add<-1>(t);
@@ -436,18 +455,19 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
     }
 }
 
-// The kernel for few rows per expert, where the weights are the traffic: a workgroup owns
-// 16 MT tokens x 16 NT features and its W waves share K, each a run of blocks whose operands
-// go from memory straight into the fragments' registers (a lane's two 16-byte chunks of a
-// row; four lanes cover 64 contiguous bytes), kAhead blocks ahead.  The waves' sums meet in
-// LDS and are added in wave order.
-template <int MT, int NT, int W>
-__global__ __launch_bounds__(64 * W) void block_gemm_rows_kernel(
+// The kernel for few rows and few tiles, where a tile's walk along K would be the time: a
+// workgroup owns 16 tokens x 32 features and its 4 waves share K, each a run of blocks whose
+// operands go from memory straight into the fragments' registers (a lane's two 16-byte chunks
+// of a row; four lanes cover 64 contiguous bytes), kAhead blocks ahead.  The waves' sums meet
+// in LDS and are added in wave order.
+constexpr int kRowsTM = 16, kRowsTN = 32, kRowsWaves = 4;
+
+__global__ __launch_bounds__(64 * kRowsWaves) void block_gemm_rows_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
     const float* __restrict__ sw, uint16_t* __restrict__ y, const int32_t* __restrict__ offs, int G, int64_t N,
     int64_t K, uint32_t ntm)
 {
-    constexpr int TM = 16 * MT, TN = 16 * NT, kAhead = 3;
+    constexpr int TM = kRowsTM, TN = kRowsTN, W = kRowsWaves, NT = TN / 16, kAhead = 3;
     constexpr int kRow = TN + 4;                  // floats of a token's row in LDS
     __shared__ __attribute__((aligned(16))) float part[W][TM][kRow];
 
@@ -475,8 +495,8 @@ __global__ __launch_bounds__(64 * W) void block_gemm_rows_kernel(
     const __amdgpu_buffer_rsrc_t rsw = strip_rsrc(sw + ((int64_t)g * nb_n + n0 / 128) * kb_n, (uint64_t)kb_n * 4);
 
     struct Block {
-        i32x8 w[NT], a[MT];
-        float sa[MT], sw;
+        i32x8 w[NT], a;
+        float sa, sw;
     };
     auto chunk = [&](__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t k) {
         return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
@@ -492,22 +512,16 @@ __global__ __launch_bounds__(64 * W) void block_gemm_rows_kernel(
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             b.w[nt] = row_of(rw, 16 * nt + r, kb);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            b.a[mt] = row_of(ra, 16 * mt + r, kb);
+        b.a = row_of(ra, r, kb);
         b.sw = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
             rsw, (int)(kb < kb1 ? 4 * kb : kOutOfRange), 0, 0));
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            b.sa[mt] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-                rsa, (int)(kb < kb1 ? ((16 * mt + r) * kb_n + kb) * 4 : kOutOfRange), 0, 0));
+        b.sa = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+            rsa, (int)(kb < kb1 ? (r * kb_n + kb) * 4 : kOutOfRange), 0, 0));
     };
-    f32x4 acc[MT][NT];
+    f32x4 acc[NT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            acc[mt][nt] = f32x4{};
+    for (int nt = 0; nt < NT; ++nt)
+        acc[nt] = f32x4{};
     Block blk[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
@@ -516,24 +530,20 @@ __global__ __launch_bounds__(64 * W) void block_gemm_rows_kernel(
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             Block& b = blk[u];
+            const float sc = b.sa * b.sw;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nt = 0; nt < NT; ++nt) {
+                const f32x4 p = mfma128(b.w[nt], b.a, f32x4{});
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const f32x4 p = mfma128(b.w[nt], b.a[mt], f32x4{});
-                    const float sc = b.sa[mt] * b.sw;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        acc[mt][nt][i] = __builtin_fmaf(sc, p[i], acc[mt][nt][i]);
-                }
+                for (int i = 0; i < 4; ++i)
+                    acc[nt][i] = __builtin_fmaf(sc, p[i], acc[nt][i]);
+            }
             load(b, kb + kAhead + u);
         }
     }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            *reinterpret_cast<f32x4*>(&part[wave][16 * mt + r][16 * nt + 4 * h]) = acc[mt][nt];
+    for (int nt = 0; nt < NT; ++nt)
+        *reinterpret_cast<f32x4*>(&part[wave][r][16 * nt + 4 * h]) = acc[nt];
     __syncthreads();
     for (int i = tid; i < TM * TN / 4; i += 64 * W) {
         const int m = i / (TN / 4), n = i % (TN / 4) * 4;
@@ -576,37 +586,37 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
         nt = (uint32_t)((N + TN - 1) / TN);
         return launch(kernel, tiles(M_cap, G, N, TM, TN), threads);
     };
-    auto rows = [&](const void* kernel, int TN) {
-        nt = (uint32_t)tiles(M_cap, G, 1, 16, 1);
-        return launch(kernel, tiles(M_cap, G, N, 16, TN), 256);
-    };
     // The choice goes by the rows an expert has on average and by the number of workgroups
     // (256 CUs).  Measured in us, the chosen one first:
-    //   256 x 256, from 192 rows per expert on: 8 experts, 2048 rows x 4096 x 7168: 110, 128 x
-    //     128: 132; 32768 rows: 920, 1096; but 1 expert, 1024 rows x 4096 x 4096 (64 tiles): 52
-    //     against 25.5
+    //   256 x 256, from 192 rows per expert on: 8 experts, 2048 rows x 4096 x 7168: 108, 128 x
+    //     128: 129; 32768 rows: 890, 1100; but 1 expert, 1024 rows x 4096 x 4096 (64 tiles): 49
+    //     against 25
     //   128 x 128, from 12 rows on: two buffers and 4 waves where CUs share workgroups (32
-    //     experts, 2048 rows: 231, 8 waves and four buffers 243), the latter for fewer tiles (3
-    //     experts, 1501 rows x 1352 x 1744: 15.5, 17.7)
-    //   32 x 128 below (32 experts, 128 rows: 156, 128 x 128 164; 1 expert, 200 rows x 4096 x
-    //     7168: 21.7, 33.1)
-    //   rows kernel, for at most a row per expert on average or a few rows and few tiles: 256
-    //     experts, 64 rows x 4096 x 2048: 97, 32 x 128 149; 1 expert, 16 rows x 2112 x 7168:
-    //     14.6, 18.8 (64 rows: 19.4, 8.7); 64 features a workgroup, or 32 to have enough of
-    //     them (1 row x 7168 x 2048: 6.4, 8.7)
+    //     experts, 512 rows: 167, 8 waves and four buffers 172), the latter for fewer tiles (3
+    //     experts, 1501 rows x 1352 x 1744: 15.5, 17.7); against 32 x 128: 8 experts, 256 rows x
+    //     7168 x 2048: 27, 32
+    //   rows kernel, for up to 16 rows per expert and few tiles: 1 expert, 16 rows x 2112 x 7168:
+    //     14.4, 32 x 128 18.8 (64 rows: 19.2, 8.4); 1 row x 7168 x 2048: 6.2, 7.9; 4 experts'
+    //     rows x 4096 x 7168 (128 tiles) 26.5, 28.6; but 16 rows over 4 experts x 4096 x 4096
+    //     (160 tiles) 20 against 12.9, 64 over 256 x 4096 x 2048 109 against 80
+    //   32 x 128 for the rest (32 experts, 128 rows: 146, 128 x 128 158; 1 expert, 200 rows x
+    //     4096 x 7168: 20.3, 33), four buffers while there is one workgroup per CU (5 experts'
+    //     rows x 4096 x 7168: 30.7, three buffers 35.1)
     if (M_cap >= 192 * (int64_t)G && tiles(M_cap, G, N, 256, 256) >= 192)
         return tile((const void*)block_gemm_tile_kernel<2, 4, 8, 4, 2>, 256, 256, 512);
-    if (M_cap >= 12 * (int64_t)G && tiles(M_cap, G, N, 128, 128) >= 128) {
-        if (tiles(M_cap, G, N, 128, 128) >= 512)
+    const int64_t large = tiles(M_cap, G, N, 128, 128), small = tiles(M_cap, G, N, 32, 128);
+    if (M_cap >= 12 * (int64_t)G && large >= 128) {
+        if (large >= 512)
             return tile((const void*)block_gemm_tile_kernel<2, 2, 4, 4, 2>, 128, 128, 256);
         return tile((const void*)block_gemm_tile_kernel<2, 4, 4, 2, 4>, 128, 128, 512);
     }
-    if (M_cap <= G || (M_cap <= 16 * (int64_t)G && tiles(M_cap, G, N, 32, 128) < 128)) {
-        if (tiles(M_cap, G, N, 16, 64) >= 512)
-            return rows((const void*)block_gemm_rows_kernel<1, 4, 4>, 64);
-        return rows((const void*)block_gemm_rows_kernel<1, 2, 4>, 32);
+    if (M_cap <= 16 * (int64_t)G && small <= 128) {
+        nt = (uint32_t)tiles(M_cap, G, 1, kRowsTM, 1);
+        return launch((const void*)block_gemm_rows_kernel, tiles(M_cap, G, N, kRowsTM, kRowsTN), 64 * kRowsWaves);
     }
-    return tile((const void*)block_gemm_tile_kernel<1, 4, 2, 2, 4>, 32, 128, 256);
+    if (small <= 256)
+        return tile((const void*)block_gemm_tile_kernel<1, 4, 2, 2, 4>, 32, 128, 256);
+    return tile((const void*)block_gemm_tile_kernel<1, 4, 2, 2, 3>, 32, 128, 256);
 }
 
 }  // namespace mxfp4
