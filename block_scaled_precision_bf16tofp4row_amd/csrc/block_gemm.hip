@@ -18,9 +18,9 @@
 // vector cycles beside them, the fragment reads 1536 LDS cycles and the loads 512.  With few
 // rows it is the weights' bytes: 128 rows over 32 experts x 4096 x 7168 take 147 us, 6.4 TB/s.
 //
-// Two kernels.  The tile kernel stages both operands in LDS; the rows kernel reads fragments
-// straight from memory and splits K over its waves, where there are so few tiles that a
-// tile's walk along K is the time.  Buffer loads take the bounds: rows past the expert's and features past N are
+// Two kernels, both with the operands staged in LDS: in the tile kernel all waves share a
+// stage, in the rows kernel the waves split K, where there are so few tiles that a tile's walk
+// along K would be the time.  Buffer loads take the bounds: rows past the expert's and features past N are
 // outside the ranges and read as zero, and a lane whose bytes are past K gets an offset
 // outside every range.
 #include "tiles.h"
@@ -456,19 +456,28 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
 }
 
 // The kernel for few rows and few tiles, where a tile's walk along K would be the time: a
-// workgroup owns 16 tokens x 32 features and its 4 waves share K, each a run of blocks whose
-// operands go from memory straight into the fragments' registers (a lane's two 16-byte chunks
-// of a row; four lanes cover 64 contiguous bytes), kAhead blocks ahead.  The waves' sums meet
-// in LDS and are added in wave order.
-constexpr int kRowsTM = 16, kRowsTN = 32, kRowsWaves = 4;
+// workgroup owns 16 MT tokens x 32 features and its 4 waves share K, each a run of blocks
+// that it loads for itself, kAhead blocks ahead, through a ring of its own in LDS: no wave
+// waits for another before the end.  The waves' sums meet in LDS and are added in wave order.
+// What bounds it is what a CU can load (one expert's 16 rows x 4096 x 7168: 8.5 us; straight
+// into the fragments' registers, 64 bytes of a row at a time, the same took 12.6).
+constexpr int kRowsTN = 32, kRowsWaves = 4;
 
+template <int MT>
 __global__ __launch_bounds__(64 * kRowsWaves) void block_gemm_rows_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
     const float* __restrict__ sw, uint16_t* __restrict__ y, const int32_t* __restrict__ offs, int G, int64_t N,
     int64_t K, uint32_t ntm)
 {
-    constexpr int TM = kRowsTM, TN = kRowsTN, W = kRowsWaves, NT = TN / 16, kAhead = 3;
+    constexpr int TM = 16 * MT, TN = kRowsTN, W = kRowsWaves, NT = TN / 16, kAhead = 4;
     constexpr int kRow = TN + 4;                  // floats of a token's row in LDS
+    constexpr int kStage = (TM + TN) * kBK, kBuf = kStage + 512;          // operands; token scales, the weights'
+    constexpr int kLoads = (TM + TN) / 8 + 2;     // of a block
+    // separate arrays: what is loaded into one does not hold up reads of another
+    __shared__ __attribute__((aligned(16))) uint8_t lds0[W * kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds1[W * kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds2[W * kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds3[W * kBuf];
     __shared__ __attribute__((aligned(16))) float part[W][TM][kRow];
 
     const int tid = threadIdx.x;
@@ -494,56 +503,72 @@ __global__ __launch_bounds__(64 * kRowsWaves) void block_gemm_rows_kernel(
     const __amdgpu_buffer_rsrc_t rsa = strip_rsrc(sa + row0 * kb_n, (uint64_t)rows * kb_n * 4);
     const __amdgpu_buffer_rsrc_t rsw = strip_rsrc(sw + ((int64_t)g * nb_n + n0 / 128) * kb_n, (uint64_t)kb_n * 4);
 
-    struct Block {
-        i32x8 w[NT], a;
-        float sa, sw;
-    };
-    auto chunk = [&](__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t k) {
-        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             rs, (int)(k < (uint32_t)K ? off + k : kOutOfRange), 0, 0));
-    };
-    auto row_of = [&](__amdgpu_buffer_rsrc_t rs, uint32_t row, uint32_t kb) {
+    // as in the tile kernel: a load fills 8 rows, lane L row L / 8 and LDS chunk L % 8 of them
+    const uint32_t lrow = (uint32_t)(lane >> 3), lc = (uint32_t)(lane & 7);
+    const uint32_t even = 16 * (lc ^ h), odd = 16 * (lc ^ (4 + h));       // chunks of load 0, 2, .. and 1, 3, ..
+    const uint32_t c0 = 16 * (h ^ ((r >> 1) & 7)), c1 = 16 * ((4 + h) ^ ((r >> 1) & 7));
+    auto load = [&](uint8_t* to, uint32_t kb) {
         // (a block of another wave's run, or past the last, reads nothing)
-        const uint32_t k = kb < kb1 ? kb * kBK + 16 * h : kOutOfRange;
-        const u32x4 v0 = chunk(rs, row * (uint32_t)K, k), v1 = chunk(rs, row * (uint32_t)K, k + 64);
-        return i32x8{(int)v0.x, (int)v0.y, (int)v0.z, (int)v0.w, (int)v1.x, (int)v1.y, (int)v1.z, (int)v1.w};
+        const uint32_t k0 = kb < kb1 ? kb * kBK : kOutOfRange;
+        const uint32_t oe = even + k0 < (uint32_t)K ? lrow * (uint32_t)K + even : kOutOfRange;
+        const uint32_t oo = odd + k0 < (uint32_t)K ? lrow * (uint32_t)K + odd : kOutOfRange;
+        const uint32_t kc = kb < kb1 ? k0 : 0;
+#pragma unroll
+        for (int i = 0; i < (TM + TN) / 8; ++i) {
+            const bool tok = i < TM / 8;
+            const uint32_t first = 8 * (tok ? i : i - TM / 8);
+            load16_to_lds(tok ? ra : rw, to + 8 * i * kBK, (i & 1 ? oo : oe) + first * (uint32_t)K, kc);
+        }
+        const uint32_t slot = (uint32_t)lane;     // (slots past TM are not read)
+        load4_to_lds(rsa, to + kStage, kb < kb1 ? (slot * kb_n + kb) * 4 : kOutOfRange);
+        load4_to_lds(rsw, to + kStage + 256, kb < kb1 ? 4 * kb : kOutOfRange);
     };
-    auto load = [&](Block& b, uint32_t kb) {
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-            b.w[nt] = row_of(rw, 16 * nt + r, kb);
-        b.a = row_of(ra, r, kb);
-        b.sw = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-            rsw, (int)(kb < kb1 ? 4 * kb : kOutOfRange), 0, 0));
-        b.sa = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
-            rsa, (int)(kb < kb1 ? (r * kb_n + kb) * 4 : kOutOfRange), 0, 0));
-    };
-    f32x4 acc[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        acc[nt] = f32x4{};
-    Block blk[kAhead];
+            acc[mt][nt] = f32x4{};
+    uint8_t* const buf[kAhead] = {lds0 + wave * kBuf, lds1 + wave * kBuf, lds2 + wave * kBuf, lds3 + wave * kBuf};
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-        load(blk[u], kb0 + u);
+        load(buf[u], kb0 + u);
     for (uint32_t kb = kb0; kb < kb1; kb += kAhead) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            Block& b = blk[u];
-            const float sc = b.sa * b.sw;
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(vmcnt_at_most((kAhead - 1) * kLoads));
+            asm volatile("" ::: "memory");
+            i32x8 fw[NT], fa[MT];
+            float sc[MT];
+            const float* const scales = reinterpret_cast<const float*>(buf[u] + kStage);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const f32x4 p = mfma128(b.w[nt], b.a, f32x4{});
+            for (int nt = 0; nt < NT; ++nt)
+                fw[nt] = frag(buf[u] + (TM + 16 * nt + r) * kBK, c0, c1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[nt][i] = __builtin_fmaf(sc, p[i], acc[nt][i]);
+            for (int mt = 0; mt < MT; ++mt) {
+                fa[mt] = frag(buf[u] + (16 * mt + r) * kBK, c0, c1);
+                sc[mt] = scales[16 * mt + r] * scales[64];
             }
-            load(b, kb + kAhead + u);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");             // all of it is in registers
+            load(buf[u], kb + kAhead + u);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const f32x4 p = mfma128(fw[nt], fa[mt], f32x4{});
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[mt][nt][i] = __builtin_fmaf(sc[mt], p[i], acc[mt][nt][i]);
+                }
         }
     }
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0));  // no load into LDS is left
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<f32x4*>(&part[wave][r][16 * nt + 4 * h]) = acc[nt];
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            *reinterpret_cast<f32x4*>(&part[wave][16 * mt + r][16 * nt + 4 * h]) = acc[mt][nt];
     __syncthreads();
     for (int i = tid; i < TM * TN / 4; i += 64 * W) {
         const int m = i / (TN / 4), n = i % (TN / 4) * 4;
@@ -586,8 +611,14 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
         nt = (uint32_t)((N + TN - 1) / TN);
         return launch(kernel, tiles(M_cap, G, N, TM, TN), threads);
     };
-    // The choice goes by the rows an expert has on average and by the number of workgroups
-    // (256 CUs).  Measured in us, the chosen one first:
+    // The choice goes by the number of workgroups (256 CUs) and the rows an expert has on
+    // average.  Measured in us, the chosen one first:
+    //   rows kernel, where its workgroups are so few that each has a CU, or nearly, with 16
+    //     tokens or 32: one expert's 16 rows x 2112 x 7168 (132 workgroups): 8.5, 32 x 128 18.9;
+    //     32 rows x 4096 x 7168: 11.1 with 32 tokens, 15.0 with 16, 32 x 128 19.2; 48 rows (512):
+    //     15.3 with 16, 17.1 with 32, 32 x 128 19.1; 1 row x 7168 x 2048: 5.8, 7.8; 64 rows over
+    //     16 experts x 512 x 4096 8.8, 12.5; but 16 rows over 4 x 4096 x 4096 (640) 15.1 against
+    //     12.8, one expert's 32 rows x 8192 x 7168 30.4 against 19.4
     //   256 x 256, from 192 rows per expert on: 8 experts, 2048 rows x 4096 x 7168: 108, 128 x
     //     128: 129; 32768 rows: 890, 1100; but 1 expert, 1024 rows x 4096 x 4096 (64 tiles): 49
     //     against 25
@@ -595,26 +626,27 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
     //     experts, 512 rows: 167, 8 waves and four buffers 172), the latter for fewer tiles (3
     //     experts, 1501 rows x 1352 x 1744: 15.5, 17.7); against 32 x 128: 8 experts, 256 rows x
     //     7168 x 2048: 27, 32
-    //   rows kernel, for up to 16 rows per expert and few tiles: 1 expert, 16 rows x 2112 x 7168:
-    //     14.4, 32 x 128 18.8 (64 rows: 19.2, 8.4); 1 row x 7168 x 2048: 6.2, 7.9; 4 experts'
-    //     rows x 4096 x 7168 (128 tiles) 26.5, 28.6; but 16 rows over 4 experts x 4096 x 4096
-    //     (160 tiles) 20 against 12.9, 64 over 256 x 4096 x 2048 109 against 80
     //   32 x 128 for the rest (32 experts, 128 rows: 146, 128 x 128 158; 1 expert, 200 rows x
     //     4096 x 7168: 20.3, 33), four buffers while there is one workgroup per CU (5 experts'
     //     rows x 4096 x 7168: 30.7, three buffers 35.1)
+    const int64_t rows16 = tiles(M_cap, G, N, 16, kRowsTN), rows32 = tiles(M_cap, G, N, 32, kRowsTN);
+    if (rows16 <= 320 || (rows16 <= 512 && rows32 > 320)) {
+        nt = (uint32_t)tiles(M_cap, G, 1, 16, 1);
+        return launch((const void*)block_gemm_rows_kernel<1>, rows16, 64 * kRowsWaves);
+    }
+    if (rows32 <= 320) {
+        nt = (uint32_t)tiles(M_cap, G, 1, 32, 1);
+        return launch((const void*)block_gemm_rows_kernel<2>, rows32, 64 * kRowsWaves);
+    }
     if (M_cap >= 192 * (int64_t)G && tiles(M_cap, G, N, 256, 256) >= 192)
         return tile((const void*)block_gemm_tile_kernel<2, 4, 8, 4, 2>, 256, 256, 512);
-    const int64_t large = tiles(M_cap, G, N, 128, 128), small = tiles(M_cap, G, N, 32, 128);
+    const int64_t large = tiles(M_cap, G, N, 128, 128);
     if (M_cap >= 12 * (int64_t)G && large >= 128) {
         if (large >= 512)
             return tile((const void*)block_gemm_tile_kernel<2, 2, 4, 4, 2>, 128, 128, 256);
         return tile((const void*)block_gemm_tile_kernel<2, 4, 4, 2, 4>, 128, 128, 512);
     }
-    if (M_cap <= 16 * (int64_t)G && small <= 128) {
-        nt = (uint32_t)tiles(M_cap, G, 1, kRowsTM, 1);
-        return launch((const void*)block_gemm_rows_kernel, tiles(M_cap, G, N, kRowsTM, kRowsTN), 64 * kRowsWaves);
-    }
-    if (small <= 256)
+    if (tiles(M_cap, G, N, 32, 128) <= 256)
         return tile((const void*)block_gemm_tile_kernel<1, 4, 2, 2, 4>, 32, 128, 256);
     return tile((const void*)block_gemm_tile_kernel<1, 4, 2, 2, 3>, 32, 128, 256);
 }

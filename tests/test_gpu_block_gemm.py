@@ -76,6 +76,31 @@ def test_every_kernel(counts, N, K):
     check(counts, N, K, seed=N)
 
 
+@pytest.mark.parametrize("K", [16, 144, 272, 400, 528])
+@pytest.mark.parametrize("counts,N", [
+    ([16, 0, 5], 1032),                           # waves that share K, 16 tokens
+    ([121], 2040),                                # the same, 32 tokens
+    ([17, 0, 13], 4104),                          # 32 x 128, one workgroup per CU
+    ([3, 0, 9, 1, 0, 33, 2, 5], 4104),            # 32 x 128, several
+    ([100, 0, 130], 4104),                        # 128 x 128, one workgroup per CU
+    ([50, 51, 49, 0, 64, 1, 100, 85], 8200),      # 128 x 128, several
+    ([500, 3], 12296),                            # 256 x 256
+])
+def test_every_kernel_at_every_stage_count(counts, N, K):
+    """One to five blocks of K, the last one partial: fewer and more than a kernel's buffers."""
+    check(counts, N, K, seed=K + N)
+
+
+@pytest.mark.parametrize("counts,N,K", [
+    ([9, 8], 4104, 4096),
+    ([1, 0, 2, 1, 0, 1, 1, 1] * 12, 264, 4096),   # 32 x 128, several workgroups per CU
+    ([5], 520, 7184), ([40], 2048, 8192),
+])
+def test_deep(counts, N, K):
+    """Rows a multiple of 4096 bytes apart, whose blocks are taken in turned order, and others."""
+    check(counts, N, K, seed=N)
+
+
 @pytest.mark.parametrize("M", [1, 2, 8, 15, 31, 32, 33, 47, 48, 96, 192, 255, 256, 320])
 def test_row_counts(M):
     check([M], 384, 512, slack=0, seed=M)
