@@ -121,15 +121,16 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(
     const int64_t t = at.t;
     const uint32_t lane = at.lane;                // its lowest 3 bits are the hardware lane's
     const int64_t e0 = 16 * (int64_t)lane;
-    // (lanes without elements stay for the exchange)
-    const bool in = t < n_tokens && (!kInPlace || t < offs[G]) && e0 < K;       // K is a multiple of 16
+    const bool here = t < n_tokens && (!kInPlace || t < offs[G]);
+    const bool in = here && e0 < K;               // K is a multiple of 16
     u32x4 v0 = {0, 0, 0, 0}, v1 = {0, 0, 0, 0};
     if (in) {
         const u32x4* const p = reinterpret_cast<const u32x4*>(x + t * K + e0);
         v0 = load_stream(p);
         v1 = load_stream(p + 1);
     }
-    if (!kWhole || in) {
+    // (lanes past the row's end stay: those of its last block exchange with them)
+    if (!kWhole || here) {
         const int n = kInPlace ? 1 : k;
         if (kFp4) {
             uint32_t m = max(mag_max8(v0), mag_max8(v1));
@@ -137,8 +138,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(
             const int s = max((int)(m >> 7) - 2, 0);
             const u32x2 codes = {fp4_of8(v0, s), fp4_of8(v1, s)};
             for (int j = 0; j < n; ++j) {
-                const int64_t row = !in ? -1 : kInPlace ? t : (int64_t)pos[t * k + j];
-                if (row < 0 || row >= M_cap)
+                const int64_t row = !here ? -1 : kInPlace ? t : (int64_t)pos[t * k + j];
+                if (!in || row < 0 || row >= M_cap)
                     continue;
                 store_stream(reinterpret_cast<u32x2*>(y + (row * K + e0) / 2), codes);
                 if (!(lane & 1))
@@ -148,8 +149,8 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(
             const Fp8Lane q = fp8_lane(v0, v1);
             const int64_t kb = (K + 127) / 128;
             for (int j = 0; j < n; ++j) {
-                const int64_t row = !in ? -1 : kInPlace ? t : (int64_t)pos[t * k + j];
-                if (row < 0 || row >= M_cap)
+                const int64_t row = !here ? -1 : kInPlace ? t : (int64_t)pos[t * k + j];
+                if (!in || row < 0 || row >= M_cap)
                     continue;
                 store_stream(reinterpret_cast<u32x4*>(y + row * K + e0), q.bytes);
                 if (!(lane & 7))

@@ -145,6 +145,15 @@ def test_dispatch_mxfp4(T, k, E, K, wide):
     assert (codes[n:] == 0xA5).all() and (sc[n:] == 0xA5).all()
 
 
+@pytest.mark.parametrize("K", [912, 928, 944, 960, 976, 992, 1008, 1936, 3024, 7152])
+def test_partial_last_block_of_whole_waves(K):
+    """Rows whose blocks fill whole waves and whose last block is partial: its lanes without
+    elements take part in the block's maximum."""
+    test_dispatch_fp8(37, 3, 8, K, False)
+    if K % 32 == 0:
+        test_dispatch_mxfp4(37, 3, 8, K, False)
+
+
 def test_positions_outside_the_output_are_skipped():
     T, k, K, cap = 4, 3, 128, 5
     pos = torch.tensor([[0, 5, -7], [2 ** 31 - 1, -2 ** 31, 1], [2, 6, 3], [-1, -1, 4]], dtype=torch.int32).cuda()
