@@ -459,8 +459,8 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
 // workgroup owns 16 MT tokens x 32 features and its 4 waves share K, each a run of blocks
 // that it loads for itself, kAhead blocks ahead, through a ring of its own in LDS: no wave
 // waits for another before the end.  The waves' sums meet in LDS and are added in wave order.
-// What bounds it is what a CU can load (one expert's 16 rows x 4096 x 7168: 8.5 us; straight
-// into the fragments' registers, 64 bytes of a row at a time, the same took 12.6).
+// What bounds it is what a CU can load (one expert's 16 rows x 2112 x 7168: 8.5 us; straight
+// into the fragments' registers, 64 bytes of a row at a time, the same took 14.4).
 constexpr int kRowsTN = 32, kRowsWaves = 4;
 
 template <int MT>
@@ -586,11 +586,12 @@ __global__ __launch_bounds__(64 * kRowsWaves) void block_gemm_rows_kernel(
 
 namespace {
 
-// Workgroups of TM x TN tiles that a call can need: every token tile holds a row.
+// Workgroups of TM x TN tiles that a call can need: m rows make at most (m + TM - 1) / TM
+// token tiles, and at most min(G, M_cap) experts have rows.
 int64_t tiles(int64_t M_cap, int32_t G, int64_t N, int TM, int TN)
 {
-    const int64_t mt = (M_cap + TM - 1) / TM + G;
-    return (mt < M_cap ? mt : M_cap) * ((N + TN - 1) / TN);
+    const int64_t live = G < M_cap ? G : M_cap;
+    return (M_cap + live * (TM - 1)) / TM * ((N + TN - 1) / TN);
 }
 
 }  // namespace
@@ -613,24 +614,25 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
     };
     // The choice goes by the number of workgroups (256 CUs) and the rows an expert has on
     // average.  Measured in us, the chosen one first:
-    //   rows kernel, where its workgroups are so few that each has a CU, or nearly, with 16
-    //     tokens or 32: one expert's 16 rows x 2112 x 7168 (132 workgroups): 8.5, 32 x 128 18.9;
-    //     32 rows x 4096 x 7168: 11.1 with 32 tokens, 15.0 with 16, 32 x 128 19.2; 48 rows (512):
-    //     15.3 with 16, 17.1 with 32, 32 x 128 19.1; 1 row x 7168 x 2048: 5.8, 7.8; 64 rows over
-    //     16 experts x 512 x 4096 8.8, 12.5; but 16 rows over 4 x 4096 x 4096 (640) 15.1 against
-    //     12.8, one expert's 32 rows x 8192 x 7168 30.4 against 19.4
+    //   rows kernel, where each of its workgroups has a CU, or nearly, with 16 tokens or 32: one
+    //     expert's 16 rows x 4096 x 7168: 8.8 with 16, 9.5 with 32, 32 x 128 18.8; 32 rows: 9.1,
+    //     11.0, 19.0; 64 rows: 11.2 with 32, 15.6 with 16, 32 x 128 19.3; 1 row x 7168 x 2048:
+    //     5.8, 7.8; 64 rows over 16 experts x 512 x 4096: 8.7, 12.5; and up to two workgroups of
+    //     16 tokens per CU if K is long: 8 rows x 16384 x 7168 25.9, 30.2, but 8 rows x 16384 x
+    //     4096 14.8 against 13.0
     //   256 x 256, from 192 rows per expert on: 8 experts, 2048 rows x 4096 x 7168: 108, 128 x
     //     128: 129; 32768 rows: 890, 1100; but 1 expert, 1024 rows x 4096 x 4096 (64 tiles): 49
     //     against 25
-    //   128 x 128, from 12 rows on: two buffers and 4 waves where CUs share workgroups (32
-    //     experts, 512 rows: 167, 8 waves and four buffers 172), the latter for fewer tiles (3
-    //     experts, 1501 rows x 1352 x 1744: 15.5, 17.7); against 32 x 128: 8 experts, 256 rows x
+    //   128 x 128, from 12 rows on: two buffers and 4 waves where CUs share workgroups (8
+    //     experts, 256 rows x 7168 x 2048, 504 of them: 27, 8 waves and four buffers 29), the
+    //     latter for fewer tiles (8 experts, 512 rows x 4096 x 7168, 352: 61.6, 68.5; 3 experts,
+    //     1501 rows x 1352 x 1744, 154: 15.5, 17.7); against 32 x 128: 8 experts, 256 rows x
     //     7168 x 2048: 27, 32
     //   32 x 128 for the rest (32 experts, 128 rows: 146, 128 x 128 158; 1 expert, 200 rows x
     //     4096 x 7168: 20.3, 33), four buffers while there is one workgroup per CU (5 experts'
     //     rows x 4096 x 7168: 30.7, three buffers 35.1)
     const int64_t rows16 = tiles(M_cap, G, N, 16, kRowsTN), rows32 = tiles(M_cap, G, N, 32, kRowsTN);
-    if (rows16 <= 320 || (rows16 <= 512 && rows32 > 320)) {
+    if (rows16 <= 320 || (rows16 <= 512 && rows32 > 320 && K > 4096)) {
         nt = (uint32_t)tiles(M_cap, G, 1, 16, 1);
         return launch((const void*)block_gemm_rows_kernel<1>, rows16, 64 * kRowsWaves);
     }
@@ -642,7 +644,7 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
         return tile((const void*)block_gemm_tile_kernel<2, 4, 8, 4, 2>, 256, 256, 512);
     const int64_t large = tiles(M_cap, G, N, 128, 128);
     if (M_cap >= 12 * (int64_t)G && large >= 128) {
-        if (large >= 512)
+        if (large >= 448)
             return tile((const void*)block_gemm_tile_kernel<2, 2, 4, 4, 2>, 128, 128, 256);
         return tile((const void*)block_gemm_tile_kernel<2, 4, 4, 2, 4>, 128, 128, 512);
     }

@@ -84,7 +84,8 @@ def test_every_kernel(counts, N, K):
     ([3, 0, 9, 1, 0, 33, 2, 5], 4104),            # 32 x 128, several
     ([100, 0, 130], 4104),                        # 128 x 128, one workgroup per CU
     ([50, 51, 49, 0, 64, 1, 100, 85], 8200),      # 128 x 128, several
-    ([500, 3], 12296),                            # 256 x 256
+    ([500, 3], 12296),
+    ([900, 3], 12296),                            # 256 x 256
 ])
 def test_every_kernel_at_every_stage_count(counts, N, K):
     """One to five blocks of K, the last one partial: fewer and more than a kernel's buffers."""
@@ -93,6 +94,7 @@ def test_every_kernel_at_every_stage_count(counts, N, K):
 
 @pytest.mark.parametrize("counts,N,K", [
     ([9, 8], 4104, 4096),
+    ([9, 8, 7], 4104, 4096),                      # 32 x 128, one per CU
     ([1, 0, 2, 1, 0, 1, 1, 1] * 12, 264, 4096),   # 32 x 128, several workgroups per CU
     ([5], 520, 7184), ([40], 2048, 8192),
 ])
