@@ -80,7 +80,7 @@ __device__ __forceinline__ void meet()
 template <int D>
 struct TileCtx {
     uint8_t* buf[D];                              // the LDS stage buffers
-    float* scl;                                   // staged token scales: [2 pairs][2 stages][slots]
+    uint8_t* late[2];                             // with two: the rows of the later half of the tokens
     __amdgpu_buffer_rsrc_t ra, rw, rsa, rsw;      // operand rows, token and weight scales
     uint32_t abase, wbase, ac0, ac1, wc0, wc1, K; // loader: row offsets and the two chunk offsets of each
     uint32_t lds_a, lds_w, lds_s;                 // loader: LDS offsets of the wave's first rows, scale slots
@@ -95,7 +95,6 @@ template <int WM, int WN, int MT, int NT, int D>
 struct Tile {
     static constexpr int TM = 16 * MT * WM, TN = 16 * NT * WN;
     static constexpr int kWaves = WM * WN;
-    static constexpr int kStage = (TM + TN) * kBK;
     static constexpr int kLoadsA = TM / 8 / kWaves, kLoadsW = TN / 8 / kWaves;   // 8-row loads of a wave
     static constexpr int kSlots = 64 * kWaves;              // scale slots (those past TM are not read)
     static constexpr int kTiles = MT * NT;
@@ -105,18 +104,28 @@ struct Tile {
     // 128 experts x 4096 x 4096: 138 us, 160 all from the start; at 7168 deep it would cost 5 %).
     static constexpr bool kTurn = TM == 32;
     static constexpr int kLag = 3;                          // products in flight before their scaled add
-    // Scales: with two buffers, those of two stages at a time go through registers to LDS
-    // (half the requests); with more, each stage's go into its buffer with the operands, a
-    // wave's token slots and then its weights' scale, so that no register waits for memory
-    // over several stages.
-    static constexpr bool kDmaScales = D > 2;
-    static constexpr int kBuf = kStage + (kDmaScales ? 8 * kSlots : 0);
-    // While stage s + 1 is awaited, the loads of stages s + 2 .. s + D - 1 may be in flight.
-    static constexpr int kInFlight = (D - 2) * (kLoadsA + kLoadsW + 2);
+    static constexpr int kLoads = kLoadsA + kLoadsW + 2;
+    // With two buffers, the earlier half of each wave's token tiles, the weights and the scales
+    // of a later stage are loaded from the middle of a stage on, as soon as this stage's are in
+    // registers; the rest after the stage's barrier, as all of it with more buffers.
+    static constexpr bool kHalves = D == 2;
+    // A buffer: token rows (the early ones), weights' rows, then a wave's token scales and its
+    // weights' scale.
+    static constexpr int kTok = kHalves ? TM / 2 : TM;
+    static constexpr int kScales = (kTok + TN) * kBK;
+    static constexpr int kBuf = kScales + 8 * kSlots;
+    static constexpr int kLate = kHalves ? TM / 2 * kBK : 0;
+    static constexpr int kEarlyOps = kHalves ? kLoadsW + kLoadsA / 2 : 0;
+    // While stage s + 1 is awaited, the loads of later stages may be in flight: s + 2's early
+    // ones, or all of s + 2 .. s + D - 1.
+    static constexpr int kInFlight = kHalves ? kEarlyOps + 2 : (D - 2) * kLoads;
     static_assert(D >= 2 && D <= 4, "stage buffers");
     static_assert(TM % (8 * kWaves) == 0 && TN % (8 * kWaves) == 0 && TM <= kSlots, "loads");
     static_assert(TN % 128 == 0 && 128 % (16 * NT) == 0, "a wave's features lie in one scale block");
-    static_assert(2 * kStage >= TM * TN * 2, "the epilogue stages the tile in two buffers");
+    // The epilogue's place for a row of the tile: half the rows per buffer, of two buffers.
+    static constexpr int kOutRows = kHalves ? 3 * TM / 8 : TM / 2;        // in the buffer, the others in its late rows
+    static_assert(kBuf >= kOutRows * TN * 2 && (!kHalves || kLate >= (TM / 2 - kOutRows) * TN * 2), "epilogue");
+    static_assert(!kHalves || (MT % 2 == 0 && kLoadsA % 4 == 0 && MT >= 4), "halves");
     static_assert((MT == 2 || MT % 4 == 0) && kTiles % 4 == 0, "scale reads, ring of products");
 
     struct State {
@@ -125,13 +134,8 @@ struct Tile {
         i32x8 fw[NT], fa[2];
         float raw[MT], sc[MT];                    // next and present token scales (sc: times the weights')
         float wsc[D];                             // the weights' scale of the stages
-        float ld[D];                              // token scales on their way to LDS
     };
 
-    static __device__ __forceinline__ float load_f32(__amdgpu_buffer_rsrc_t r, uint32_t off)
-    {
-        return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
-    }
     // The block of K that stage s takes.
     static __device__ __forceinline__ uint32_t block_of(const TileCtx<D>& cx, uint32_t s)
     {
@@ -140,65 +144,46 @@ struct Tile {
         const uint32_t b = s + cx.turn;
         return s < cx.blocks ? b < cx.blocks ? b : b - cx.blocks : cx.blocks;
     }
-    // Part `part` of NT of the operand loads of stage s into buffer b = s % D.  Offsets are
-    // made here, from registers that live across the stages; a stage past the last reads
-    // nothing (its columns are past K).
-    static __device__ __forceinline__ void issue_operands(const TileCtx<D>& cx, int b, uint32_t s, int part)
+    // Operand loads `from` .. `to` - 1 of stage s into buffer b = s % D, the weights' first, then
+    // the tokens'.  Offsets are made here, from registers that live across the stages; a stage
+    // past the last reads nothing (its columns are past K).
+    static __device__ __forceinline__ void issue_operands(const TileCtx<D>& cx, int b, uint32_t s, int from, int to)
     {
         const uint32_t k0 = block_of(cx, s) * kBK;
 #pragma unroll
-        for (int j = part * (kLoadsA + kLoadsW) / NT; j < (part + 1) * (kLoadsA + kLoadsW) / NT; ++j) {
-            const bool tok = j < kLoadsA;
-            const int i = tok ? j : j - kLoadsA;
+        for (int j = from; j < to; ++j) {
+            const bool tok = j >= kLoadsW;
+            const int i = tok ? j - kLoadsW : j;
+            const int half = tok && kHalves ? i / (kLoadsA / 2) : 0, in_half = tok && kHalves ? i % (kLoadsA / 2) : i;
+            const int rows = 8 * (in_half + half * MT);
+            uint8_t* const to_buf = half ? cx.late[b] : cx.buf[b];
             const uint32_t c = tok ? (i & 1 ? cx.ac1 : cx.ac0) : (i & 1 ? cx.wc1 : cx.wc0);
             const uint32_t off = c + k0 < cx.K ? (tok ? cx.abase : cx.wbase) + c : kOutOfRange;
-            load16_to_lds(tok ? cx.ra : cx.rw, cx.buf[b] + (tok ? cx.lds_a : cx.lds_w) + 8 * i * kBK,
-                          off + 8u * i * cx.K, k0);
+            load16_to_lds(tok ? cx.ra : cx.rw, to_buf + (tok ? cx.lds_a : cx.lds_w) + 8 * in_half * kBK,
+                          off + (uint32_t)rows * cx.K, k0);
         }
     }
     // Its scales.
-    static __device__ __forceinline__ void issue_scales(const TileCtx<D>& cx, State& t, int b, uint32_t s)
+    static __device__ __forceinline__ void issue_scales(const TileCtx<D>& cx, int b, uint32_t s)
     {
-        if constexpr (kDmaScales) {
-            const uint32_t kb = block_of(cx, s);
-            uint8_t* const to = cx.buf[b] + kStage + cx.lds_s;
-            load4_to_lds(cx.rsa, to, kb * kBK < cx.K ? cx.srow + 4 * kb : kOutOfRange);
-            load4_to_lds(cx.rsw, to + 4 * kSlots, 4 * kb);
-            return;
-        }
-        const uint32_t k0 = s * kBK;
-        t.wsc[b] = load_f32(cx.rsw, 4 * s);
-        if (b % 2 == 0) {
-            t.ld[b] = load_f32(cx.rsa, k0 < cx.K ? cx.srow + 4 * s : kOutOfRange);
-            t.ld[b + 1] = load_f32(cx.rsa, k0 + kBK < cx.K ? cx.srow + 4 * s + 4 : kOutOfRange);
-        }
-    }
-    // The token scales of stages s, s + 1 (s even, buffer b) to LDS.
-    static __device__ __forceinline__ void store_scales(const TileCtx<D>& cx, const State& t, int b, uint32_t s)
-    {
-        float* const to = cx.scl + (s & 2) * kSlots + cx.sslot;
-        to[0] = t.ld[b];
-        to[kSlots] = t.ld[b + 1];
+        const uint32_t kb = block_of(cx, s);
+        uint8_t* const to = cx.buf[b] + kScales + cx.lds_s;
+        load4_to_lds(cx.rsa, to, kb * kBK < cx.K ? cx.srow + 4 * kb : kOutOfRange);
+        load4_to_lds(cx.rsw, to + 4 * kSlots, 4 * kb);
     }
     // The scales of stage s (buffer b).
-    static __device__ __forceinline__ void read_scales(const TileCtx<D>& cx, State& t, int b, uint32_t s)
+    static __device__ __forceinline__ void read_scales(const TileCtx<D>& cx, State& t, int b)
     {
-        if constexpr (kDmaScales) {
-            const float* const from = reinterpret_cast<const float*>(cx.buf[b] + kStage);
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-                t.raw[i] = from[cx.scl_at + i];
-            t.wsc[b] = from[kSlots + cx.sslot];
-            return;
-        }
-        const float* const from = cx.scl + (s & 3) * kSlots + cx.scl_at;
+        const float* const from = reinterpret_cast<const float*>(cx.buf[b] + kScales);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-            t.raw[i] = from[i];
+            t.raw[i] = from[cx.scl_at + i];
+        t.wsc[b] = from[kSlots + cx.sslot];
     }
     static __device__ __forceinline__ i32x8 token_frag(const TileCtx<D>& cx, int b, int mt)
     {
-        return frag(cx.buf[b] + cx.arow + 16 * mt * kBK, cx.c0, cx.c1);
+        const uint8_t* const from = kHalves && mt >= MT / 2 ? cx.late[b] : cx.buf[b];
+        return frag(from + cx.arow + 16 * (kHalves ? mt % (MT / 2) : mt) * kBK, cx.c0, cx.c1);
     }
     static __device__ __forceinline__ i32x8 weight_frag(const TileCtx<D>& cx, int b, int nt)
     {
@@ -213,17 +198,22 @@ struct Tile {
         for (int e = 0; e < 4; ++e)
             t.acc[mt][nt][e] = __builtin_fmaf(t.sc[mt], t.p[i & 3][e], t.acc[mt][nt][e]);
     }
-    // Products I .. END - 1, each followed by the scaled add of the one kLag before it, in
-    // this order (the scheduler would put dependent ones together).  In the stage's last
-    // token tile a weight fragment is replaced by the next stage's (buffer b) after its use.
+    // Products I .. END - 1 of the stage in buffer b, each followed by the scaled add of the one
+    // kLag before it, in this order (the scheduler would put dependent ones together), and by
+    // loads of stage s into this buffer, where they are due.  In the stage's last token tile a
+    // weight fragment is replaced by the next stage's after its use.
     template <int I, int END>
     static __device__ __forceinline__ void products(const TileCtx<D>& cx, State& t, int b, uint32_t s)
     {
         if constexpr (I < END) {
-            t.p[I & 3] = mfma128(t.fw[I % NT], t.fa[I / NT % 2], f32x4{});
-            if constexpr (I / NT == MT - 1) {
-                t.fw[I % NT] = weight_frag(cx, b, I % NT);
-                issue_operands(cx, (b + D - 1) % D, s, I % NT);
+            constexpr int mt = I / NT, nt = I % NT, kOps = kLoadsA + kLoadsW;
+            t.p[I & 3] = mfma128(t.fw[nt], t.fa[mt % 2], f32x4{});
+            if constexpr (mt == MT - 1) {
+                t.fw[nt] = weight_frag(cx, (b + 1) % D, nt);
+                issue_operands(cx, b, s, kEarlyOps + nt * (kOps - kEarlyOps) / NT,
+                               kEarlyOps + (nt + 1) * (kOps - kEarlyOps) / NT);
+            } else if constexpr (kHalves && mt == MT / 2) {
+                issue_operands(cx, b, s, nt * kEarlyOps / NT, (nt + 1) * kEarlyOps / NT);
             }
             if constexpr (I >= kLag)
                 add<I - kLag>(t);
@@ -232,13 +222,17 @@ struct Tile {
         }
     }
     template <int M>
-    static __device__ __forceinline__ void token_tiles(const TileCtx<D>& cx, State& t, int b)
+    static __device__ __forceinline__ void token_tiles(const TileCtx<D>& cx, State& t, int b, uint32_t s)
     {
         if constexpr (M < MT - 1) {
+            if constexpr (kHalves && M == MT / 2) {
+                meet();                           // every wave has the weights and half the tokens in registers
+                issue_scales(cx, b, s);
+            }
             t.fa[(M + 1) % 2] = token_frag(cx, b, M + 1);
             __builtin_amdgcn_sched_barrier(0);
-            products<M * NT, (M + 1) * NT>(cx, t, 0, 0);
-            token_tiles<M + 1>(cx, t, b);
+            products<M * NT, (M + 1) * NT>(cx, t, b, s);
+            token_tiles<M + 1>(cx, t, b, s);
         }
     }
     // Stage s in buffer B = s % D.
@@ -252,20 +246,16 @@ struct Tile {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
             t.sc[mt] = t.raw[mt] * t.wsc[B];
-        token_tiles<0>(cx, t, B);
+        token_tiles<0>(cx, t, B, s + D);
         // every fragment of this stage is in registers: wait for the next one's loads, meet
-        // the others, and load a later one into this buffer
+        // the others, and load (the rest of) a later one into this buffer
         __builtin_amdgcn_s_waitcnt(vmcnt_at_most(kInFlight));
-        if (!kDmaScales && B % 2 == 1)
-            store_scales(cx, t, kNext, s + 1);
-        if constexpr (D == 2)
-            __syncthreads();
-        else
-            meet();
+        meet();
         t.fa[0] = token_frag(cx, kNext, 0);
-        read_scales(cx, t, kNext, s + 1);
-        issue_scales(cx, t, B, s + D);
-        products<(MT - 1) * NT, kTiles>(cx, t, kNext, s + D);
+        read_scales(cx, t, kNext);
+        if constexpr (!kHalves)
+            issue_scales(cx, B, s + D);
+        products<(MT - 1) * NT, kTiles>(cx, t, B, s + D);
     }
 };
 
@@ -277,15 +267,17 @@ struct Tile {
 // while the next stage's first fragments are read (a weight fragment right after its last
 // use) and a later stage's loads go out into the buffer just left.  So the barrier never
 // finds a wave without matrix work behind it.  The scaled adds run three products late and
-// the operand loads go out one or two at a time between the last tile's products (256 x 256,
-// 32768 rows x 7168 x 4096: 890-940 us; adds two late 925-960; all loads in a burst behind
-// the barrier as well 970-990).
-// D = 2 for the tiles of 64 KB and 32 KB stages that share a CU or fill it; D = 4 where a CU
-// holds one workgroup with little work per stage, which would wait for memory each time (128
-// x 128, 1024 rows x 4096 x 4096: 25.5 us with 8 waves and D = 4, 26.8 with 4 and D = 2); D =
-// 3 for the 32 x 128 tile where there is more than one per CU: two then fit its LDS, and one
-// works while the other starts or ends (64 rows over 256 experts x 4096 x 2048: 80 us, D = 4
-// 83, D = 2 87; 128 rows over 32 experts x 4096 x 7168: 146, 148, 179).
+// the loads go out one or two at a time between products (256 x 256, 32768 rows x 7168 x
+// 4096: 890-940 us; adds two late 925-960; all loads in a burst behind the barrier as well
+// 970-990; with zeros for operands, which leave the clock at its top, 784).
+// D = 2 for the large tiles, whose buffers fill a CU's LDS or half of it.  A load then has one
+// stage to arrive, so most of them go out half a stage earlier, behind a barrier in the
+// middle: 8 experts, 2048 rows x 4096 x 7168: 102 us (256 x 256), 119 (128 x 128), 106 and 128
+// without that; it costs the largest products nothing and gains them nothing, which the chip's
+// power holds.  For the 32 x 128 tile D = 4 where a CU has one workgroup, which would wait for
+// memory each stage, and D = 3 where there are more: two then fit its LDS, and one works while
+// the other starts or ends (64 rows over 256 experts x 4096 x 2048: 80 us, D = 4 83, D = 2 87;
+// 128 rows over 32 experts x 4096 x 7168: 146, 148, 179).
 template <int WM, int WN, int MT, int NT, int D>
 __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
@@ -297,9 +289,8 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
     // separate arrays: what is loaded into one does not hold up reads of another
     __shared__ __attribute__((aligned(16))) uint8_t lds0[W::kBuf];
     __shared__ __attribute__((aligned(16))) uint8_t lds1[W::kBuf];
-    __shared__ __attribute__((aligned(16))) uint8_t lds2[D > 2 ? W::kBuf : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t lds3[D > 3 ? W::kBuf : 16];
-    __shared__ __attribute__((aligned(16))) float scl[W::kDmaScales ? 4 : 4 * W::kSlots];
+    __shared__ __attribute__((aligned(16))) uint8_t lds2[D > 2 ? W::kBuf : W::kLate];
+    __shared__ __attribute__((aligned(16))) uint8_t lds3[D > 3 ? W::kBuf : W::kHalves ? W::kLate : 16];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -324,11 +315,14 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
     const uint32_t r = (uint32_t)(lane & 15), h = (uint32_t)(lane >> 4);
 
     // loader: instruction i of wave w fills token rows 8 (kLoadsA w + i) .. + 7 (and feature
-    // rows alike); lane L takes row L / 8 of them and LDS chunk L % 8, the row's chunk
+    // rows alike), or with two halves the same of the early rows and of the late ones, each wave
+    // row's MT groups of 8; lane L takes row L / 8 of them and LDS chunk L % 8, the row's chunk
     // (L % 8) ^ ((row >> 1) & 7), which is the same for every other i.  Token scales: slot
     // 64 w + L, which is token tile slot % MT of row slot / MT % 16 of wave row slot / (16 MT)
     const uint32_t l8 = (uint32_t)(lane >> 3), l16 = (uint32_t)(lane >> 4), lc = (uint32_t)(lane & 7);
-    const uint32_t ag = (uint32_t)(W::kLoadsA * wave), wg = (uint32_t)(W::kLoadsW * wave);   // first 8-row groups
+    const uint32_t al = (uint32_t)(W::kLoadsA * wave) / (W::kHalves ? 2 : 1);      // first 8-row groups: in LDS
+    const uint32_t ag = W::kHalves ? 2 * MT * (al / MT) + al % MT : al;            // of the tile
+    const uint32_t wg = (uint32_t)(W::kLoadsW * wave);
     const uint32_t slot = (uint32_t)tid;
     const uint32_t srow = slot / (16 * MT) * (16 * MT) + slot % MT * 16 + slot / MT % 16;
     const uint32_t nb = min((uint32_t)(n0 + 16 * NT * wn) / 128, nb_n - 1);
@@ -339,7 +333,8 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
         cx.buf[2] = lds2;
     if constexpr (D > 3)
         cx.buf[3] = lds3;
-    cx.scl = scl;
+    cx.late[0] = lds2;                            // (of two buffers)
+    cx.late[1] = lds3;
     cx.ra = strip_rsrc(a + row0 * K, (uint64_t)rows * (uint64_t)K);
     cx.rw = strip_rsrc(w + ((int64_t)g * N + n0) * K, (uint64_t)cols * (uint64_t)K);
     cx.rsa = strip_rsrc(sa + row0 * kb_n, (uint64_t)rows * kb_n * 4);
@@ -353,13 +348,13 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
     cx.ac1 = 16 * (lc ^ ((4 * ag + 4 + l16) & 7));
     cx.wc0 = 16 * (lc ^ ((4 * wg + l16) & 7));
     cx.wc1 = 16 * (lc ^ ((4 * wg + 4 + l16) & 7));
-    cx.lds_a = 8 * ag * kBK;
-    cx.lds_w = (TM + 8 * wg) * kBK;
+    cx.lds_a = 8 * al * kBK;
+    cx.lds_w = (W::kTok + 8 * wg) * kBK;
     cx.lds_s = 256 * (uint32_t)wave;
     cx.srow = srow * kb_n * 4;
     cx.sslot = slot;
-    cx.arow = (uint32_t)(16 * MT * wm + r) * kBK;
-    cx.wrow = (uint32_t)(TM + 16 * NT * wn + r) * kBK;
+    cx.arow = (uint32_t)((W::kHalves ? 8 : 16) * MT * wm + r) * kBK;
+    cx.wrow = (uint32_t)(W::kTok + 16 * NT * wn + r) * kBK;
     cx.c0 = 16 * (h ^ ((r >> 1) & 7));
     cx.c1 = 16 * ((4 + h) ^ ((r >> 1) & 7));
     cx.scl_at = (16 * (uint32_t)wm + r) * MT;
@@ -377,22 +372,15 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
         t.p[i] = f32x4{};
 #pragma unroll
     for (int b = 0; b < D; ++b) {
-        W::issue_scales(cx, t, b, b);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            W::issue_operands(cx, b, b, nt);
+        W::issue_scales(cx, b, b);
+        W::issue_operands(cx, b, b, 0, W::kLoadsA + W::kLoadsW);
         __builtin_amdgcn_sched_barrier(0);        // (the waits count the loads in this order)
     }
-    // with scales in registers everything is awaited: loads into LDS and loads into registers
-    // do not return in one order (measured: counting over both let a stage start early), so
-    // only a kernel whose loads all go to LDS may wait by count
-    __builtin_amdgcn_s_waitcnt(vmcnt_at_most(W::kDmaScales ? W::kInFlight + W::kLoadsA + W::kLoadsW + 2 : 0));
-    if constexpr (!W::kDmaScales) {
-        asm volatile("" : "+v"(t.wsc[0]), "+v"(t.wsc[1]));   // loaded by now, not in the loop's way
-        W::store_scales(cx, t, 0, 0);
-    }
+    // (only loads into LDS are counted: those into registers do not return in one order with
+    // them; measured: counting over both let a stage start early)
+    __builtin_amdgcn_s_waitcnt(vmcnt_at_most((D - 1) * W::kLoads));
     meet();
-    W::read_scales(cx, t, 0, 0);
+    W::read_scales(cx, t, 0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
         t.fw[nt] = W::weight_frag(cx, 0, nt);
@@ -425,6 +413,12 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
     // epilogue through LDS: lane (r, h) of tile (mt, nt) holds token 16 (MT wm + mt) + r and
     // features 16 (NT wn + nt) + 4 h + (0..3); a token's row is 2 TN bytes there with 16-byte
     // chunk c at chunk c ^ (token % 16), then whole row segments go out, 16 bytes a lane
+    auto place = [&](uint32_t row) {
+        const uint32_t in = row % (TM / 2);
+        if (in < (uint32_t)W::kOutRows)
+            return (row < TM / 2 ? lds0 : lds1) + in * (2 * TN);
+        return (row < TM / 2 ? lds2 : lds3) + (in - W::kOutRows) * (2 * TN);
+    };
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0));  // no load into LDS is left
     __syncthreads();
 #pragma unroll
@@ -436,8 +430,7 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
             const bf16x2 p1 = {(__bf16)v[2], (__bf16)v[3]};
             const uint32_t c = (uint32_t)(2 * (NT * wn + nt)) + (h >> 1);
             const uint32_t row = (uint32_t)(16 * (MT * wm + mt)) + r;
-            *reinterpret_cast<u32x2*>((row < TM / 2 ? lds0 : lds1) + row % (TM / 2) * (2 * TN) + 16 * (c ^ r) +
-                                      8 * (h & 1)) =
+            *reinterpret_cast<u32x2*>(place(row) + 16 * (c ^ r) + 8 * (h & 1)) =
                 u32x2{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1)};
         }
     __syncthreads();
@@ -448,8 +441,7 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
 #pragma unroll
     for (int i = 0; i < TM / kRows; ++i) {
         const uint32_t row = (uint32_t)tid / kChunks + kRows * i;
-        const uint8_t* const from =
-            (row < TM / 2 ? lds0 : lds1) + row % (TM / 2) * (2 * TN) + 16 * (c ^ (row & 15));
+        const uint8_t* const from = place(row) + 16 * (c ^ (row & 15));
         const uint32_t off = (int)(8 * c) < cols ? (row * (uint32_t)N + (uint32_t)n0) * 2 + 16 * c : kOutOfRange;
         __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4*>(from), ry, (int)off, 0, 2);
     }
@@ -620,14 +612,12 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
     //     5.8, 7.8; 64 rows over 16 experts x 512 x 4096: 8.7, 12.5; and up to two workgroups of
     //     16 tokens per CU if K is long: 8 rows x 16384 x 7168 25.9, 30.2, but 8 rows x 16384 x
     //     4096 14.8 against 13.0
-    //   256 x 256, from 192 rows per expert on: 8 experts, 2048 rows x 4096 x 7168: 108, 128 x
-    //     128: 129; 32768 rows: 890, 1100; but 1 expert, 1024 rows x 4096 x 4096 (64 tiles): 49
-    //     against 25
-    //   128 x 128, from 12 rows on: two buffers and 4 waves where CUs share workgroups (8
-    //     experts, 256 rows x 7168 x 2048, 504 of them: 27, 8 waves and four buffers 29), the
-    //     latter for fewer tiles (8 experts, 512 rows x 4096 x 7168, 352: 61.6, 68.5; 3 experts,
-    //     1501 rows x 1352 x 1744, 154: 15.5, 17.7); against 32 x 128: 8 experts, 256 rows x
-    //     7168 x 2048: 27, 32
+    //   256 x 256, from 192 rows per expert on: 8 experts, 2048 rows x 4096 x 7168: 102, 128 x
+    //     128: 119; 32768 rows: 930, 1160; but 1 expert, 1024 rows x 4096 x 4096 (64 tiles): 49
+    //     against 27
+    //   128 x 128, from 12 rows on: 8 experts, 256 rows x 7168 x 2048: 27, 32 x 128 32; 3
+    //     experts, 1501 rows x 1352 x 1744: 14.9, 20.5; 32 experts, 512 rows x 4096 x 7168: 171,
+    //     175
     //   32 x 128 for the rest (32 experts, 128 rows: 146, 128 x 128 158; 1 expert, 200 rows x
     //     4096 x 7168: 20.3, 33), four buffers while there is one workgroup per CU (5 experts'
     //     rows x 4096 x 7168: 30.7, three buffers 35.1)
@@ -642,12 +632,8 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
     }
     if (M_cap >= 192 * (int64_t)G && tiles(M_cap, G, N, 256, 256) >= 192)
         return tile((const void*)block_gemm_tile_kernel<2, 4, 8, 4, 2>, 256, 256, 512);
-    const int64_t large = tiles(M_cap, G, N, 128, 128);
-    if (M_cap >= 12 * (int64_t)G && large >= 128) {
-        if (large >= 448)
-            return tile((const void*)block_gemm_tile_kernel<2, 2, 4, 4, 2>, 128, 128, 256);
-        return tile((const void*)block_gemm_tile_kernel<2, 4, 4, 2, 4>, 128, 128, 512);
-    }
+    if (M_cap >= 12 * (int64_t)G && tiles(M_cap, G, N, 128, 128) >= 128)
+        return tile((const void*)block_gemm_tile_kernel<2, 2, 4, 4, 2>, 128, 128, 256);
     if (tiles(M_cap, G, N, 32, 128) <= 256)
         return tile((const void*)block_gemm_tile_kernel<1, 4, 2, 2, 4>, 32, 128, 256);
     return tile((const void*)block_gemm_tile_kernel<1, 4, 2, 2, 3>, 32, 128, 256);
