@@ -11,18 +11,19 @@
 // v_mfma_f32_32x32x64 per block, 16 results each, measured 1490 us where this form, in the
 // first version of the same tile, took 1225.)
 //
-// What bounds it (32768 rows x 7168 x 4096, 8 experts, 890-940 us, 2.05-2.15 PFLOP/s; this
+// What bounds it (32768 rows x 7168 x 4096, 8 experts, 890-950 us, 2.0-2.15 PFLOP/s; this
 // library's UE8M0-scaled product of that size, where the matrix cores apply the scales,
-// takes 802, the vendor library's per-tensor-scaled FP8 product 710): the matrix
-// instructions fill 2048 cycles of a 256 x 256 tile's stage, the scaled adds half as many
-// vector cycles beside them, the fragment reads 1536 LDS cycles and the loads 512.  With few
-// rows it is the weights' bytes: 128 rows over 32 experts x 4096 x 7168 take 147 us, 6.4 TB/s.
+// takes 802, the vendor library's per-tensor-scaled FP8 product 710): power, at 1.92-2.07 GHz
+// with the matrix cores busy half the time (784 us with zeros for operands and the clock at
+// its top).  Of a 256 x 256 tile's stage the matrix instructions fill 2048 cycles, the scaled
+// adds half as many vector cycles beside them, and its 64 KB have to arrive.  With few rows
+// it is the weights' bytes: 128 rows over 32 experts x 4096 x 7168 take 147 us, 6.4 TB/s.
 //
 // Two kernels, both with the operands staged in LDS: in the tile kernel all waves share a
 // stage, in the rows kernel the waves split K, where there are so few tiles that a tile's walk
-// along K would be the time.  Buffer loads take the bounds: rows past the expert's and features past N are
-// outside the ranges and read as zero, and a lane whose bytes are past K gets an offset
-// outside every range.
+// along K would be the time.  Buffer loads take the bounds: rows past the expert's and
+// features past N are outside the ranges and read as zero, and a lane whose bytes are past K
+// gets an offset outside every range.
 #include "tiles.h"
 
 namespace mxfp4 {
