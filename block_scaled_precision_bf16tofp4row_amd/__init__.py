@@ -53,6 +53,7 @@ still works but every call raises; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -521,6 +522,7 @@ def mxfp4_route_topk_backward(logits, ids, dweights, dlogits, score="softmax", r
                                                     float(scale), _stream(stream)), "mxfp4_route_topk_backward")
 
 
+@functools.lru_cache(maxsize=4096)                 # (of the sizes alone; a call of its own costs a microsecond)
 def mxfp4_expert_map_workspace(T: int, k: int, G: int) -> int:
     return int(load_library().mxfp4_expert_map_workspace(int(T), int(k), int(G)))
 
