@@ -8,7 +8,7 @@
 // Backward, with D = sum_i s_i + 1e-20 over the selected experts:
 //     ds_j = scale * (dw_j - sum_i dw_i s_i / D) / D, or scale * dw_j
 //     softmax: dl_e = s_e (ds_e - sum_j ds_j s_j), ds_e = 0 where e is not selected
-//     sigmoid: dl_e = s_e (1 - s_e) ds_e
+//     sigmoid: dl_e = s_e (1 - s_e) ds_e, s (1 - s) as e / (1 + e)^2 with e = exp(-|l|)
 // All of it in FP32; the logits are read once (16-byte loads where the rows allow them).
 //
 // Selection works on order keys: the FP32 bits of c made monotone as unsigned integers,
@@ -49,7 +49,18 @@ __device__ __forceinline__ float exp_f32(float x)
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269502162933349609375f); }
 // (the hardware reciprocal: one unit in the last place; below 2^-126 it gives 0)
 __device__ __forceinline__ float sigmoid_fast(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x)); }
-__device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x)); }
+// The sigmoid and its derivative.  From e = exp(-|x|) neither is a difference of nearly equal
+// numbers: s (1 - s) of the rounded s has 4 bits left at x = 16, where it is as confident as
+// the experts that are chosen, and none from 17 on.
+struct Sigmoid {
+    float s, ds;
+};
+__device__ __forceinline__ Sigmoid sigmoid_f32(float x)
+{
+    const float e = exp_f32(-__builtin_fabsf(x));
+    const float r = 1.0f / (1.0f + e);
+    return {x < 0.0f ? e * r : r, e * r * r};
+}
 
 // FP32 -> order key: larger key, larger value.  Numbers take 0x00FFFFFE (-inf) to 0xFFFFFFFF
 // (+inf); the sum that puts +inf there lets every NaN wrap to less than -inf, and the maximum
@@ -529,30 +540,29 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const float lj = load_logit(row + max(id, 0));
     float p[Q][4];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        const int e = (q * LANES + r) * 4;
-        if (VEC) {
-            const f32x4 v = load_logit4(row + (e < E ? e : 0));
+    for (int q = 0; q < Q; ++q)
+        *reinterpret_cast<f32x4*>(ds_row + (q * LANES + r) * 4) = f32x4{};
+    RowNorm n{0.0f, 1.0f};
+    Sigmoid own{0.0f, 0.0f};
+    if (sigmoid) {                                // of the chosen alone: the others' gradient is 0
+        own = sigmoid_f32(lj);
+    } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                p[q][j] = e < E ? v[j] : -__builtin_inff();
-        } else {
+        for (int q = 0; q < Q; ++q) {
+            const int e = (q * LANES + r) * 4;
+            if (VEC) {
+                const f32x4 v = load_logit4(row + (e < E ? e : 0));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float v = load_logit(row + min(e + j, E - 1));
-                p[q][j] = e + j < E ? v : -__builtin_inff();
+                for (int j = 0; j < 4; ++j)
+                    p[q][j] = e < E ? v[j] : -__builtin_inff();
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float v = load_logit(row + min(e + j, E - 1));
+                    p[q][j] = e + j < E ? v : -__builtin_inff();
+                }
             }
         }
-        *reinterpret_cast<f32x4*>(ds_row + e) = f32x4{};
-    }
-    RowNorm n{0.0f, 1.0f};
-    if (sigmoid) {
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                p[q][j] = sigmoid_f32(p[q][j]);
-    } else {
         float top = -__builtin_inff(), sum = 0.0f;
 #pragma unroll
         for (int q = 0; q < Q; ++q)
@@ -567,14 +577,14 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
                 sum += p[q][j] = exp_f32(p[q][j] - n.m);
         n.inv = norm_inv(lanes_sum<LANES>(sum));
     }
-    const float sj = id < 0 ? 0.0f : sigmoid ? sigmoid_f32(lj) : softmax_of(lj, n);
+    const float sj = id < 0 ? 0.0f : sigmoid ? own.s : softmax_of(lj, n);
     float ds = scale * dw;
     if (renorm) {
         const float D = lanes_sum<LANES>(sj) + 1e-20f;
         ds = scale * ((dw - lanes_sum<LANES>(dw * sj) / D) / D);
     }
     if (id >= 0)
-        ds_row[id] = ds;
+        ds_row[id] = sigmoid ? ds * own.ds : ds;
     else
         ds = 0.0f;
     const float dot = sigmoid ? 0.0f : lanes_sum<LANES>(ds * sj);
@@ -586,10 +596,8 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
         const f32x4 d = *reinterpret_cast<const f32x4*>(ds_row + e);
         f32x4 v;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float s = p[q][j] * n.inv;
-            v[j] = sigmoid ? d[j] * (s * (1.0f - s)) : s * (d[j] - dot);
-        }
+        for (int j = 0; j < 4; ++j)
+            v[j] = sigmoid ? d[j] : p[q][j] * n.inv * (d[j] - dot);
         if (VEC) {
             if (live && e < E)
                 store_logit4(out + e, v);

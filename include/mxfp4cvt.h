@@ -264,7 +264,8 @@ mxfp4_status mxfp4_route_topk(const void* logits, int32_t logits_f32, const floa
  * D = sum_i s_i + 1e-20 over a token's ids,
  *     ds_j = scale (dw_j - sum_i dw_i s_i / D) / D  if renorm, else scale dw_j
  *     softmax: dl_e = s_e (ds_e - sum_j ds_j s_j);   sigmoid: dl_e = s_e (1 - s_e) ds_e
- * (ds_e = 0 where e was not chosen; the choice itself has no gradient).  Ids outside
+ * (ds_e = 0 where e was not chosen, and dl_e = 0 there under sigmoid whatever l_e is; the
+ * choice itself has no gradient).  Ids outside
  * [0, E) (masked rows) count as no choice; a token's ids are distinct otherwise. */
 mxfp4_status mxfp4_route_topk_backward(const void* logits, int32_t logits_f32, const int32_t* ids,
                                        const float* dweights, void* dlogits, int64_t T, int32_t E, int32_t k,

@@ -1,0 +1,70 @@
+"""The router's gradient where FP32 loses most: confident experts; and rows with NaN logits.
+
+In units of u = 2^-24, with an exponential good to 3 u (the instruction's unit in the last
+place and one rounding): a sigmoid's derivative e / (1 + e)^2 is good to 9 u, what it is
+multiplied by to about 3 k + 20 u of the magnitudes it is made of: 2^-17 of those for the k
+here.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+import block_scaled_precision_bf16tofp4row_amd as mx  # noqa: E402
+
+
+def backward(l, ids, dw, **kw):
+    dl = torch.full_like(l, 77.0, device="cuda")
+    mx.mxfp4_route_topk_backward(l.cuda(), ids.cuda(), dw.cuda(), dl, **kw)
+    return dl.double().cpu().numpy()
+
+
+def sigmoid_gradient(l, ids, dw, renorm, scale):
+    """dlogits and the magnitudes it is made of, the derivative as e / (1 + e)^2, e = exp(-|l|)."""
+    e = np.exp(-np.abs(l))
+    s, der = np.where(l < 0, e, 1) / (1 + e), e / (1 + e) ** 2
+    sj, dj = np.take_along_axis(s, ids, 1), np.take_along_axis(der, ids, 1)
+    if renorm:
+        D = sj.sum(1, keepdims=True) + 1e-20
+        ds = scale * (dw - (dw * sj).sum(1, keepdims=True) / D) / D
+        mag = abs(scale) * (np.abs(dw) + (np.abs(dw) * sj).sum(1, keepdims=True) / D) / D
+    else:
+        ds, mag = scale * dw, abs(scale * dw)
+    out, big = np.zeros_like(l), np.zeros_like(l)
+    np.put_along_axis(out, ids, ds * dj, 1)
+    np.put_along_axis(big, ids, mag * dj, 1)
+    return out, big
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,k,f32", [(16, 4, True), (256, 8, True), (60, 6, False), (300, 8, True), (64, 20, True)])
+def test_sigmoid_gradient_of_confident_experts(E, k, f32, renorm):
+    T = 64
+    g = torch.Generator().manual_seed(E + k)
+    size = torch.tensor([5.0, 10.0, 17.0, 30.0, 60.0])[torch.randint(0, 5, (T, E), generator=g)]
+    l = size * (torch.randint(0, 2, (T, E), generator=g) * 2 - 1) + torch.randn(T, E, generator=g) * 0.5
+    l = l if f32 else l.bfloat16()
+    ids = torch.rand(T, E, generator=g).topk(k, 1).indices.to(torch.int32)
+    dw = torch.randn(T, k, generator=g)
+    got = backward(l, ids, dw, score="sigmoid", renorm=renorm, scale=2.5)
+    want, mag = sigmoid_gradient(l.double().numpy(), ids.numpy().astype(np.int64), dw.double().numpy(), renorm, 2.5)
+    assert np.all(np.abs(got - want) <= 2.0 ** -17 * mag + (0 if f32 else 2.0 ** -8) * np.abs(want) + 1e-37)
+
+
+def test_nan_logits_of_the_gradient():
+    """Under softmax every score of such a row is NaN; a sigmoid's gradient is of the chosen alone."""
+    T, E, k = 6, 40, 4
+    g = torch.Generator().manual_seed(2)
+    l = torch.randn(T, E, generator=g)
+    ids = torch.rand(T, E, generator=g).topk(k, 1).indices.to(torch.int32)
+    dw = torch.randn(T, k, generator=g)
+    clean = {s: backward(l, ids, dw, score=s) for s in ("softmax", "sigmoid")}
+    free = [e for e in range(E) if e not in ids[2].tolist()]
+    l[2, free[0]], l[2, free[1]] = torch.nan, torch.inf
+    rest = [0, 1, 3, 4, 5]
+    got = backward(l, ids, dw, score="softmax")
+    assert np.isnan(got[2]).all() and np.array_equal(got[rest], clean["softmax"][rest])
+    got = backward(l, ids, dw, score="sigmoid")
+    assert np.array_equal(got, clean["sigmoid"])
