@@ -588,6 +588,8 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     else
         ds = 0.0f;
     const float dot = sigmoid ? 0.0f : lanes_sum<LANES>(ds * sj);
+    // (a row without a choice may hold anything, NaN too, and has no gradient)
+    const bool any = lanes_max<LANES>(id >= 0) != 0;
     __builtin_amdgcn_wave_barrier();              // (one wave writes and reads the row)
     T* const out = dlogits + tr * E;
 #pragma unroll
@@ -597,7 +599,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
         f32x4 v;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            v[j] = sigmoid ? d[j] : p[q][j] * n.inv * (d[j] - dot);
+            v[j] = sigmoid ? d[j] : any ? p[q][j] * n.inv * (d[j] - dot) : 0.0f;
         if (VEC) {
             if (live && e < E)
                 store_logit4(out + e, v);

@@ -266,7 +266,8 @@ mxfp4_status mxfp4_route_topk(const void* logits, int32_t logits_f32, const floa
  *     softmax: dl_e = s_e (ds_e - sum_j ds_j s_j);   sigmoid: dl_e = s_e (1 - s_e) ds_e
  * (ds_e = 0 where e was not chosen, and dl_e = 0 there under sigmoid whatever l_e is; the
  * choice itself has no gradient).  Ids outside
- * [0, E) (masked rows) count as no choice; a token's ids are distinct otherwise. */
+ * [0, E) (masked rows) count as no choice, and a row without one gets zeros whatever it
+ * holds; a token's ids are distinct otherwise. */
 mxfp4_status mxfp4_route_topk_backward(const void* logits, int32_t logits_f32, const int32_t* ids,
                                        const float* dweights, void* dlogits, int64_t T, int32_t E, int32_t k,
                                        int32_t score, int32_t renorm, float scale, hipStream_t stream);

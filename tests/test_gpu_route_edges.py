@@ -1,4 +1,5 @@
-"""The router's gradient where FP32 loses most: confident experts; and rows with NaN logits.
+"""The router's gradient where FP32 loses most: confident experts; and rows with
+NaN logits, with or without a choice.
 
 In units of u = 2^-24, with an exponential good to 3 u (the instruction's unit in the last
 place and one rounding): a sigmoid's derivative e / (1 + e)^2 is good to 9 u, what it is
@@ -51,6 +52,28 @@ def test_sigmoid_gradient_of_confident_experts(E, k, f32, renorm):
     got = backward(l, ids, dw, score="sigmoid", renorm=renorm, scale=2.5)
     want, mag = sigmoid_gradient(l.double().numpy(), ids.numpy().astype(np.int64), dw.double().numpy(), renorm, 2.5)
     assert np.all(np.abs(got - want) <= 2.0 ** -17 * mag + (0 if f32 else 2.0 ** -8) * np.abs(want) + 1e-37)
+
+
+@pytest.mark.parametrize("E,k", [(32, 4), (300, 20)])                         # 16 lanes and a wave per token
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_of_rows_without_a_choice_is_zero(score, E, k):
+    """Whatever their logits are: NaN, infinities, the type's lowest value."""
+    T = 12
+    g = torch.Generator().manual_seed(E)
+    l = torch.randn(T, E, generator=g)
+    ids = torch.rand(T, E, generator=g).topk(k, 1).indices.to(torch.int32)
+    dw = torch.randn(T, k, generator=g)
+    clean = backward(l, ids, dw, score=score)
+    odd = [(1, torch.nan), (3, torch.inf), (5, -torch.inf), (6, torch.finfo(torch.float32).min)]
+    for t, v in odd:
+        l[t] = v
+        ids[t] = -1
+    l[8, 5], ids[8], dw[8] = torch.nan, E + 3, torch.nan
+    got = backward(l, ids, dw, score=score)
+    none = [t for t, _ in odd] + [8]
+    assert (got[none] == 0).all()
+    rest = [t for t in range(T) if t not in none]
+    assert np.array_equal(got[rest], clean[rest])
 
 
 def test_nan_logits_of_the_gradient():
