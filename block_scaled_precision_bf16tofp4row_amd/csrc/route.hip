@@ -522,10 +522,10 @@ __device__ __forceinline__ void store_logit4(uint16_t* p, f32x4 v)
 // per load); lane j < k holds selection j.  The selected experts' ds are placed in a row of
 // LDS that is zero elsewhere, from which every lane takes its experts'.  Reading and writing
 // the logits is what bounds it (16384 tokens x 256 experts, FP32: 34.6 MB).
-template <int LANES, int Q, bool VEC, typename T>
+template <int LANES, int Q, bool VEC, bool SIGMOID, typename T>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const T* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ dweights,
-    T* __restrict__ dlogits, int64_t n_tokens, int E, int k, int sigmoid, int renorm, float scale)
+    T* __restrict__ dlogits, int64_t n_tokens, int E, int k, int renorm, float scale)
 {
     __shared__ __attribute__((aligned(16))) float ds_lds[kThreads / LANES][LANES * 4 * Q];
     const int r = threadIdx.x % LANES;
@@ -534,17 +534,20 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const bool live = t < n_tokens;               // (a row of lanes without a token does the last one's, unstored)
     const int64_t tr = live ? t : n_tokens - 1;
     const T* const row = logits + tr * E;
-    int id = r < k ? ids[tr * k + r] : -1;
-    id = (uint32_t)id < (uint32_t)E ? id : -1;
-    const float dw = id >= 0 ? dweights[tr * k + r] : 0.0f;
+    // (loads and scores without branches: behind one each of them waits for the last, which takes
+    // a wave per token, 32768 x 384, from 19.7 to 21.6 us)
+    int id = ids[tr * k + min(r, k - 1)];
+    id = r < k && (uint32_t)id < (uint32_t)E ? id : -1;
+    float dw = dweights[tr * k + min(r, k - 1)];
+    dw = id >= 0 ? dw : 0.0f;
     const float lj = load_logit(row + max(id, 0));
-    float p[Q][4];
 #pragma unroll
     for (int q = 0; q < Q; ++q)
         *reinterpret_cast<f32x4*>(ds_row + (q * LANES + r) * 4) = f32x4{};
+    float p[Q][4];
     RowNorm n{0.0f, 1.0f};
     Sigmoid own{0.0f, 0.0f};
-    if (sigmoid) {                                // of the chosen alone: the others' gradient is 0
+    if constexpr (SIGMOID) {                      // its gradient is of the chosen alone
         own = sigmoid_f32(lj);
     } else {
 #pragma unroll
@@ -577,19 +580,32 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
                 sum += p[q][j] = exp_f32(p[q][j] - n.m);
         n.inv = norm_inv(lanes_sum<LANES>(sum));
     }
-    const float sj = id < 0 ? 0.0f : sigmoid ? own.s : softmax_of(lj, n);
+    const uint32_t sbits = __float_as_uint(SIGMOID ? own.s : softmax_of(lj, n));
+    const float sj = __uint_as_float(id < 0 ? 0u : sbits);
     float ds = scale * dw;
     if (renorm) {
         const float D = lanes_sum<LANES>(sj) + 1e-20f;
         ds = scale * ((dw - lanes_sum<LANES>(dw * sj) / D) / D);
     }
     if (id >= 0)
-        ds_row[id] = sigmoid ? ds * own.ds : ds;
+        ds_row[id] = SIGMOID ? ds * own.ds : ds;
     else
         ds = 0.0f;
-    const float dot = sigmoid ? 0.0f : lanes_sum<LANES>(ds * sj);
-    // (a row without a choice may hold anything, NaN too, and has no gradient)
-    const bool any = lanes_max<LANES>(id >= 0) != 0;
+    float dot = 0.0f;
+    if constexpr (!SIGMOID) {
+        dot = lanes_sum<LANES>(ds * sj);
+        // a row without a choice may hold anything, NaN too, and has no gradient
+        const uint64_t chosen = __ballot(id >= 0);
+        const bool none = (LANES == 16 ? chosen >> (threadIdx.x & 48) & 0xFFFF : chosen) == 0;
+        if (__ballot(none) && none) {
+            n.inv = 0.0f;
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    p[q][j] = 0.0f;
+        }
+    }
     __builtin_amdgcn_wave_barrier();              // (one wave writes and reads the row)
     T* const out = dlogits + tr * E;
 #pragma unroll
@@ -599,7 +615,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
         f32x4 v;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            v[j] = sigmoid ? d[j] : any ? p[q][j] * n.inv * (d[j] - dot) : 0.0f;
+            v[j] = SIGMOID ? d[j] : p[q][j] * n.inv * (d[j] - dot);
         if (VEC) {
             if (live && e < E)
                 store_logit4(out + e, v);
@@ -634,16 +650,23 @@ static const void* route_quad_kernel_for(int vpl, bool vec)
     }
 }
 
-template <bool VEC, typename T>
-static const void* route_backward_for(int lanes, int q)
+template <bool VEC, bool SIGMOID, typename T>
+static const void* route_backward_of(int lanes, int q)
 {
     if (lanes == 16)
-        return q == 1   ? (const void*)route_backward_kernel<16, 1, VEC, T>
-               : q == 2 ? (const void*)route_backward_kernel<16, 2, VEC, T>
-                        : (const void*)route_backward_kernel<16, 4, VEC, T>;
-    return q == 1   ? (const void*)route_backward_kernel<64, 1, VEC, T>
-           : q == 2 ? (const void*)route_backward_kernel<64, 2, VEC, T>
-                    : (const void*)route_backward_kernel<64, 4, VEC, T>;
+        return q == 1   ? (const void*)route_backward_kernel<16, 1, VEC, SIGMOID, T>
+               : q == 2 ? (const void*)route_backward_kernel<16, 2, VEC, SIGMOID, T>
+                        : (const void*)route_backward_kernel<16, 4, VEC, SIGMOID, T>;
+    return q == 1   ? (const void*)route_backward_kernel<64, 1, VEC, SIGMOID, T>
+           : q == 2 ? (const void*)route_backward_kernel<64, 2, VEC, SIGMOID, T>
+                    : (const void*)route_backward_kernel<64, 4, VEC, SIGMOID, T>;
+}
+template <typename T>
+static const void* route_backward_for(int lanes, int q, bool vec, bool sigmoid)
+{
+    if (sigmoid)
+        return vec ? route_backward_of<true, true, T>(lanes, q) : route_backward_of<false, true, T>(lanes, q);
+    return vec ? route_backward_of<true, false, T>(lanes, q) : route_backward_of<false, false, T>(lanes, q);
 }
 
 // Workgroups of the router at most with a wave per token: the 8 a CU holds at a time; they
@@ -708,15 +731,13 @@ hipError_t launch_route_backward(const void* logits, bool f32, const int32_t* id
     const int per = kThreads / lanes;             // tokens of a workgroup
     const int64_t grid = (T + per - 1) / per;
     int64_t t = T;
-    int e = E, kk = k, sg = sigmoid, rn = renorm;
+    int e = E, kk = k, rn = renorm;
     float sc = scale;
     void* args[] = {(void*)&logits, (void*)&ids, (void*)&dweights, (void*)&dlogits, (void*)&t, (void*)&e,
-                    (void*)&kk, (void*)&sg, (void*)&rn, (void*)&sc};
-    const void* kernel;
-    if (E % 4 == 0)
-        kernel = f32 ? route_backward_for<true, float>(lanes, q) : route_backward_for<true, uint16_t>(lanes, q);
-    else
-        kernel = f32 ? route_backward_for<false, float>(lanes, q) : route_backward_for<false, uint16_t>(lanes, q);
+                    (void*)&kk, (void*)&rn, (void*)&sc};
+    const bool vec = E % 4 == 0;
+    const void* kernel = f32 ? route_backward_for<float>(lanes, q, vec, sigmoid)
+                             : route_backward_for<uint16_t>(lanes, q, vec, sigmoid);
     return launch_kernel(kernel, dim3((unsigned)grid), dim3(kThreads), args, stream);
 }
 
