@@ -29,26 +29,37 @@ namespace {
 
 constexpr int kMaxRouteV = 32;                    // experts per lane at most
 
-// exp(x) in FP32 to about 2 units in the last place: 2^(x log2 e) with the product's
-// rounding error put back (x log2 e carries an absolute error of |x| 2^-24 otherwise).
-__device__ __forceinline__ float exp_f32(float x)
+constexpr float kLog2eHi = 1.44269502162933349609375f;       // log2 e, rounded to FP32
+constexpr float kLog2eLo = 1.9259629911e-8f;                 // and the rest of it
+
+// exp(x + dx) in FP32 to about 2 units in the last place, for x <= 0 and dx far below x:
+// 2^(x log2 e) with the product's rounding error put back (x log2 e carries an absolute error
+// of |x| 2^-24 otherwise).  Where x log2 e is -inf, and the result 0, the correction is
+// infinite or NaN: the median makes it finite (it is below 2^-13 elsewhere).
+__device__ __forceinline__ float exp_f32(float x, float dx = 0.0f)
 {
-    constexpr float kHi = 1.44269502162933349609375f;        // log2 e, rounded to FP32
-    constexpr float kLo = 1.9259629911e-8f;                // log2 e - kHi
     constexpr float kLn2 = 0.6931471805599453f;
-    const float t = x * kHi;
+    const float t = x * kLog2eHi;
     const float e = __builtin_amdgcn_exp2f(t);
-    const float lo = __builtin_fmaf(x, kHi, -t) + x * kLo;
-    const float r = __builtin_fmaf(e, lo * kLn2, e);
-    return __builtin_isfinite(r) ? r : e;         // exp(+-inf), exp(NaN) as they are
+    const float lo = __builtin_fmaf(x, kLog2eLo, __builtin_fmaf(x, kLog2eHi, -t));
+    return __builtin_fmaf(e, __builtin_amdgcn_fmed3f(__builtin_fmaf(lo, kLn2, dx), -1.0f, 1.0f), e);
 }
 
-// The router's exp, without that correction: its relative error is |x| 2^-24 and the
-// instruction's, 4e-7 at |x| = 8, under what may decide a choice among FP32 scores anyway,
-// for a third of the score's instructions less.
-__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269502162933349609375f); }
-// (the hardware reciprocal: one unit in the last place; below 2^-126 it gives 0)
-__device__ __forceinline__ float sigmoid_fast(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_fast(-x)); }
+// The forward pass takes exp of every logit without that correction, for the order keys and a
+// softmax row's sum, and forms the scores of the chosen anew for their weights.  A softmax
+// row's terms are off by |x| 2^-24 and the instruction's unit, to either side: in the sum that
+// weighs |x| e^x, a few 2^-24 at most (with the correction 32768 x 256: 10.5 us for 9.5).
+__device__ __forceinline__ float exp_row(float x)
+{
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2eHi, x * kLog2eLo));
+}
+// A sigmoid's key: off by |x| (2^-24 + 1.4e-8) of itself, in part to one side, and the
+// exponential's and the reciprocal's unit each.  It rises with x, so it decides like the exact
+// score but for what differs by less than that beside a bias or in a group's sum.
+__device__ __forceinline__ float sigmoid_key(float x)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2eHi));
+}
 // The sigmoid and its derivative.  From e = exp(-|x|) neither is a difference of nearly equal
 // numbers: s (1 - s) of the rounded s has 4 bits left at x = 16, where it is as confident as
 // the experts that are chosen, and none from 17 on.
@@ -57,8 +68,9 @@ struct Sigmoid {
 };
 __device__ __forceinline__ Sigmoid sigmoid_f32(float x)
 {
-    const float e = exp_f32(-__builtin_fabsf(x));
-    const float r = 1.0f / (1.0f + e);
+    const float e = exp_f32(-__builtin_fabsf(x)), d = 1.0f + e;
+    float r = __builtin_amdgcn_rcpf(d);           // 1 / d, d in [1, 2]: one Newton step rounds it
+    r = __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);
     return {x < 0.0f ? e * r : r, e * r * r};
 }
 
@@ -128,7 +140,14 @@ __device__ __forceinline__ f32x4 load_logit4(const uint16_t* p)
 struct RowNorm {
     float m, inv;
 };
-__device__ __forceinline__ float softmax_of(float l, RowNorm n) { return exp_f32(l - n.m) * n.inv; }
+// One of its scores, with what l - m loses put back (half a unit of the difference: 4e-6 of the
+// score at 80 below the maximum).  In the row's sum such terms weigh nothing and go without.
+__device__ __forceinline__ float softmax_of(float l, RowNorm n)
+{
+    const float d = l - n.m, b = d - l;           // (the exact error of a difference, after Knuth)
+    const float err = (l - (d - b)) - (n.m + b);
+    return exp_f32(d, err) * n.inv;
+}
 // The maximum from its key (0 for a row of -inf or NaN only), the factor from the sum (NaN if
 // a logit is NaN, which the maximum leaves out).
 __device__ __forceinline__ float norm_top(uint32_t key)
@@ -138,7 +157,7 @@ __device__ __forceinline__ float norm_top(uint32_t key)
 }
 __device__ __forceinline__ float norm_inv(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
 // The norm of a row spread over a wave, and its scores in place of the logits.
-template <int V, bool FAST = false>
+template <int V>
 __device__ __forceinline__ RowNorm softmax_row(float (&l)[V])
 {
     float top = l[0];
@@ -150,7 +169,7 @@ __device__ __forceinline__ RowNorm softmax_row(float (&l)[V])
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        sum += l[i] = FAST ? exp_fast(l[i] - n.m) : exp_f32(l[i] - n.m);
+        sum += l[i] = exp_row(l[i] - n.m);
     n.inv = norm_inv(wave_sum(sum));
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -172,7 +191,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(
     int32_t* __restrict__ ids, float* __restrict__ weights, int64_t n_tokens, int E, int n_group, int gs,
     int topk_group, int group_best, int k, int sigmoid, int renorm, float scale, int l_log)
 {
-    __shared__ __attribute__((aligned(16))) float s_lds[kThreads / 64][64 * VPL];
+    __shared__ __attribute__((aligned(16))) float l_lds[kThreads / 64][64 * VPL];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t step = (int64_t)gridDim.x * (kThreads / 64);
@@ -205,27 +224,26 @@ __global__ __launch_bounds__(kThreads) void route_kernel(
     load_row(next, logits + t * E);
     for (; t < n_tokens; t += step) {
         float s[VPL];
+        RowNorm n{0.0f, 1.0f};
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            s[i] = next[i];
+            l_lds[wave][lane * VPL + i] = s[i] = next[i];
         if (t + step < n_tokens)
             load_row(next, logits + (t + step) * E);
         if (sigmoid) {
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                s[i] = sigmoid_fast(s[i]);
+                s[i] = sigmoid_key(s[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
                 s[i] = i < nv ? s[i] : -__builtin_inff();
-            softmax_row<VPL, true>(s);
+            n = softmax_row(s);
         }
         uint32_t key[VPL];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
+        for (int i = 0; i < VPL; ++i)
             key[i] = order_key(s[i] + b[i]) & (i < nv ? ~0u : 0u);
-            s_lds[wave][lane * VPL + i] = s[i];
-        }
         if (topk_group < n_group) {
             uint32_t k1 = 0, k2 = 0;              // the two largest keys of the lane, then of the group
 #pragma unroll
@@ -245,7 +263,7 @@ __global__ __launch_bounds__(kThreads) void route_kernel(
             for (int i = 0; i < VPL; ++i)
                 key[i] = rank < topk_group ? key[i] : 0u;
         }
-        int mine = 0;                             // lane j: place of selection j in s_lds
+        int mine = 0;                             // lane j: place of selection j in l_lds
         for (int j = 0; j < k; ++j) {
             uint32_t lm = key[0];
 #pragma unroll
@@ -271,7 +289,11 @@ __global__ __launch_bounds__(kThreads) void route_kernel(
             const int at = (int)__builtin_ctzll(any) * VPL + __builtin_ctz(slots);
             mine = lane == j ? at : mine;
         }
-        const float sj = lane < k ? s_lds[wave][mine] : 0.0f;
+        float sj = 0.0f;
+        if (lane < k) {
+            const float l = l_lds[wave][mine];
+            sj = sigmoid ? sigmoid_f32(l).s : softmax_of(l, n);
+        }
         float w = scale * sj;
         if (renorm)
             w = scale * (sj / (wave_sum(sj) + 1e-20f));
@@ -422,7 +444,8 @@ __global__ __launch_bounds__(kThreads) void route_quad_kernel(
                 v[i] = load_logit(from + (i < nv ? e0 + i : 0));
         }
     };
-    float s[VPL], b[VPL] = {}, m = 0.0f, inv = 1.0f;
+    float s[VPL], b[VPL] = {};
+    RowNorm n{0.0f, 1.0f};
     load_row(s, row);
     if (bias)
         load_row(b, bias);
@@ -431,7 +454,7 @@ __global__ __launch_bounds__(kThreads) void route_quad_kernel(
     if (sigmoid) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            s[i] = sigmoid_fast(s[i]);
+            s[i] = sigmoid_key(s[i]);
     } else {
         float top = -__builtin_inff(), sum = 0.0f;
 #pragma unroll
@@ -439,14 +462,14 @@ __global__ __launch_bounds__(kThreads) void route_quad_kernel(
             s[i] = i < nv ? s[i] : -__builtin_inff();
             top = fmaxf(top, s[i]);
         }
-        m = norm_top(row_max(order_key(top)));
+        n.m = norm_top(row_max(order_key(top)));
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            sum += s[i] = exp_fast(s[i] - m);
-        inv = norm_inv(row_sum(sum));
+            sum += s[i] = exp_row(s[i] - n.m);
+        n.inv = norm_inv(row_sum(sum));
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            s[i] *= inv;
+            s[i] *= n.inv;
     }
     double c[VPL];
 #pragma unroll
@@ -490,7 +513,7 @@ __global__ __launch_bounds__(kThreads) void route_quad_kernel(
     float sj = 0.0f;                              // its score once more, from the cached logit
     if (r < k) {
         const float l = load_logit(row + e);
-        sj = sigmoid ? sigmoid_fast(l) : exp_fast(l - m) * inv;
+        sj = sigmoid ? sigmoid_f32(l).s : softmax_of(l, n);
     }
     float w = scale * sj;
     if (renorm)

@@ -1,19 +1,33 @@
-"""The router's gradient where FP32 loses most: confident experts; and rows with
-NaN logits, with or without a choice.
+"""Routing where FP32 loses most: confident experts, scores far below the largest, rows with
+NaN and infinities beside rows without choices.
 
 In units of u = 2^-24, with an exponential good to 3 u (the instruction's unit in the last
-place and one rounding): a sigmoid's derivative e / (1 + e)^2 is good to 9 u, what it is
-multiplied by to about 3 k + 20 u of the magnitudes it is made of: 2^-17 of those for the k
-here.
+place and one rounding): a sigmoid score is good to 5 u (a sum, a division) and a weight
+without renormalisation to 6 u (the scale); a softmax score adds the sum of the row, at most 8
+u for the sizes here (runs of at most 4, then at most 6 levels of pairs, less the terms' own 3
+u, which they share), and one division: 18 u.  A renormalised weight is a quotient of two such
+numbers (the second a sum of at most 16 in 4 or 6 levels): 40 u.  A sigmoid's derivative
+e / (1 + e)^2 is good to 9 u, what it is multiplied by to about 3 k + 20 u of the magnitudes
+it is made of: 2^-17 of those for the k here.
 """
 from __future__ import annotations
 
 import numpy as np
 import pytest
 
+import moe_ref as ref
+
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 import block_scaled_precision_bf16tofp4row_amd as mx  # noqa: E402
+
+U = 2.0 ** -24
+
+
+def route(l, k, **kw):
+    ids, w = mx.alloc_route_outputs(l.shape[0], k)
+    mx.mxfp4_route_topk(l.cuda(), ids, w, **kw)
+    return ids.cpu().numpy(), w.cpu().numpy()
 
 
 def backward(l, ids, dw, **kw):
@@ -52,6 +66,22 @@ def test_sigmoid_gradient_of_confident_experts(E, k, f32, renorm):
     got = backward(l, ids, dw, score="sigmoid", renorm=renorm, scale=2.5)
     want, mag = sigmoid_gradient(l.double().numpy(), ids.numpy().astype(np.int64), dw.double().numpy(), renorm, 2.5)
     assert np.all(np.abs(got - want) <= 2.0 ** -17 * mag + (0 if f32 else 2.0 ** -8) * np.abs(want) + 1e-37)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,k", [(8, 8), (16, 16), (64, 8), (64, 10)])       # both kernels
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_weights_far_below_the_largest_score(score, E, k, renorm):
+    """Chosen experts down to e^-80 of the best: their weights to FP32's precision."""
+    T = 500
+    g = torch.Generator().manual_seed(E * k)
+    l = torch.full((T, E), -85.0)
+    l[:, :k] = -80 * torch.rand(T, k, generator=g)
+    l = l.gather(1, torch.rand(T, E, generator=g).argsort(1))
+    ids, w = route(l, k, score=score, renorm=renorm, scale=1.25)
+    want = ref.weights_of(ref.scores(l.double().numpy(), score), ids.astype(np.int64), renorm, 1.25)
+    bound = 40 * U if renorm else 18 * U if score == "softmax" else 6 * U
+    assert np.all(np.abs(w - want) <= bound * want + 1e-37), np.abs(w / want - 1).max() / U
 
 
 @pytest.mark.parametrize("E,k", [(32, 4), (300, 20)])                         # 16 lanes and a wave per token
