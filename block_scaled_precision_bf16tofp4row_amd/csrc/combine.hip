@@ -125,6 +125,7 @@ __global__ __launch_bounds__(kWaves > 4 ? 64 * kWaves : kThreads) void combine_b
     if (t < n_tokens) {
         const Choices c = choices_of(pos, weights, t, k, M_cap);
         part[tok][sub][lane] = 0.0f;              // the choices without a row keep it
+        wave_lds_order();                         // (the sums come from lane 0)
         for (uint64_t left = c.live; left;) {
             int64_t row[kBatch];
             float w[kBatch], dot[kBatch] = {};

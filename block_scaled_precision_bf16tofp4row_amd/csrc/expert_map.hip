@@ -13,7 +13,7 @@
 // 256 experts take 4.0 us in one launch (5.8 in two), 2048 5.0 (6.1), 4096 7.0 (7.1), 8192
 // 11.1 (7.4); 65536 slots 7.2, 262144 12.0 with at most 64 chunks (16 chunks: 9.4, 25.6; 128:
 // 7.2, 11.8).
-#include "strips.h"
+#include "lanes.h"
 
 namespace mxfp4 {
 
@@ -165,11 +165,12 @@ __global__ __launch_bounds__(kMapThreads) void expert_place_kernel(
         const int rank =
             __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
         int32_t row = -1;
-        if (e < G) {
+        if (e < G)
             row = next[wave][e] + rank;
-            if (rank == 0)                        // one lane per expert moves its counter on
-                next[wave][e] = row + (int)__popcll(same);
-        }
+        wave_lds_order();                         // every lane has read its counter
+        if (e < G && rank == 0)                   // one lane per expert moves it on
+            next[wave][e] = row + (int)__popcll(same);
+        wave_lds_order();
         if (slot < (uint32_t)slots) {
             const bool live = row >= 0 && row < cap;
             pos[slot] = live ? row : -1;

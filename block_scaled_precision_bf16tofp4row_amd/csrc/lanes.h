@@ -1,4 +1,5 @@
-// lanes.h -- sums and maxima over a wave and over its rows of 16 lanes, by DPP.
+// lanes.h -- sums and maxima over a wave and over its rows of 16 lanes, by DPP, and the order
+// of a wave's own LDS accesses.
 #pragma once
 
 #include "strips.h"
@@ -8,6 +9,16 @@ namespace mxfp4 {
 // (two quad permutations, the mirrors of 8 and 16 lanes, then lane 15 of a row to the next
 // and lane 31 to the upper half: lane 63 has everything.)
 constexpr int kRowMirror = 0x140, kRowHalfMirror = 0x141, kRowBcast15 = 0x142, kRowBcast31 = 0x143;
+
+// What lanes of this wave wrote to LDS before it, every lane of the wave reads after it.  No
+// instruction: a wave's LDS accesses are carried out in order, but without this the compiler
+// need not keep accesses of different lanes to one place in it.
+__device__ __forceinline__ void wave_lds_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
 
 // Lanes that a broadcast does not reach take 0, the identity of both reductions below (keys
 // and sums), so that the compiler folds the move into the operation.

@@ -289,11 +289,12 @@ __global__ __launch_bounds__(kThreads) void route_kernel(
             const int at = (int)__builtin_ctzll(any) * VPL + __builtin_ctz(slots);
             mine = lane == j ? at : mine;
         }
+        wave_lds_order();
+        const float l = l_lds[wave][mine];        // (of every lane: place 0 past the choices)
+        wave_lds_order();                         // the next token's logits take its place
         float sj = 0.0f;
-        if (lane < k) {
-            const float l = l_lds[wave][mine];
+        if (lane < k)
             sj = sigmoid ? sigmoid_f32(l).s : softmax_of(l, n);
-        }
         float w = scale * sj;
         if (renorm)
             w = scale * (sj / (wave_sum(sj) + 1e-20f));
@@ -610,6 +611,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
         const float D = lanes_sum<LANES>(sj) + 1e-20f;
         ds = scale * ((dw - lanes_sum<LANES>(dw * sj) / D) / D);
     }
+    wave_lds_order();                             // the zeros are other lanes'
     if (id >= 0)
         ds_row[id] = SIGMOID ? ds * own.ds : ds;
     else
@@ -629,7 +631,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
                     p[q][j] = 0.0f;
         }
     }
-    __builtin_amdgcn_wave_barrier();              // (one wave writes and reads the row)
+    wave_lds_order();                             // (one wave writes and reads the row)
     T* const out = dlogits + tr * E;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
