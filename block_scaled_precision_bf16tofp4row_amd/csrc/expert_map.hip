@@ -98,7 +98,7 @@ __global__ __launch_bounds__(kMapThreads) void expert_place_kernel(
     __syncthreads();
     const int run = chunk / kMapWaves;            // slots of a wave (a multiple of 64)
     const int64_t from = (int64_t)blockIdx.x * chunk + wave * run;
-    const int steps = from < slots ? min(run, (int)(slots - from) + 63) / 64 : 0;
+    const int steps = from < slots ? (int)((min((int64_t)run, slots - from) + 63) / 64) : 0;
     for (int i = 0; i < steps; ++i) {
         const int e = local_expert(ids, (uint32_t)from + 64 * i + lane, slots, first, G);
         if (e < G)
