@@ -7,12 +7,14 @@ Forward: the router chooses k of E experts per token, the map gives every choice
 expert order, the token rows are quantized into those rows (E4M3, an FP32 scale per 1x128
 block), two expert products with 128x128-scaled E4M3 weights around a gated SiLU, and the
 expert rows come back to their tokens under the router's weights.  The activation itself is
-plain torch.  Buffers are sized once for a number of tokens, nothing reads a count on the
-host, so a layer can be captured into a graph.
+plain torch.  Buffers are sized once for the most tokens of a call, nothing reads a count on
+the host, so a layer can be captured into a graph.
 
 Backward: of the layer's output to the routing weights and router logits and to the tokens.
 The activation gradients run through the same product on the transposed weights (kept beside
-the weights); the weight gradients are mxfp4_fp8_grouped_gemm_wgrad's business and not shown.
+the weights).  Weight gradients are not shown: mxfp4_fp8_grouped_gemm_wgrad computes them from
+the column layouts of the MXFP4 path or of BF16 rows in expert order, which the FP8 dispatch
+here does not make.
 """
 from __future__ import annotations
 
@@ -53,25 +55,34 @@ class ExpertLayer:
                         scale=scale)
 
     def plan(self, T: int, device="cuda"):
-        """The buffers of a call on up to T tokens."""
+        """The buffers of calls on up to T tokens."""
         rows = T * self.k
         bf = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=device)      # noqa: E731
-        b = {"rows": rows}
+        b = {}
         b["ids"], b["w"] = mx.alloc_route_outputs(T, self.k, device)
         b["offs"], b["pos"], b["ws"] = mx.alloc_expert_map_outputs(T, self.k, self.E, device)
         b["x"], b["xs"] = mx.alloc_fp8_rows_f32_outputs(rows, self.H, device)
         b["h"], b["a"], b["y"] = bf(rows, 2 * self.I), bf(rows, self.I), bf(rows, self.H)
         b["aq"], b["as"] = mx.alloc_fp8_rows_f32_outputs(rows, self.I, device)
         b["out"] = bf(T, self.H)
+        b["logits"] = torch.empty((T, self.E), device=device)
         # rows that no token has keep what the buffers hold: make that finite once
         b["h"].zero_()
         return b
 
-    def forward(self, x, b, row_mask=None, shared=None):
+    def part(self, b, T: int):
+        """The part of a plan that T tokens use: every buffer's first rows."""
+        if T > b["out"].shape[0]:
+            raise ValueError(f"{T} tokens, planned for {b['out'].shape[0]}")
+        rows = {"offs": None, "ws": None} | dict.fromkeys(("ids", "w", "pos", "out", "logits"), T)
+        return {name: v[:rows.get(name, T * self.k)] for name, v in b.items()}
+
+    def forward(self, x, plan, row_mask=None, shared=None):
         """x [T, H] BF16 -> [T, H]; shared: a shared expert's output, added in."""
-        b["logits"] = x.float() @ self.router.t()
+        b = self.part(plan, x.shape[0])
+        torch.matmul(x.float(), self.router.t(), out=b["logits"])
         mx.mxfp4_route_topk(b["logits"], b["ids"], b["w"], bias=self.bias, row_mask=row_mask, **self.how)
-        mx.mxfp4_expert_map(b["ids"], b["offs"], b["pos"], b["ws"], M_cap=b["rows"])
+        mx.mxfp4_expert_map(b["ids"], b["offs"], b["pos"], b["ws"])
         mx.mxfp4_dispatch_fp8_rows(x, b["pos"], b["x"], b["xs"])
         mx.mxfp4_fp8_block_gemm(b["x"], b["xs"], self.up, self.up_s, b["h"], b["offs"])
         gate, up = b["h"].chunk(2, 1)
@@ -81,21 +92,22 @@ class ExpertLayer:
         mx.mxfp4_combine_rows(b["y"], b["pos"], b["out"], weights=b["w"], base=shared)
         return b["out"]
 
-    def backward(self, dout, b):
+    def backward(self, dout, plan):
         """After forward: the gradients of the tokens (through the experts) and of the logits."""
         T = dout.shape[0]
+        b = self.part(plan, T)
         dy, da = torch.zeros_like(b["y"]), torch.zeros_like(b["a"])
         dw = torch.empty_like(b["w"])
         mx.mxfp4_combine_rows_backward(dout, b["y"], b["pos"], b["w"], dy, dw)
         dlogits = torch.empty_like(b["logits"])
         mx.mxfp4_route_topk_backward(b["logits"], b["ids"], dw, dlogits, score="sigmoid", scale=self.how["scale"])
-        q, s = mx.alloc_fp8_rows_f32_outputs(b["rows"], self.H)
+        q, s = mx.alloc_fp8_rows_f32_outputs(T * self.k, self.H)
         mx.mxfp4_bf16_to_fp8_rows_f32(dy, q, s, b["offs"])
         mx.mxfp4_fp8_block_gemm(q, s, self.down_t, self.down_ts, da, b["offs"])
         gate, up = b["h"].float().chunk(2, 1)
         sig = torch.sigmoid(gate)
         dh = torch.cat([da.float() * up * sig * (1 + gate * (1 - sig)), da.float() * gate * sig], 1).bfloat16()
-        q, s = mx.alloc_fp8_rows_f32_outputs(b["rows"], 2 * self.I)
+        q, s = mx.alloc_fp8_rows_f32_outputs(T * self.k, 2 * self.I)
         mx.mxfp4_bf16_to_fp8_rows_f32(dh, q, s, b["offs"])
         dxr = torch.zeros_like(b["y"])
         mx.mxfp4_fp8_block_gemm(q, s, self.up_t, self.up_ts, dxr, b["offs"])
