@@ -522,9 +522,13 @@ def mxfp4_route_topk_backward(logits, ids, dweights, dlogits, score="softmax", r
                                                     float(scale), _stream(stream)), "mxfp4_route_topk_backward")
 
 
-@functools.lru_cache(maxsize=4096)                 # (of the sizes alone; a call of its own costs a microsecond)
+@functools.lru_cache(maxsize=4096)                 # (a call of its own costs a microsecond)
+def _map_workspace(T: int, k: int, G: int) -> int:
+    return int(load_library().mxfp4_expert_map_workspace(T, k, G))
+
+
 def mxfp4_expert_map_workspace(T: int, k: int, G: int) -> int:
-    return int(load_library().mxfp4_expert_map_workspace(int(T), int(k), int(G)))
+    return _map_workspace(int(T), int(k), int(G))   # (kept by the numbers: a tensor's may change)
 
 
 def mxfp4_expert_map(ids, offs, pos, workspace, src=None, first_expert=0, T=None, k=None, G=None, M_cap=None,
@@ -545,7 +549,7 @@ def mxfp4_expert_map(ids, offs, pos, workspace, src=None, first_expert=0, T=None
     n = 4 * T * k
     at = _take("mxfp4_expert_map", ((ids, n, "ids", _I32), (offs, 4 * (G + 1), "group_offsets", _I32),
                                     (pos, n, "pos", _I32), (src, 4 * M_cap, "src", _I32),
-                                    (workspace, mxfp4_expert_map_workspace(T, k, G), "workspace", _WORK)))
+                                    (workspace, _map_workspace(T, k, G), "workspace", _WORK)))
     _check(load_library().mxfp4_expert_map(*at, T, k, int(first_expert), G, M_cap, _stream(stream)),
            "mxfp4_expert_map")
 
