@@ -213,7 +213,8 @@ def _current_stream() -> int:
         return _raw_stream(_device())
     import torch
     if hasattr(torch._C, "_cuda_getCurrentRawStream") and torch.cuda.is_initialized():
-        _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        # (the stream function last: another thread may look in between)
+        _device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     return torch.cuda.current_stream().cuda_stream
 
 
