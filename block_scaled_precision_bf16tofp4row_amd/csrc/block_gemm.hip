@@ -150,7 +150,11 @@ struct Tile {
     // past the last reads nothing (its columns are past K).
     static __device__ __forceinline__ void issue_operands(const TileCtx<D>& cx, int b, uint32_t s, int from, int to)
     {
-        const uint32_t k0 = block_of(cx, s) * kBK;
+        // (the resource's range is less than 128 K for an expert of few rows, so a block past the
+        // last is given no scalar offset: what is left of the range would be negative)
+        const uint32_t kb = block_of(cx, s);
+        const bool past = kb >= cx.blocks;
+        const uint32_t k0 = past ? 0 : kb * kBK, K = past ? 0 : cx.K;
 #pragma unroll
         for (int j = from; j < to; ++j) {
             const bool tok = j >= kLoadsW;
@@ -159,7 +163,7 @@ struct Tile {
             const int rows = 8 * (in_half + half * MT);
             uint8_t* const to_buf = half ? cx.late[b] : cx.buf[b];
             const uint32_t c = tok ? (i & 1 ? cx.ac1 : cx.ac0) : (i & 1 ? cx.wc1 : cx.wc0);
-            const uint32_t off = c + k0 < cx.K ? (tok ? cx.abase : cx.wbase) + c : kOutOfRange;
+            const uint32_t off = c + k0 < K ? (tok ? cx.abase : cx.wbase) + c : kOutOfRange;
             load16_to_lds(tok ? cx.ra : cx.rw, to_buf + (tok ? cx.lds_a : cx.lds_w) + 8 * in_half * kBK,
                           off + (uint32_t)rows * cx.K, k0);
         }
