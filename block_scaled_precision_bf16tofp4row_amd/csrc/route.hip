@@ -336,7 +336,7 @@ __device__ __forceinline__ double f64_min(double a, double b)
 }
 __device__ __forceinline__ double candidate(uint32_t key, uint32_t low)
 {
-    const uint32_t hi = __builtin_amdgcn_alignbit(0x40000u, key, 12), lo = key << 20 | low;
+    const uint32_t hi = __builtin_amdgcn_alignbit(0x400u, key, 12), lo = key << 20 | low;
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 __device__ __forceinline__ uint32_t key_of(double c)
