@@ -13,11 +13,13 @@
 //
 // What bounds it (32768 rows x 7168 x 4096, 8 experts, 890-950 us, 2.0-2.15 PFLOP/s; this
 // library's UE8M0-scaled product of that size, where the matrix cores apply the scales,
-// takes 802, the vendor library's per-tensor-scaled FP8 product 710): power, at 1.92-2.07 GHz
-// with the matrix cores busy half the time (784 us with zeros for operands and the clock at
-// its top).  Of a 256 x 256 tile's stage the matrix instructions fill 2048 cycles, the scaled
-// adds half as many vector cycles beside them, and its 64 KB have to arrive.  With few rows
-// it is the weights' bytes: 128 rows over 32 experts x 4096 x 7168 take 147 us, 6.4 TB/s.
+// takes 802, the vendor library's per-tensor-scaled FP8 product 710): first the load path (the
+// loads alone take 820 us, 590 with every operand in the L2; the products alone 685), then
+// power, at 1.92-2.07 GHz with the matrix cores busy half the time (784 us with zeros for
+// operands and the clock at its top).  Of a 256 x 256 tile's stage the matrix instructions
+// fill 2048 cycles, the scaled adds half as many vector cycles beside them, and its 64 KB have
+// to arrive.  With few rows it is the weights' bytes: 128 rows over 32 experts x 4096 x 7168
+// take 147-152 us, 6.2-6.4 TB/s.
 //
 // Two kernels, both with the operands staged in LDS: in the tile kernel all waves share a
 // stage, in the rows kernel the waves split K, where there are so few tiles that a tile's walk
@@ -610,7 +612,10 @@ hipError_t launch_block_gemm(const uint8_t* a, const float* sa, const uint8_t* w
         return launch(kernel, tiles(M_cap, G, N, TM, TN), threads);
     };
     // The choice goes by the number of workgroups (256 CUs) and the rows an expert has on
-    // average.  Measured in us, the chosen one first:
+    // average, as far as the host knows them: by M_cap.  (Where the rows are far fewer, as on a
+    // rank that passes T k for its share, a larger tile than fits is the price: 1033 rows over 32
+    // experts x 4096 x 7168 with M_cap 8192 215 us, with M_cap 1033 173; 502 with 4096 168, 161.)
+    // Measured in us, the chosen one first:
     //   rows kernel, where each of its workgroups has a CU, or nearly, with 16 tokens or 32: one
     //     expert's 16 rows x 4096 x 7168: 8.8 with 16, 9.5 with 32, 32 x 128 18.8; 32 rows: 9.1,
     //     11.0, 19.0; 64 rows: 11.2 with 32, 15.6 with 16, 32 x 128 19.3; 1 row x 7168 x 2048:

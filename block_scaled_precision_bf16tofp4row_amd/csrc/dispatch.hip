@@ -18,7 +18,8 @@
 // positions are scalar loads; else rows follow each other without a gap (32768 rows of 128
 // elements to 8 places: 21.4 us with a wave per row, 10.8 without).  What bounds it is the writing,
 // streamed past the caches: 8192 rows of 7168 to 8 places each take 110 us for 602 MB, 125
-// with ordinary stores.
+// with ordinary stores.  In place, 65536 rows x 7168: 233 us for 1424 MB, x 2048: 68 for 407;
+// 512 x 2048: 2.8.
 #include "common.h"
 
 namespace mxfp4 {

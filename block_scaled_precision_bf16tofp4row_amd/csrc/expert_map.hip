@@ -12,7 +12,8 @@
 // is nothing; two launches and the steps between their barriers are the time: 1024 slots of
 // 256 experts take 4.0 us in one launch (5.8 in two), 2048 5.0 (6.1), 4096 7.0 (7.1), 8192
 // 11.1 (7.4); 65536 slots 7.2, 262144 12.0 with at most 64 chunks (16 chunks: 9.4, 25.6; 128:
-// 7.2, 11.8).
+// 7.2, 11.8), ids in the caches; behind a kernel that streams 600 MB through those 65536 slots
+// take 10.
 #include "lanes.h"
 
 namespace mxfp4 {

@@ -15,12 +15,12 @@
 // NaN below every number, and 0 for what is excluded, so that a comparison is one integer
 // maximum and any input gives k distinct valid indices.
 //
-// What bounds it: 32768 tokens x 256 experts in 8 groups, FP32 logits, 8 choices: 12.8 us for
-// 36 MB, which a copy moves in 7.0; the vector unit is busy for 80 % of the time (600
+// What bounds it: 32768 tokens x 256 experts in 8 groups, FP32 logits, 8 choices: 11.4-12.4 us
+// for 36 MB, which a copy moves in 7.0; the vector unit is busy for 80 % of the time (600
 // instructions per four tokens, half of them the scores and keys, a fifth the sort), with half
-// the bytes (BF16, softmax) it is 11.4 us.  32768 x 64, softmax: 5.6 us.  Few tokens are a
-// launch: 3.6 us for one, 4.2 for 128.  The gradient is its bytes: 16384 x 256, FP32: 8.0 us
-// for 35 MB (6.8 copied).
+// the bytes (BF16, softmax) it is 9.8 us.  32768 x 64, softmax: 5.5 us.  Few tokens are a
+// launch: 3.5 us for one, 4.0 for 128.  The gradient is its bytes: 16384 x 256, FP32, softmax:
+// 7.9 us for 35 MB (6.8 copied), sigmoid, which reads the chosen logits only: 6.2.
 #include "lanes.h"
 
 namespace mxfp4 {
@@ -48,7 +48,7 @@ __device__ __forceinline__ float exp_f32(float x, float dx = 0.0f)
 // The forward pass takes exp of every logit without that correction, for the order keys and a
 // softmax row's sum, and forms the scores of the chosen anew for their weights.  A softmax
 // row's terms are off by |x| 2^-24 and the instruction's unit, to either side: in the sum that
-// weighs |x| e^x, a few 2^-24 at most (with the correction 32768 x 256: 10.5 us for 9.5).
+// weighs |x| e^x, a few 2^-24 at most (with the correction 32768 x 256, BF16: 10.5 us for 9.8).
 __device__ __forceinline__ float exp_row(float x)
 {
     return __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2eHi, x * kLog2eLo));
@@ -185,6 +185,9 @@ __device__ __forceinline__ RowNorm softmax_row(float (&l)[V])
 // is one wave maximum (six DPP steps); the lane and slot that hold it are found on the
 // scalar unit from one ballot per slot.  VEC: VPL is a multiple of 4, groups are too and
 // rows aligned, so a lane's logits are 16-byte (BF16: 8-byte) loads.
+// The selections, one after the other, are its time: 32768 tokens x 384 with 8 choices 44 us
+// for 52 MB (10.3 copied), x 512 with 10 choices 53 (13.7), x 160 in 8 groups with 6 choices
+// 28 (4.4), x 32 in 8 groups with 8 choices 16 (1.2).
 template <int VPL, bool VEC, typename T>
 __global__ __launch_bounds__(kThreads) void route_kernel(
     const T* __restrict__ logits, const float* __restrict__ bias, const uint8_t* __restrict__ row_mask,
@@ -748,7 +751,7 @@ hipError_t launch_route_backward(const void* logits, bool f32, const int32_t* id
                                  float scale, hipStream_t stream)
 {
     // a row of 16 lanes per token where it holds the choices and 16 experts a lane: 32768 x 60,
-    // BF16: 4.7 us, a wave per token 11.7; 16384 x 256, FP32: 8.0 and 8.6
+    // BF16: 4.5 us, a wave per token 11.7; 16384 x 256, FP32: 7.9 and 8.6
     const int lanes = E <= 256 && k <= 16 ? 16 : 64;
     int q = 1;
     while (4 * lanes * q < E)

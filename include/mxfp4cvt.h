@@ -250,6 +250,8 @@ mxfp4_status mxfp4_fp8_grouped_gemm_wgrad(const uint8_t* dyT_e4m3, const uint8_t
  * Equal values (groups and experts): the lower index first; a NaN counts as lower than
  * every number.  So the ids are k different experts whatever the logits are.  A row of
  * -inf only has s = 0 under softmax; a row that holds a NaN or +inf has NaN weights there.
+ * The scores that decide the choice are good to about (|x| + 4) 2^-23 of themselves (x = l,
+ * under softmax l - max l), those of the weights to a few 2^-24.
  *   logits   [T, E] FP32 (logits_f32 != 0) or BF16.      bias [E] (optional).
  *   row_mask [T] (optional): a row whose byte is 0 gets ids -1 and weights 0.
  *   ids, weights [T, k].
