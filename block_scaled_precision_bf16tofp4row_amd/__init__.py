@@ -32,6 +32,12 @@ The binding has the same names as the C ABI:
   ...)`` (the latter for rows in expert order)
 * ``mxfp4_fp8_block_gemm(a, a_scales, w, w_scales, y, offs, ...)`` (expert product with FP32
   scales, 1x128 and 128x128)
+* ``mxfp4_fp8_gated_gemm(a, a_scales, w, w_scales, offs, ...)`` and
+  ``mxfp4_fp8_gated_gemm_backward(a, a_scales, w, w_scales, h, offs, ...)`` (gate and up
+  projections, activation and product in one call, and the gradient behind the down projection)
+* ``mxfp4_fp8_block_gemm_act(a, a_scales, w, w_scales, y, offs, ...)`` (the product with bias,
+  activation and residual) and ``mxfp4_act_rows_backward(dout, pre, offs, ...)`` (the gradient of
+  its rows and biases)
 * ``mxfp4_combine_rows(y, pos, out, weights, base, ...)`` and
   ``mxfp4_combine_rows_backward(dout, y, pos, weights, dy, dweights, ...)`` (expert rows back
   to the tokens)
@@ -68,6 +74,12 @@ MXFP4_ERR_HIP = 4
 MXFP4_SCORE_SOFTMAX = 0
 MXFP4_SCORE_SIGMOID = 1
 
+MXFP4_ACT_NONE = 0
+MXFP4_ACT_RELU = 1
+MXFP4_ACT_SILU = 2
+MXFP4_ACT_GELU = 3
+MXFP4_ACT_GELU_TANH = 4
+
 EXPORTED = (
     "mxfp4_quantize_rows",
     "mxfp4_nvfp4_quantize_rows",
@@ -87,6 +99,13 @@ EXPORTED = (
     "mxfp4_dispatch_fp8_rows",
     "mxfp4_bf16_to_fp8_rows_f32",
     "mxfp4_fp8_block_gemm",
+    "mxfp4_fp8_gated_gemm",
+    "mxfp4_fp8_gated_gemm_workspace",
+    "mxfp4_fp8_gated_gemm_backward",
+    "mxfp4_fp8_gated_gemm_backward_workspace",
+    "mxfp4_fp8_block_gemm_act",
+    "mxfp4_act_rows_backward",
+    "mxfp4_act_rows_backward_workspace",
     "mxfp4_combine_rows",
     "mxfp4_combine_rows_backward",
     "mxfp4_cols_scale_capacity",
@@ -164,6 +183,20 @@ def load_library(path: str = LIB_PATH):
     lib.mxfp4_bf16_to_fp8_rows_f32.restype = st
     lib.mxfp4_fp8_block_gemm.argtypes = [P, P, P, P, P, P, I32, I64, I64, I64, P]
     lib.mxfp4_fp8_block_gemm.restype = st
+    lib.mxfp4_fp8_gated_gemm.argtypes = [P] * 11 + [I32, I64, I64, I64, I32, P]
+    lib.mxfp4_fp8_gated_gemm.restype = st
+    lib.mxfp4_fp8_gated_gemm_workspace.argtypes = [I32, I64, I64, I64]
+    lib.mxfp4_fp8_gated_gemm_workspace.restype = I64
+    lib.mxfp4_fp8_gated_gemm_backward.argtypes = [P] * 11 + [I32, I64, I64, I64, I32, P]
+    lib.mxfp4_fp8_gated_gemm_backward.restype = st
+    lib.mxfp4_fp8_gated_gemm_backward_workspace.argtypes = [I32, I64, I64, I64]
+    lib.mxfp4_fp8_gated_gemm_backward_workspace.restype = I64
+    lib.mxfp4_fp8_block_gemm_act.argtypes = [P] * 9 + [I32, I64, I64, I64, I32, P]
+    lib.mxfp4_fp8_block_gemm_act.restype = st
+    lib.mxfp4_act_rows_backward.argtypes = [P] * 8 + [I32, I64, I64, I32, P]
+    lib.mxfp4_act_rows_backward.restype = st
+    lib.mxfp4_act_rows_backward_workspace.argtypes = [I32, I64, I64]
+    lib.mxfp4_act_rows_backward_workspace.restype = I64
     lib.mxfp4_combine_rows.argtypes = [P, P, P, P, P, I64, I32, I64, I64, P]
     lib.mxfp4_combine_rows.restype = st
     lib.mxfp4_combine_rows_backward.argtypes = [P, P, P, P, P, P, I64, I32, I64, I64, P]
@@ -614,6 +647,135 @@ def mxfp4_fp8_block_gemm(a, a_scales, w, w_scales, y, offs, G=None, M_cap=None, 
                                         (w, G * N * K, "w", _FP8), (w_scales, 4 * G * nb * kb, "w_scales", _F32),
                                         (y, 2 * M_cap * N, "y", _B16), (offs, 4 * (G + 1), "group_offsets", _I32)))
     _check(load_library().mxfp4_fp8_block_gemm(*at, G, M_cap, N, K, _stream(stream)), "mxfp4_fp8_block_gemm")
+
+
+def _take_here(what: str, args):
+    """_take, and every tensor has to be on the current device, whose stream the call goes to."""
+    at = _take(what, args)
+    here = None
+    for t, _, name, _ in args:
+        if t is None or isinstance(t, int):
+            continue
+        if here is None:
+            import torch
+            here = _device() if _device is not None else torch.cuda.current_device()
+        if t.get_device() != here:
+            raise ValueError(f"{what}: {name} is on cuda:{t.get_device()}, the current device is cuda:{here}")
+    return at
+
+
+_ACTS = {"none": MXFP4_ACT_NONE, "relu": MXFP4_ACT_RELU, "silu": MXFP4_ACT_SILU, "gelu": MXFP4_ACT_GELU,
+         "gelu_tanh": MXFP4_ACT_GELU_TANH}
+
+
+def _act(act) -> int:
+    if isinstance(act, str) and act not in _ACTS:
+        raise ValueError(f"act must be one of {', '.join(map(repr, _ACTS))}, got {act!r}")
+    return _ACTS.get(act, act)
+
+
+def _ffn_dims(a, w, offs, G, M_cap, N, K, parts=1):
+    """G, M_cap, N (the features of a part) and K, from the tensors where they are not given."""
+    if G is None:
+        G = offs.numel() - 1
+    if M_cap is None or K is None:
+        shape = a.shape
+        M_cap = shape[0] if M_cap is None else M_cap
+        K = shape[1] if K is None else K
+    if N is None:
+        shape = w.shape
+        N = shape[-2] if len(shape) > 3 or parts == 1 else shape[-2] // parts
+    return int(G), int(M_cap), int(N), int(K)
+
+
+@functools.lru_cache(maxsize=4096)
+def _ffn_workspace(name: str, *sizes: int) -> int:
+    return int(getattr(load_library(), name)(*sizes))
+
+
+def mxfp4_fp8_gated_gemm_workspace(G: int, M_cap: int, I: int, K: int) -> int:
+    """Bytes of workspace of mxfp4_fp8_gated_gemm with FP8 outputs; -1 for invalid sizes."""
+    return _ffn_workspace("mxfp4_fp8_gated_gemm_workspace", int(G), int(M_cap), int(I), int(K))
+
+
+def mxfp4_fp8_gated_gemm_backward_workspace(G: int, M_cap: int, I: int, K: int) -> int:
+    """Bytes of workspace of mxfp4_fp8_gated_gemm_backward with FP8 outputs; -1 for invalid sizes."""
+    return _ffn_workspace("mxfp4_fp8_gated_gemm_backward_workspace", int(G), int(M_cap), int(I), int(K))
+
+
+def mxfp4_act_rows_backward_workspace(G: int, M_cap: int, N: int) -> int:
+    """Bytes of workspace of mxfp4_act_rows_backward with bias gradients; -1 for invalid sizes."""
+    return _ffn_workspace("mxfp4_act_rows_backward_workspace", int(G), int(M_cap), int(N))
+
+
+def mxfp4_fp8_gated_gemm(a, a_scales, w, w_scales, offs, out=None, q=None, q_scales=None, h=None, bias=None,
+                         workspace=None, act="silu", G=None, M_cap=None, I=None, K=None, stream=None):
+    """act(h[:, :I]) * h[:, I:] of h = a w^T + bias: E4M3 a [M_cap, K] (+ FP32 [M_cap, ceil(K/128)])
+    and per-expert E4M3 w [G, 2, I, K] or [G, 2 I, K], gate before up (+ FP32 [G, 2, ceil(I/128),
+    ceil(K/128)]), bias [G, 2 I] float32.  Outputs: out [M_cap, I] BF16, or q [M_cap, I] E4M3 with
+    FP32 q_scales [M_cap, ceil(I/128)], or both; h [M_cap, 2 I] BF16 for the gradient (see the
+    header).  act: "silu", "gelu", "gelu_tanh", "relu" or "none"."""
+    G, M_cap, I, K = _ffn_dims(a, w, offs, G, M_cap, I, K, 2)
+    nb, kb = (I + 127) // 128, (K + 127) // 128
+    need = _ffn_workspace("mxfp4_fp8_gated_gemm_workspace", G, M_cap, I, K) if q is not None else 0
+    at = _take_here("mxfp4_fp8_gated_gemm", (
+        (a, M_cap * K, "a", _FP8), (a_scales, 4 * M_cap * kb, "a_scales", _F32), (w, 2 * G * I * K, "w", _FP8),
+        (w_scales, 8 * G * nb * kb, "w_scales", _F32), (bias, 8 * G * I, "bias", _F32),
+        (out, 2 * M_cap * I, "out", _B16), (q, M_cap * I, "q", _FP8), (q_scales, 4 * M_cap * nb, "q_scales", _F32),
+        (h, 4 * M_cap * I, "h", _B16), (workspace, need, "workspace", _WORK),
+        (offs, 4 * (G + 1), "group_offsets", _I32)))
+    _check(load_library().mxfp4_fp8_gated_gemm(*at, G, M_cap, I, K, _act(act), _stream(stream)),
+           "mxfp4_fp8_gated_gemm")
+
+
+def mxfp4_fp8_gated_gemm_backward(a, a_scales, w, w_scales, h, offs, dh=None, dq=None, dq_scales=None,
+                                  out=None, workspace=None, act="silu", G=None, M_cap=None, I=None, K=None, stream=None):
+    """The gradient of h from E4M3 a [M_cap, K], the gradient behind the down projection, and that
+    projection's transposed weights w [G, I, K]; h [M_cap, 2 I] as mxfp4_fp8_gated_gemm left it.
+    Outputs: dh [M_cap, 2 I] BF16 (may be h), or dq [M_cap, 2 I] E4M3 with FP32 dq_scales
+    [M_cap, 2 I / 128], or both; out [M_cap, I] BF16: the forward's output again (see the header)."""
+    G, M_cap, I, K = _ffn_dims(a, w, offs, G, M_cap, I, K)
+    nb, kb, n = (I + 127) // 128, (K + 127) // 128, 2 * M_cap * I
+    need = _ffn_workspace("mxfp4_fp8_gated_gemm_backward_workspace", G, M_cap, I, K) if dq is not None else 0
+    at = _take_here("mxfp4_fp8_gated_gemm_backward", (
+        (a, M_cap * K, "a", _FP8), (a_scales, 4 * M_cap * kb, "a_scales", _F32), (w, G * I * K, "w", _FP8),
+        (w_scales, 4 * G * nb * kb, "w_scales", _F32), (h, 2 * n, "h", _B16), (dh, 2 * n, "dh", _B16),
+        (dq, n, "dq", _FP8), (dq_scales, 4 * M_cap * ((2 * I + 127) // 128), "dq_scales", _F32), (out, n, "out", _B16),
+        (workspace, need, "workspace", _WORK), (offs, 4 * (G + 1), "group_offsets", _I32)))
+    _check(load_library().mxfp4_fp8_gated_gemm_backward(*at, G, M_cap, I, K, _act(act), _stream(stream)),
+           "mxfp4_fp8_gated_gemm_backward")
+
+
+def mxfp4_fp8_block_gemm_act(a, a_scales, w, w_scales, y, offs, bias=None, residual=None, pre=None, act="none",
+                             G=None, M_cap=None, N=None, K=None, stream=None):
+    """mxfp4_fp8_block_gemm with an epilogue: y = act(a w^T + bias) + residual, bias [G, N] float32,
+    residual [M_cap, N] BF16 (may be y); pre [M_cap, N] BF16: a w^T + bias, for the gradient (see
+    the header)."""
+    G, M_cap, N, K = _ffn_dims(a, w, offs, G, M_cap, N, K)
+    nb, kb, n = (N + 127) // 128, (K + 127) // 128, 2 * M_cap * N
+    at = _take_here("mxfp4_fp8_block_gemm_act", (
+        (a, M_cap * K, "a", _FP8), (a_scales, 4 * M_cap * kb, "a_scales", _F32), (w, G * N * K, "w", _FP8),
+        (w_scales, 4 * G * nb * kb, "w_scales", _F32), (bias, 4 * G * N, "bias", _F32),
+        (residual, n, "residual", _B16), (pre, n, "pre", _B16), (y, n, "y", _B16),
+        (offs, 4 * (G + 1), "group_offsets", _I32)))
+    _check(load_library().mxfp4_fp8_block_gemm_act(*at, G, M_cap, N, K, _act(act), _stream(stream)),
+           "mxfp4_fp8_block_gemm_act")
+
+
+def mxfp4_act_rows_backward(dout, pre, offs, dpre=None, q=None, q_scales=None, dbias=None, workspace=None,
+                            act="none", G=None, M_cap=None, N=None, stream=None):
+    """dpre = dout * act'(pre) of BF16 rows [M_cap, N] (pre may be None for "none"), as BF16 dpre
+    (may be dout or pre) or as E4M3 q with FP32 q_scales [M_cap, ceil(N/128)] or both, and the
+    bias gradient dbias [G, N] float32, the sums over each expert's rows (see the header)."""
+    G, M_cap, N = _dims(dout, offs, G, M_cap, N)
+    n = 2 * M_cap * N
+    need = _ffn_workspace("mxfp4_act_rows_backward_workspace", G, M_cap, N) if dbias is not None else 0
+    at = _take_here("mxfp4_act_rows_backward", (
+        (dout, n, "dout", _B16), (pre, n, "pre", _B16), (dpre, n, "dpre", _B16), (q, M_cap * N, "q", _FP8),
+        (q_scales, 4 * M_cap * ((N + 127) // 128), "q_scales", _F32), (dbias, 4 * G * N, "dbias", _F32),
+        (workspace, need, "workspace", _WORK), (offs, 4 * (G + 1), "group_offsets", _I32)))
+    _check(load_library().mxfp4_act_rows_backward(*at, G, M_cap, N, _act(act), _stream(stream)),
+           "mxfp4_act_rows_backward")
 
 
 def mxfp4_combine_rows(y, pos, out, weights=None, base=None, T=None, k=None, M_cap=None, K=None, stream=None):

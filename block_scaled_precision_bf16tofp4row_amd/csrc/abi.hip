@@ -1,6 +1,7 @@
 // abi.hip -- the C ABI of libmxfp4cvt (declared in include/mxfp4cvt.h): synchronous
 // argument validation, then the call's kernel launches on the caller's stream (one per
-// call, three for the NVFP4 quantizer, two for an expert map of many slots), all through
+// call, three for the NVFP4 quantizer, two for an expert map of many slots, for FP8 rows of a
+// gated product of few rows and for bias gradients of many rows), all through
 // launch_kernel.
 #include <math.h>
 #include <stdlib.h>
@@ -47,6 +48,20 @@ hipError_t launch_fp8_rows_f32(const uint16_t*, uint8_t*, float*, const int32_t*
                                hipStream_t);
 hipError_t launch_block_gemm(const uint8_t*, const float*, const uint8_t*, const float*, uint16_t*, const int32_t*,
                              int32_t, int64_t, int64_t, int64_t, hipStream_t);
+int64_t gated_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K);
+int64_t gated_backward_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K);
+hipError_t launch_gated_gemm(const uint8_t*, const float*, const uint8_t*, const float*, const float*, uint16_t*,
+                             uint8_t*, float*, uint16_t*, float*, const int32_t*, int32_t, int64_t, int64_t, int64_t,
+                             int, hipStream_t);
+hipError_t launch_gated_gemm_backward(const uint8_t*, const float*, const uint8_t*, const float*, const uint16_t*,
+                                      uint16_t*, uint8_t*, float*, uint16_t*, float*, const int32_t*, int32_t, int64_t,
+                                      int64_t, int64_t, int, hipStream_t);
+hipError_t launch_block_gemm_act(const uint8_t*, const float*, const uint8_t*, const float*, const float*,
+                                 const uint16_t*, uint16_t*, uint16_t*, const int32_t*, int32_t, int64_t, int64_t,
+                                 int64_t, int, hipStream_t);
+int64_t act_rows_workspace(int32_t G, int64_t M_cap, int64_t N);
+hipError_t launch_act_rows_backward(const uint16_t*, const uint16_t*, uint16_t*, uint8_t*, float*, float*, float*,
+                                    const int32_t*, int32_t, int64_t, int64_t, int, hipStream_t);
 hipError_t launch_combine(const uint16_t*, const int32_t*, const float*, const uint16_t*, uint16_t*, int64_t, int32_t,
                           int64_t, int64_t, hipStream_t);
 hipError_t launch_combine_backward(const uint16_t*, const uint16_t*, const int32_t*, const float*, uint16_t*, float*,
@@ -101,6 +116,23 @@ mxfp4_status check_route(int64_t T, int32_t E, int32_t k, int32_t score, float s
         return MXFP4_ERR_SHAPE;
     return isfinite(scale) ? MXFP4_OK : MXFP4_ERR_SHAPE;
 }
+
+// A product of E4M3 operands with FP32 block scales: N features of K elements, in `parts` parts.
+mxfp4_status check_product(int32_t G, int64_t M_cap, int64_t N, int64_t K, int parts)
+{
+    mxfp4_status st = check_shape(G, M_cap, K, 16);
+    if (st != MXFP4_OK)
+        return st;
+    if (K > kMaxGemmDim || N <= 0 || N % 8 != 0 || N > kMaxGemmDim / parts)
+        return MXFP4_ERR_SHAPE;
+    if (M_cap > 0 && parts * N > kMaxElems / M_cap)  // output elements
+        return MXFP4_ERR_SHAPE;
+    if ((int64_t)G > kMaxElems / (parts * N * K))     // weight elements
+        return MXFP4_ERR_SHAPE;
+    return MXFP4_OK;
+}
+
+bool check_act(int32_t act) { return act >= MXFP4_ACT_NONE && act <= MXFP4_ACT_GELU_TANH; }
 
 mxfp4_status from_hip(hipError_t e) { return e == hipSuccess ? MXFP4_OK : MXFP4_ERR_HIP; }
 
@@ -522,6 +554,130 @@ mxfp4_status mxfp4_fp8_block_gemm(const uint8_t* a_e4m3, const float* a_scales, 
         return MXFP4_OK;
     return from_hip(mxfp4::launch_block_gemm(a_e4m3, a_scales, w_e4m3, w_scales, y_bf16, group_offsets, G, M_cap, N,
                                              K, stream));
+}
+
+int64_t mxfp4_fp8_gated_gemm_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
+{
+    return check_product(G, M_cap, I, K, 2) == MXFP4_OK ? mxfp4::gated_workspace(G, M_cap, I, K) : -1;
+}
+
+mxfp4_status mxfp4_fp8_gated_gemm(const uint8_t* a_e4m3, const float* a_scales, const uint8_t* w_e4m3,
+                                  const float* w_scales, const float* bias, uint16_t* out_bf16, uint8_t* q_e4m3,
+                                  float* q_scales, uint16_t* h_bf16, void* workspace, const int32_t* group_offsets,
+                                  int32_t G, int64_t M_cap, int64_t I, int64_t K, int32_t act, hipStream_t stream)
+{
+    if (!a_e4m3 || !a_scales || !w_e4m3 || !w_scales || !group_offsets || (!out_bf16 && !q_e4m3) ||
+        !q_e4m3 != !q_scales)
+        return MXFP4_ERR_NULL;
+    mxfp4_status st = check_product(G, M_cap, I, K, 2);
+    if (st != MXFP4_OK)
+        return st;
+    if (!check_act(act) || (q_e4m3 && I % 16 != 0))
+        return MXFP4_ERR_SHAPE;
+    if (q_e4m3 && !workspace && mxfp4::gated_workspace(G, M_cap, I, K) > 0)
+        return MXFP4_ERR_NULL;
+    if (!aligned(a_e4m3, 16) || !aligned(a_scales, 16) || !aligned(w_e4m3, 16) || !aligned(w_scales, 16) ||
+        !aligned(bias, 16) || !aligned(out_bf16, 16) || !aligned(q_e4m3, 16) || !aligned(q_scales, 16) ||
+        !aligned(h_bf16, 16) || !aligned(workspace, 16) || !aligned(group_offsets, 4))
+        return MXFP4_ERR_ALIGN;
+    if (M_cap == 0)
+        return MXFP4_OK;
+    return from_hip(mxfp4::launch_gated_gemm(a_e4m3, a_scales, w_e4m3, w_scales, bias, out_bf16, q_e4m3, q_scales,
+                                             h_bf16, static_cast<float*>(workspace), group_offsets, G, M_cap, I, K,
+                                             act, stream));
+}
+
+int64_t mxfp4_fp8_gated_gemm_backward_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
+{
+    return check_product(G, M_cap, I, K, 1) == MXFP4_OK && I <= kMaxGemmDim / 2
+               ? mxfp4::gated_backward_workspace(G, M_cap, I, K) : -1;
+}
+
+mxfp4_status mxfp4_fp8_gated_gemm_backward(const uint8_t* a_e4m3, const float* a_scales, const uint8_t* w_e4m3,
+                                           const float* w_scales, const uint16_t* h_bf16, uint16_t* dh_bf16,
+                                           uint8_t* dq_e4m3, float* dq_scales, uint16_t* out_bf16, void* workspace,
+                                           const int32_t* group_offsets, int32_t G, int64_t M_cap, int64_t I,
+                                           int64_t K, int32_t act, hipStream_t stream)
+{
+    if (!a_e4m3 || !a_scales || !w_e4m3 || !w_scales || !h_bf16 || !group_offsets || (!dh_bf16 && !dq_e4m3) ||
+        !dq_e4m3 != !dq_scales)
+        return MXFP4_ERR_NULL;
+    mxfp4_status st = check_product(G, M_cap, I, K, 1);
+    if (st != MXFP4_OK)
+        return st;
+    if (!check_act(act) || I > kMaxGemmDim / 2 || (M_cap > 0 && 2 * I > kMaxElems / M_cap) ||
+        (dq_e4m3 && I % 128 != 0))
+        return MXFP4_ERR_SHAPE;
+    if (dq_e4m3 && !workspace && mxfp4::gated_backward_workspace(G, M_cap, I, K) > 0)
+        return MXFP4_ERR_NULL;
+    if (!aligned(a_e4m3, 16) || !aligned(a_scales, 16) || !aligned(w_e4m3, 16) || !aligned(w_scales, 16) ||
+        !aligned(h_bf16, 16) || !aligned(dh_bf16, 16) || !aligned(dq_e4m3, 16) || !aligned(dq_scales, 16) ||
+        !aligned(out_bf16, 16) || !aligned(workspace, 16) || !aligned(group_offsets, 4))
+        return MXFP4_ERR_ALIGN;
+    if (M_cap == 0)
+        return MXFP4_OK;
+    return from_hip(mxfp4::launch_gated_gemm_backward(a_e4m3, a_scales, w_e4m3, w_scales, h_bf16, dh_bf16, dq_e4m3,
+                                                      dq_scales, out_bf16, static_cast<float*>(workspace),
+                                                      group_offsets, G, M_cap, I, K, act, stream));
+}
+
+mxfp4_status mxfp4_fp8_block_gemm_act(const uint8_t* a_e4m3, const float* a_scales, const uint8_t* w_e4m3,
+                                      const float* w_scales, const float* bias, const uint16_t* residual_bf16,
+                                      uint16_t* pre_bf16, uint16_t* y_bf16, const int32_t* group_offsets, int32_t G,
+                                      int64_t M_cap, int64_t N, int64_t K, int32_t act, hipStream_t stream)
+{
+    if (!a_e4m3 || !a_scales || !w_e4m3 || !w_scales || !y_bf16 || !group_offsets)
+        return MXFP4_ERR_NULL;
+    mxfp4_status st = check_product(G, M_cap, N, K, 1);
+    if (st != MXFP4_OK)
+        return st;
+    if (!check_act(act))
+        return MXFP4_ERR_SHAPE;
+    if (!aligned(a_e4m3, 16) || !aligned(a_scales, 16) || !aligned(w_e4m3, 16) || !aligned(w_scales, 16) ||
+        !aligned(bias, 16) || !aligned(residual_bf16, 16) || !aligned(pre_bf16, 16) || !aligned(y_bf16, 16) ||
+        !aligned(group_offsets, 4))
+        return MXFP4_ERR_ALIGN;
+    if (M_cap == 0)
+        return MXFP4_OK;
+    return from_hip(mxfp4::launch_block_gemm_act(a_e4m3, a_scales, w_e4m3, w_scales, bias, residual_bf16, pre_bf16,
+                                                 y_bf16, group_offsets, G, M_cap, N, K, act, stream));
+}
+
+// Rows of N elements of G experts.
+static mxfp4_status check_act_rows(int32_t G, int64_t M_cap, int64_t N)
+{
+    const mxfp4_status st = check_shape(G, M_cap, N, 8);
+    return st == MXFP4_OK && N > kMaxGemmDim ? MXFP4_ERR_SHAPE : st;
+}
+
+int64_t mxfp4_act_rows_backward_workspace(int32_t G, int64_t M_cap, int64_t N)
+{
+    return check_act_rows(G, M_cap, N) == MXFP4_OK ? mxfp4::act_rows_workspace(G, M_cap, N) : -1;
+}
+
+mxfp4_status mxfp4_act_rows_backward(const uint16_t* dout_bf16, const uint16_t* pre_bf16, uint16_t* dpre_bf16,
+                                     uint8_t* q_e4m3, float* q_scales, float* dbias, void* workspace,
+                                     const int32_t* group_offsets, int32_t G, int64_t M_cap, int64_t N, int32_t act,
+                                     hipStream_t stream)
+{
+    if (!dout_bf16 || !group_offsets || (!dpre_bf16 && !q_e4m3 && !dbias) || !q_e4m3 != !q_scales ||
+        (!pre_bf16 && act != MXFP4_ACT_NONE))
+        return MXFP4_ERR_NULL;
+    mxfp4_status st = check_act_rows(G, M_cap, N);
+    if (st != MXFP4_OK)
+        return st;
+    if (!check_act(act) || (q_e4m3 && N % 16 != 0))
+        return MXFP4_ERR_SHAPE;
+    if (dbias && !workspace && mxfp4::act_rows_workspace(G, M_cap, N) > 0)
+        return MXFP4_ERR_NULL;
+    if (!aligned(dout_bf16, 16) || !aligned(pre_bf16, 16) || !aligned(dpre_bf16, 16) || !aligned(q_e4m3, 16) ||
+        !aligned(q_scales, 16) || !aligned(dbias, 16) || !aligned(workspace, 16) || !aligned(group_offsets, 4))
+        return MXFP4_ERR_ALIGN;
+    if (M_cap == 0 && !dbias)
+        return MXFP4_OK;
+    return from_hip(mxfp4::launch_act_rows_backward(dout_bf16, pre_bf16, dpre_bf16, q_e4m3, q_scales, dbias,
+                                                    static_cast<float*>(workspace), group_offsets, G, M_cap, N, act,
+                                                    stream));
 }
 
 mxfp4_status mxfp4_combine_rows(const uint16_t* y_bf16, const int32_t* pos, const float* weights,

@@ -1,0 +1,454 @@
+// block_ffn.hip -- the expert-grouped FP8 product with FP32 block scales (block_tile.h) with
+// what a feed-forward layer does to its sums in the same kernel.
+//
+// With p = A W_g^T (the sums of block_gemm.hip, FP32, not rounded), g the row's expert:
+//   gated:     W_g = [Wg; Wu], h = [hg, hu] = p + bias_g, out = act(hg) hu.  A tile has the same
+//              features of both halves, so out needs no other workgroup.
+//   gradient:  p the gradient of out (A the gradient behind the down projection, W its
+//              transpose), h read back: dh = [p hu act'(hg), p act(hg)], and out again.
+//   dense:     y = act(p + bias_g) + residual.
+// Results leave as BF16, rounded once, or (gated, gradient) as E4M3 rows with an FP32 scale per
+// 1x128 block, made from the FP32 values, where the product that follows takes them.
+//
+// The sums go through LDS as FP32, a tile's rows in one phase or two: a thread then has eight
+// consecutive features of a row, 16 lanes a scale block, and its loads and stores are 16 bytes
+// in whole lines.
+#include "activation.h"
+#include "block_tile.h"
+
+namespace mxfp4 {
+
+// What a call reads and writes besides the product's operands.  NULL: not wanted.
+struct Ffn {
+    const float* bias;                            // [G, C]; C = 2 N (gated), N (dense)
+    const uint16_t* h;                            // gradient: [M, 2 N].  dense: the residual [M, N]
+    uint16_t* rows;                               // gated: h [M, 2 N].  gradient: dh [M, 2 N].  dense: y [M, N]
+    uint16_t* out;                                // gated, gradient: out [M, N].  dense: p + bias [M, N]
+    uint8_t* q;                                   // E4M3 of out (gated), of dh (gradient)
+    float* q_scales;
+    float* sums;                                  // those values in FP32 instead (kernels for few rows)
+    int act;
+};
+
+enum Kind { kGated, kGradient, kDense };
+
+// The epilogue of one thread: eight features, col .. col + 7, of rows of a tile.
+template <int KIND>
+struct Epilogue {
+    static constexpr int kParts = KIND == kGated ? 2 : 1;
+    // Values of a row in `rows` and in q, per feature.
+    static constexpr int kWide = KIND == kDense ? 1 : 2, kQuant = KIND == kGradient ? 2 : 1;
+    struct In {
+        u32x4 h[2];
+    };
+
+    const Ffn& f;
+    const uint32_t N;
+    const uint32_t col;                           // of a part, in [0, N) or past it
+    const bool there;
+    __amdgpu_buffer_rsrc_t rh, rrows, rout, rq, rqs, rsums;
+    float bias[kParts][8];
+
+    __device__ __forceinline__ Epilogue(const Ffn& f_, const TileAt& at, uint32_t N_, uint32_t c)
+        : f(f_), N(N_), col((uint32_t)at.n0 + 8 * c), there((int)(8 * c) < at.cols)
+    {
+        const uint64_t row = (uint64_t)at.rows;
+        if (KIND == kGradient || (KIND == kDense && f.h))
+            rh = strip_rsrc(f.h + at.row0 * kWide * N, row * kWide * N * 2);
+        if (f.rows)
+            rrows = strip_rsrc(f.rows + at.row0 * kWide * N, row * kWide * N * 2);
+        if (f.out)
+            rout = strip_rsrc(f.out + at.row0 * N, row * N * 2);
+        if (KIND != kDense && f.q) {
+            rq = strip_rsrc(f.q + at.row0 * kQuant * N, row * kQuant * N);
+            rqs = strip_rsrc(f.q_scales + at.row0 * blocks(), row * blocks() * 4);
+        }
+        if (KIND != kDense && f.sums)
+            rsums = strip_rsrc(f.sums + at.row0 * kQuant * N, row * kQuant * N * 4);
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                bias[p][i] = 0.0f;
+        if (KIND != kGradient && f.bias && there) {
+            const float* const from = f.bias + ((int64_t)at.g * kParts) * N + col;
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const f32x4 b = *reinterpret_cast<const f32x4*>(from + p * (int64_t)N + 4 * j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        bias[p][4 * j + e] = b[e];
+                }
+        }
+    }
+    __device__ __forceinline__ uint32_t blocks() const { return (kQuant * N + 127) / 128; }
+
+    // The byte offset of the thread's features of part p in a row of `wide` parts of elements of
+    // `size` bytes; out of range where there are none.
+    __device__ __forceinline__ int at_byte(uint32_t row, int wide, int p, int size) const
+    {
+        return there ? (int)((row * wide * N + p * N + col) * size) : (int)kOutOfRange;
+    }
+    // What the row needs of memory.
+    __device__ __forceinline__ void fetch(uint32_t row, In& in) const
+    {
+        if constexpr (KIND == kGradient) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                in.h[p] = __builtin_amdgcn_raw_buffer_load_b128(rh, at_byte(row, 2, p, 2), 0, 0);
+        } else if constexpr (KIND == kDense) {
+            if (f.h)
+                in.h[0] = __builtin_amdgcn_raw_buffer_load_b128(rh, at_byte(row, 1, 0, 2), 0, 0);
+        }
+    }
+    static __device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, int off, u32x4 v)
+    {
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
+    }
+    // E4M3 bytes (all 16 lanes of a block take part), or FP32 sums.
+    template <bool kTile>
+    __device__ __forceinline__ void quantized(uint32_t row, int p, const float (&v)[8]) const
+    {
+        if constexpr (kTile) {
+            if (f.q) {
+                float scale;
+                const u32x2 b = to_fp8(v, scale);
+                __builtin_amdgcn_raw_buffer_store_b64(b, rq, at_byte(row, kQuant, p, 1), 0, 0);
+                const uint32_t s = (row * blocks() + (p * N + col) / 128) * 4;
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(scale), rqs,
+                                                      there && col % 128 == 0 ? (int)s : (int)kOutOfRange, 0, 0);
+            }
+        } else if (f.sums) {
+            const int off = at_byte(row, kQuant, p, 4);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const f32x4 s = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+                put(rsums, off + 16 * i, __builtin_bit_cast(u32x4, s));
+            }
+        }
+    }
+    // Row `row` of the tile: the sums of each part's eight features.
+    template <bool kTile>
+    __device__ __forceinline__ void apply(uint32_t row, float (&v)[kParts][8], const In& in) const
+    {
+        float slope[8];
+#pragma unroll
+        for (int p = 0; p < kParts; ++p)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[p][i] += bias[p][i];
+        if constexpr (KIND == kGated) {
+            if (f.rows) {
+                put(rrows, at_byte(row, 2, 0, 2), to_bf16(v[0]));
+                put(rrows, at_byte(row, 2, 1, 2), to_bf16(v[1]));
+            }
+            activate8<false>(f.act, v[0], slope);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[0][i] *= v[1][i];
+            if (f.out)
+                put(rout, at_byte(row, 1, 0, 2), to_bf16(v[0]));
+            quantized<kTile>(row, 0, v[0]);
+        } else if constexpr (KIND == kGradient) {
+            float a[8], u[8];
+            from_bf16(in.h[0], a);
+            from_bf16(in.h[1], u);
+            activate8<true>(f.act, a, slope);
+            float dg[8], du[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dg[i] = v[0][i] * u[i] * slope[i];
+                du[i] = v[0][i] * a[i];
+                u[i] *= a[i];
+            }
+            if (f.out)
+                put(rout, at_byte(row, 1, 0, 2), to_bf16(u));
+            if (f.rows) {
+                put(rrows, at_byte(row, 2, 0, 2), to_bf16(dg));
+                put(rrows, at_byte(row, 2, 1, 2), to_bf16(du));
+            }
+            quantized<kTile>(row, 0, dg);
+            quantized<kTile>(row, 1, du);
+        } else {
+            if (f.out)
+                put(rout, at_byte(row, 1, 0, 2), to_bf16(v[0]));
+            activate8<false>(f.act, v[0], slope);
+            if (f.h) {
+                from_bf16(in.h[0], slope);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[0][i] += slope[i];
+            }
+            put(rrows, at_byte(row, 1, 0, 2), to_bf16(v[0]));
+        }
+    }
+};
+
+template <class W, int KIND>
+__global__ __launch_bounds__(64 * W::kWM * W::kWN, W::kD == 2 ? 2 : 1) void ffn_tile_kernel(
+    const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
+    const float* __restrict__ sw, Ffn f, const int32_t* __restrict__ offs, int G, int64_t N, int64_t K, uint32_t ntn)
+{
+    constexpr int kParts = Epilogue<KIND>::kParts;
+    constexpr int WM = W::kWM, MT = W::kMT, NT = W::kNT, TM = W::TM, TN = W::TN, kThreads = 64 * W::kWaves;
+    // separate arrays: what is loaded into one does not hold up reads of another
+    __shared__ __attribute__((aligned(16))) uint8_t lds0[W::kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds1[W::kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds2[W::kBuf2];
+    __shared__ __attribute__((aligned(16))) uint8_t lds3[W::kBuf3];
+    typename W::State t;
+    TileAt at;
+    if (!tile_sums<W, kParts>(lds0, lds1, lds2, lds3, a, sa, w, sw, offs, G, N, K, ntn, t, at))
+        return;                                   // uniform over the workgroup
+
+    // Groups of 16 rows, those of wave row wm one after the other; kGroups of them fit the LDS.
+    // 16-byte chunk c of row r is at chunk c ^ (r % 16).
+    constexpr int kGroup = 16 * TN * 4, kIn0 = W::kBuf / kGroup, kIn2 = W::kBuf2 / kGroup, kIn3 = W::kBuf3 / kGroup;
+    constexpr int kGroups = 2 * kIn0 + kIn2 + kIn3, kPhases = TM / 16 <= kGroups ? 1 : 2;
+    constexpr int MP = MT / kPhases, kRows = TM / kPhases;
+    static_assert(kIn0 >= 1 && kRows / 16 <= kGroups && MT % kPhases == 0, "a phase's rows fit the LDS");
+    auto place = [&](int group) {
+        return group < kIn0             ? lds0 + group * kGroup
+               : group < 2 * kIn0        ? lds1 + (group - kIn0) * kGroup
+               : group < 2 * kIn0 + kIn2 ? lds2 + (group - 2 * kIn0) * kGroup
+                                         : lds3 + (group - 2 * kIn0 - kIn2) * kGroup;
+    };
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+    const uint32_t r = (uint32_t)(tid & 15), h = (uint32_t)(tid >> 4 & 3);
+    constexpr int kCols = TN / kParts / 8, kStep = kThreads / kCols;      // threads of a row, rows of a step
+    static_assert(kThreads % kCols == 0 && kRows % kStep == 0 && kStep % (64 / kCols) == 0 && 64 % kCols == 0, "rows");
+    const uint32_t c = (uint32_t)tid % kCols;
+    typedef Epilogue<KIND> E;
+    const E epi(f, at, (uint32_t)N, c);
+#pragma unroll
+    for (int phase = 0; phase < kPhases; ++phase) {
+        if (phase > 0)
+            meet();                               // the rows of the phase before have been read
+#pragma unroll
+        for (int m = 0; m < MP; ++m)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t chunk = (uint32_t)(4 * (NT * wn + nt)) + h;
+                *reinterpret_cast<f32x4*>(place(wm * MP + m) + r * (TN * 4) + 16 * (chunk ^ r)) =
+                    t.acc[phase * MP + m][nt];
+            }
+        // (rows of the phase: group by group; row `in` of the phase is this row of the tile)
+        auto row_of = [&](int i) {
+            const uint32_t in = (uint32_t)tid / kCols + kStep * i, group = in / 16;
+            return 16 * (MT * (group / MP) + phase * MP + group % MP) + in % 16;
+        };
+        typename E::In next;
+        epi.fetch(row_of(0), next);
+        meet();
+#pragma unroll 1
+        for (int i = 0; i < kRows / kStep; ++i) {
+            const typename E::In now = next;
+            if (i + 1 < kRows / kStep)
+                epi.fetch(row_of(i + 1), next);
+            const uint32_t in = (uint32_t)tid / kCols + kStep * i, rr = in % 16;
+            const uint8_t* const from = place(__builtin_amdgcn_readfirstlane((int)(in / 16))) + rr * (TN * 4);
+            float v[kParts][8];
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const f32x4 s = *reinterpret_cast<const f32x4*>(from + 16 * ((p * (TN / 8) + 2 * c + j) ^ rr));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[p][4 * j + e] = s[e];
+                }
+            epi.template apply<true>(row_of(i), v, now);
+        }
+    }
+}
+
+template <int MT, int KIND>
+__global__ __launch_bounds__(64 * kRowsWaves) void ffn_rows_kernel(
+    const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
+    const float* __restrict__ sw, Ffn f, const int32_t* __restrict__ offs, int G, int64_t N, int64_t K, uint32_t ntm)
+{
+    typedef RowsTile<MT> R;
+    typedef Epilogue<KIND> E;
+    constexpr int kParts = E::kParts;
+    // separate arrays: what is loaded into one does not hold up reads of another
+    __shared__ __attribute__((aligned(16))) uint8_t lds0[kRowsWaves * R::kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds1[kRowsWaves * R::kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds2[kRowsWaves * R::kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds3[kRowsWaves * R::kBuf];
+    __shared__ __attribute__((aligned(16))) typename R::Part part[kRowsWaves];
+    TileAt at;
+    if (!rows_sums<MT, kParts>(lds0, lds1, lds2, lds3, part, a, sa, w, sw, offs, G, N, K, ntm, at))
+        return;                                   // uniform over the workgroup
+    constexpr int kCols = R::TN / kParts / 8;
+    static_assert(R::TM * kCols <= 64 * kRowsWaves, "one item a thread");
+    const uint32_t row = threadIdx.x / kCols, c = threadIdx.x % kCols;
+    if (row >= R::TM)
+        return;
+    const E epi(f, at, (uint32_t)N, c);
+    typename E::In in;
+    epi.fetch(row, in);
+    float v[kParts][8];
+#pragma unroll
+    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f32x4 s = R::sum(part, row, p * (R::TN / 2) + 8 * c + 4 * j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[p][4 * j + e] = s[e];
+        }
+    epi.template apply<false>(row, v, in);
+}
+
+// FP32 rows [0, offs[G]) of `cols` values -> E4M3 rows with FP32 scales: 16 lanes of eight
+// values to a block, blocks of a row one after the other.
+__global__ __launch_bounds__(kThreads) void quantize_sums_kernel(
+    const float* __restrict__ x, uint8_t* __restrict__ q, float* __restrict__ q_scales,
+    const int32_t* __restrict__ offs, int G, uint32_t cols, uint32_t blocks)
+{
+    const uint64_t block = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) / 16;
+    const int64_t row = (int64_t)(block / blocks);
+    const uint32_t b = (uint32_t)(block % blocks), col = 128 * b + 8 * (threadIdx.x % 16);
+    if (row >= offs[G])
+        return;                                   // (16 lanes leave together)
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (col < cols) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f32x4 s = *reinterpret_cast<const f32x4*>(x + row * cols + col + 4 * j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[4 * j + e] = s[e];
+        }
+    }
+    float scale;
+    const u32x2 bytes = to_fp8(v, scale);
+    if (col < cols)
+        *reinterpret_cast<u32x2*>(q + row * cols + col) = bytes;
+    if (threadIdx.x % 16 == 0)
+        q_scales[row * blocks + b] = scale;
+}
+
+namespace {
+
+typedef Tile<2, 4, 8, 4, 2> Tile256;
+typedef Tile<2, 4, 4, 4, 3> Tile128x256;
+typedef Tile<2, 2, 4, 4, 2> Tile128;
+typedef Tile<1, 4, 2, 4, 4> Tile32x256;
+typedef Tile<1, 4, 2, 2, 4> Tile32;
+typedef Tile<1, 4, 2, 2, 3> Tile32Shared;
+
+// The kernel of a call: the K-splitting one with 16 or 32 tokens, or a tile.
+enum Which { kRows16, kRows32, kSmall, kSmallShared, kMedium, kLarge };
+
+Which choose(int32_t G, int64_t M_cap, int64_t N, int64_t K, int parts)
+{
+    const int64_t n = parts * N;
+    const int64_t rows16 = tiles(M_cap, G, n, 16, kRowsTN), rows32 = tiles(M_cap, G, n, 32, kRowsTN);
+    if (rows16 <= 320 || (rows16 <= 512 && rows32 > 320 && K > 4096))
+        return kRows16;
+    if (rows32 <= 320)
+        return kRows32;
+    if (M_cap >= 192 * (int64_t)G && tiles(M_cap, G, n, 256, 256) >= 192)
+        return kLarge;
+    if (M_cap >= 12 * (int64_t)G && tiles(M_cap, G, n, 128, 128) >= 128)
+        return kMedium;
+    return tiles(M_cap, G, n, 32, 128) <= 256 ? kSmall : kSmallShared;
+}
+
+template <int KIND>
+hipError_t launch_ffn(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, Ffn f,
+                      const int32_t* offs, int32_t G, int64_t M_cap, int64_t N, int64_t K, hipStream_t stream)
+{
+    constexpr int kParts = Epilogue<KIND>::kParts;
+    int g = G;
+    int64_t n = N, k = K;
+    uint32_t nt = 0;                              // feature tiles (tile kernel), token tiles (rows kernel)
+    void* args[] = {(void*)&a, (void*)&sa, (void*)&w, (void*)&sw, (void*)&f, (void*)&offs, (void*)&g,
+                    (void*)&n, (void*)&k, (void*)&nt};
+    auto tile = [&](auto W, const void* kernel) {
+        typedef decltype(W) T;
+        nt = (uint32_t)((N + T::TN / kParts - 1) / (T::TN / kParts));
+        const int64_t grid = tiles(M_cap, G, N, T::TM, T::TN / kParts);
+        f.sums = nullptr;
+        return grid > 0x7FFFFFFF ? hipErrorInvalidValue
+                                 : launch_kernel(kernel, dim3((unsigned)grid), dim3(64 * T::kWaves), args, stream);
+    };
+    auto rows = [&](int TM, const void* kernel) {
+        nt = (uint32_t)tiles(M_cap, G, 1, TM, 1);
+        const int64_t grid = tiles(M_cap, G, N, TM, kRowsTN / kParts);
+        const bool then = f.q != nullptr;
+        hipError_t e = launch_kernel(kernel, dim3((unsigned)grid), dim3(64 * kRowsWaves), args, stream, !then);
+        if (e != hipSuccess || !then)
+            return e;
+        uint32_t cols = (uint32_t)(Epilogue<KIND>::kQuant * N), blocks = (cols + 127) / 128;
+        void* more[] = {(void*)&f.sums, (void*)&f.q, (void*)&f.q_scales, (void*)&offs, (void*)&g, (void*)&cols,
+                        (void*)&blocks};
+        const int64_t lanes = M_cap * blocks * 16;
+        return launch_kernel((const void*)quantize_sums_kernel, dim3((unsigned)((lanes + kThreads - 1) / kThreads)),
+                             dim3(kThreads), more, stream);
+    };
+    switch (choose(G, M_cap, N, K, kParts)) {
+    case kRows16: return rows(16, (const void*)ffn_rows_kernel<1, KIND>);
+    case kRows32: return rows(32, (const void*)ffn_rows_kernel<2, KIND>);
+    case kLarge: return tile(Tile256{}, (const void*)ffn_tile_kernel<Tile256, KIND>);
+    case kMedium:
+        if constexpr (KIND == kGated)
+            return tile(Tile128x256{}, (const void*)ffn_tile_kernel<Tile128x256, KIND>);
+        else
+            return tile(Tile128{}, (const void*)ffn_tile_kernel<Tile128, KIND>);
+    default:
+        if constexpr (KIND == kGated)
+            return tile(Tile32x256{}, (const void*)ffn_tile_kernel<Tile32x256, KIND>);
+        else if (tiles(M_cap, G, N, 32, 128) <= 256)
+            return tile(Tile32{}, (const void*)ffn_tile_kernel<Tile32, KIND>);
+        else
+            return tile(Tile32Shared{}, (const void*)ffn_tile_kernel<Tile32Shared, KIND>);
+    }
+}
+
+bool splits_k(Which w) { return w == kRows16 || w == kRows32; }
+
+}  // namespace
+
+int64_t gated_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
+{
+    return splits_k(choose(G, M_cap, I, K, 2)) ? 4 * M_cap * I : 0;
+}
+int64_t gated_backward_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
+{
+    return splits_k(choose(G, M_cap, I, K, 1)) ? 8 * M_cap * I : 0;
+}
+
+hipError_t launch_gated_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, const float* bias,
+                             uint16_t* out, uint8_t* q, float* q_scales, uint16_t* h, float* work,
+                             const int32_t* offs, int32_t G, int64_t M_cap, int64_t I, int64_t K, int act,
+                             hipStream_t stream)
+{
+    const Ffn f = {bias, nullptr, h, out, q, q_scales, q ? work : nullptr, act};
+    return launch_ffn<kGated>(a, sa, w, sw, f, offs, G, M_cap, I, K, stream);
+}
+
+hipError_t launch_gated_gemm_backward(const uint8_t* dy, const float* sdy, const uint8_t* wt, const float* swt,
+                                      const uint16_t* h, uint16_t* dh, uint8_t* q, float* q_scales, uint16_t* out,
+                                      float* work, const int32_t* offs, int32_t G, int64_t M_cap, int64_t I,
+                                      int64_t K, int act, hipStream_t stream)
+{
+    const Ffn f = {nullptr, h, dh, out, q, q_scales, q ? work : nullptr, act};
+    return launch_ffn<kGradient>(dy, sdy, wt, swt, f, offs, G, M_cap, I, K, stream);
+}
+
+hipError_t launch_block_gemm_act(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw,
+                                 const float* bias, const uint16_t* residual, uint16_t* pre, uint16_t* y,
+                                 const int32_t* offs, int32_t G, int64_t M_cap, int64_t N, int64_t K, int act,
+                                 hipStream_t stream)
+{
+    const Ffn f = {bias, residual, y, pre, nullptr, nullptr, nullptr, act};
+    return launch_ffn<kDense>(a, sa, w, sw, f, offs, G, M_cap, N, K, stream);
+}
+
+}  // namespace mxfp4

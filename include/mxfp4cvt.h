@@ -331,6 +331,96 @@ mxfp4_status mxfp4_fp8_block_gemm(const uint8_t* a_e4m3, const float* a_scales, 
                                   const float* w_scales, uint16_t* y_bf16, const int32_t* group_offsets, int32_t G,
                                   int64_t M_cap, int64_t N, int64_t K, hipStream_t stream);
 
+/* ---- the feed-forward operators around that product ----
+ *
+ *     mxfp4_fp8_gated_gemm           gate and up projections, activation and product in one call
+ *     mxfp4_fp8_gated_gemm_backward  the gradient behind the down projection -> that of h
+ *     mxfp4_fp8_block_gemm_act       the product with bias, activation and residual
+ *     mxfp4_act_rows_backward        its gradient: of the rows and of the bias
+ * Operands, their limits, group_offsets and errors are mxfp4_fp8_block_gemm's; a dense layer
+ * is G = 1.  act is one of mxfp4_act (else MXFP4_ERR_SHAPE).  Outputs called optional may be
+ * NULL; rows [offs[G], M_cap) of every output keep what they hold.  Sums, biases and
+ * activations are FP32 (activations and their derivatives good to a few 2^-22 of themselves,
+ * an exponential's argument x adds (|x| + 2) 2^-24); every output is rounded once, from the
+ * FP32 value and not from another output.  The matrix cores' own rounding is about 2^-16 of a
+ * result on ordinary data.  FP8 outputs are E4M3 rows with one FP32 scale per 1x128 block,
+ * made as mxfp4_dispatch_fp8_rows makes them, but from the FP32 values: the operand of the
+ * next mxfp4_fp8_block_gemm or mxfp4_fp8_block_gemm_act.
+ * workspace: the bytes that the call's _workspace function gives (NULL where that is 0; -1
+ * for invalid sizes), not shared by calls that overlap; nothing has to be in it. */
+typedef enum {
+    MXFP4_ACT_NONE = 0,
+    MXFP4_ACT_RELU = 1,
+    MXFP4_ACT_SILU = 2,
+    MXFP4_ACT_GELU = 3,      /* x P(x), P the normal distribution */
+    MXFP4_ACT_GELU_TANH = 4  /* its approximation by a hyperbolic tangent */
+} mxfp4_act;
+
+/* The gated feed-forward product.  For the expert g owning row m and i < I:
+ *   h[m, i], h[m, I + i] = sum_k A[m, k] W[g, 0 or 1, i, k] + bias[g, 0 or 1, i]
+ *   out[m, i] = act(h[m, i]) h[m, I + i]
+ *   a_e4m3  [M_cap, K], a_scales [M_cap, ceil(K/128)].
+ *   w_e4m3  [G, 2, I, K]: gate, then up.   w_scales [G, 2, ceil(I/128), ceil(K/128)] (where I
+ *           is a multiple of 128 these are the arrays of one [G, 2 I, K] weight).
+ *   bias    [G, 2, I] FP32 (optional: 0).
+ *   out_bf16 [M_cap, I] (optional), q_e4m3 [M_cap, I] with q_scales [M_cap, ceil(I/128)]
+ *           (optional, both or none): out in either form; at least one is given.
+ *   h_bf16  [M_cap, 2 I] (optional): for the gradient.
+ *   workspace: for q, where few rows let workgroups share K.
+ *   I must be a multiple of 8, of 16 for q, and at most 2^19. */
+mxfp4_status mxfp4_fp8_gated_gemm(const uint8_t* a_e4m3, const float* a_scales, const uint8_t* w_e4m3,
+                                  const float* w_scales, const float* bias, uint16_t* out_bf16, uint8_t* q_e4m3,
+                                  float* q_scales, uint16_t* h_bf16, void* workspace, const int32_t* group_offsets,
+                                  int32_t G, int64_t M_cap, int64_t I, int64_t K, int32_t act, hipStream_t stream);
+int64_t mxfp4_fp8_gated_gemm_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K);
+
+/* Its gradient, joined to the product in front of it: with A the gradient behind the down
+ * projection and W that projection's weights transposed,
+ *   d[m, i] = sum_k A[m, k] W[g, i, k]
+ *   dh[m, i] = d[m, i] h[m, I + i] act'(h[m, i]),   dh[m, I + i] = d[m, i] act(h[m, i])
+ *   out[m, i] = act(h[m, i]) h[m, I + i]  (again: the other operand of the down projection's
+ *                                          weight gradient)
+ *   a_e4m3  [M_cap, K], a_scales [M_cap, ceil(K/128)]; w_e4m3 [G, I, K], w_scales
+ *           [G, ceil(I/128), ceil(K/128)].   h_bf16 [M_cap, 2 I] as the forward call left it.
+ *   dh_bf16 [M_cap, 2 I] (optional; may be h_bf16), dq_e4m3 [M_cap, 2 I] with dq_scales
+ *           [M_cap, 2 I / 128] (optional, both or none): dh in either form; at least one is
+ *           given.   out_bf16 [M_cap, I] (optional).
+ *   The rows' gradient is the product of dh with the up and gate weights transposed, the bias
+ *   gradient mxfp4_act_rows_backward of dh with MXFP4_ACT_NONE, the weight gradients
+ *   mxfp4_fp8_grouped_gemm_wgrad of dh's and out's column layouts.
+ *   workspace: for dq, as above.   I must be a multiple of 8, of 128 for dq (a scale block
+ *   belongs to one half of h), and at most 2^19. */
+mxfp4_status mxfp4_fp8_gated_gemm_backward(const uint8_t* a_e4m3, const float* a_scales, const uint8_t* w_e4m3,
+                                           const float* w_scales, const uint16_t* h_bf16, uint16_t* dh_bf16,
+                                           uint8_t* dq_e4m3, float* dq_scales, uint16_t* out_bf16, void* workspace,
+                                           const int32_t* group_offsets, int32_t G, int64_t M_cap, int64_t I,
+                                           int64_t K, int32_t act, hipStream_t stream);
+int64_t mxfp4_fp8_gated_gemm_backward_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K);
+
+/* mxfp4_fp8_block_gemm with an epilogue:
+ *   pre[m, n] = sum_k A[m, k] W[g, n, k] + bias[g, n],   y[m, n] = act(pre[m, n]) + residual[m, n]
+ *   bias [G, N] FP32 (optional: 0), residual_bf16 [M_cap, N] (optional: 0; may be y_bf16),
+ *   pre_bf16 [M_cap, N] (optional output, for the gradient).  The residual's gradient is y's. */
+mxfp4_status mxfp4_fp8_block_gemm_act(const uint8_t* a_e4m3, const float* a_scales, const uint8_t* w_e4m3,
+                                      const float* w_scales, const float* bias, const uint16_t* residual_bf16,
+                                      uint16_t* pre_bf16, uint16_t* y_bf16, const int32_t* group_offsets, int32_t G,
+                                      int64_t M_cap, int64_t N, int64_t K, int32_t act, hipStream_t stream);
+
+/* The gradient of act(pre) and of the bias in pre:
+ *   dpre[m, n] = dout[m, n] act'(pre[m, n]),   dbias[g, n] = sum of dpre[m, n] over g's rows
+ *   dout_bf16, pre_bf16 [M_cap, N] (pre may be NULL for MXFP4_ACT_NONE).
+ *   dpre_bf16 [M_cap, N] (optional; may be dout_bf16 or pre_bf16), q_e4m3 [M_cap, N] with
+ *   q_scales [M_cap, ceil(N/128)] (optional, both or none), dbias [G, N] FP32 (optional; every
+ *   element is written, 0 for an expert without rows, also when M_cap == 0): at least one of
+ *   the three is given.  dbias is summed in a fixed order.
+ *   workspace: for dbias of many rows.   N must be a multiple of 8, of 16 for q, and at most
+ *   2^20. */
+mxfp4_status mxfp4_act_rows_backward(const uint16_t* dout_bf16, const uint16_t* pre_bf16, uint16_t* dpre_bf16,
+                                     uint8_t* q_e4m3, float* q_scales, float* dbias, void* workspace,
+                                     const int32_t* group_offsets, int32_t G, int64_t M_cap, int64_t N, int32_t act,
+                                     hipStream_t stream);
+int64_t mxfp4_act_rows_backward_workspace(int32_t G, int64_t M_cap, int64_t N);
+
 /* Expert rows back to their tokens: out[t] = base[t] + sum_j weights[t, j] y[pos[t, j]] over
  * the choices with 0 <= pos < M_cap, summed in FP32 in the order of j and rounded once.
  *   y_bf16 [M_cap, K], pos [T, k], weights [T, k] (optional: 1), base_bf16 [T, K]
