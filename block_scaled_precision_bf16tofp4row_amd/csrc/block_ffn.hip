@@ -26,14 +26,14 @@ struct Ffn {
     uint16_t* out;                                // gated, gradient: out [M, N].  dense: p + bias [M, N]
     uint8_t* q;                                   // E4M3 of out (gated), of dh (gradient)
     float* q_scales;
-    float* sums;                                  // those values in FP32 instead (kernels for few rows)
+    float* sums;                                  // those values in FP32 (where a tile has no whole scale blocks)
     int act;
 };
 
 enum Kind { kGated, kGradient, kDense };
 
 // The epilogue of one thread: eight features, col .. col + 7, of rows of a tile.
-template <int KIND>
+template <Kind KIND>
 struct Epilogue {
     static constexpr int kParts = KIND == kGated ? 2 : 1;
     // Values of a row in `rows` and in q, per feature.
@@ -105,13 +105,13 @@ struct Epilogue {
     }
     static __device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, int off, u32x4 v)
     {
-        __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 2);      // (past the caches)
     }
-    // E4M3 bytes (all 16 lanes of a block take part), or FP32 sums.
-    template <bool kTile>
+    // E4M3 bytes (kBlocks: the 16 lanes of a scale block take part), or FP32 sums.
+    template <bool kBlocks>
     __device__ __forceinline__ void quantized(uint32_t row, int p, const float (&v)[8]) const
     {
-        if constexpr (kTile) {
+        if constexpr (kBlocks) {
             if (f.q) {
                 float scale;
                 const u32x2 b = to_fp8(v, scale);
@@ -130,7 +130,7 @@ struct Epilogue {
         }
     }
     // Row `row` of the tile: the sums of each part's eight features.
-    template <bool kTile>
+    template <bool kBlocks>
     __device__ __forceinline__ void apply(uint32_t row, float (&v)[kParts][8], const In& in) const
     {
         float slope[8];
@@ -150,7 +150,7 @@ struct Epilogue {
                 v[0][i] *= v[1][i];
             if (f.out)
                 put(rout, at_byte(row, 1, 0, 2), to_bf16(v[0]));
-            quantized<kTile>(row, 0, v[0]);
+            quantized<kBlocks>(row, 0, v[0]);
         } else if constexpr (KIND == kGradient) {
             float a[8], u[8];
             from_bf16(in.h[0], a);
@@ -169,8 +169,8 @@ struct Epilogue {
                 put(rrows, at_byte(row, 2, 0, 2), to_bf16(dg));
                 put(rrows, at_byte(row, 2, 1, 2), to_bf16(du));
             }
-            quantized<kTile>(row, 0, dg);
-            quantized<kTile>(row, 1, du);
+            quantized<kBlocks>(row, 0, dg);
+            quantized<kBlocks>(row, 1, du);
         } else {
             if (f.out)
                 put(rout, at_byte(row, 1, 0, 2), to_bf16(v[0]));
@@ -186,25 +186,16 @@ struct Epilogue {
     }
 };
 
-template <class W, int KIND>
-__global__ __launch_bounds__(64 * W::kWM * W::kWN, W::kD == 2 ? 2 : 1) void ffn_tile_kernel(
-    const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
-    const float* __restrict__ sw, Ffn f, const int32_t* __restrict__ offs, int G, int64_t N, int64_t K, uint32_t ntn)
+// A tile's way out: its sums through LDS to the epilogue.
+template <class W, Kind KIND>
+__device__ __forceinline__ void tile_out(uint8_t* lds0, uint8_t* lds1, uint8_t* lds2, uint8_t* lds3,
+                                         const typename W::State& t, const Ffn& f, const TileAt& at, int64_t N)
 {
     constexpr int kParts = Epilogue<KIND>::kParts;
     constexpr int WM = W::kWM, MT = W::kMT, NT = W::kNT, TM = W::TM, TN = W::TN, kThreads = 64 * W::kWaves;
-    // separate arrays: what is loaded into one does not hold up reads of another
-    __shared__ __attribute__((aligned(16))) uint8_t lds0[W::kBuf];
-    __shared__ __attribute__((aligned(16))) uint8_t lds1[W::kBuf];
-    __shared__ __attribute__((aligned(16))) uint8_t lds2[W::kBuf2];
-    __shared__ __attribute__((aligned(16))) uint8_t lds3[W::kBuf3];
-    typename W::State t;
-    TileAt at;
-    if (!tile_sums<W, kParts>(lds0, lds1, lds2, lds3, a, sa, w, sw, offs, G, N, K, ntn, t, at))
-        return;                                   // uniform over the workgroup
-
     // Groups of 16 rows, those of wave row wm one after the other; kGroups of them fit the LDS.
     // 16-byte chunk c of row r is at chunk c ^ (r % 16).
+    auto chunk_at = [](uint32_t ch, uint32_t row) { return 16 * (ch ^ row); };
     constexpr int kGroup = 16 * TN * 4, kIn0 = W::kBuf / kGroup, kIn2 = W::kBuf2 / kGroup, kIn3 = W::kBuf3 / kGroup;
     constexpr int kGroups = 2 * kIn0 + kIn2 + kIn3, kPhases = TM / 16 <= kGroups ? 1 : 2;
     constexpr int MP = MT / kPhases, kRows = TM / kPhases;
@@ -224,49 +215,99 @@ __global__ __launch_bounds__(64 * W::kWM * W::kWN, W::kD == 2 ? 2 : 1) void ffn_
     const uint32_t c = (uint32_t)tid % kCols;
     typedef Epilogue<KIND> E;
     const E epi(f, at, (uint32_t)N, c);
-#pragma unroll
-    for (int phase = 0; phase < kPhases; ++phase) {
-        if (phase > 0)
-            meet();                               // the rows of the phase before have been read
+    // A batch's rows are fetched while the one before it is worked on.
+    constexpr int kSteps = kRows / kStep, kBatch = kSteps < 4 ? kSteps : 4, kBatches = kPhases * kSteps / kBatch;
+    static_assert(kSteps % kBatch == 0, "whole batches");
+    auto write = [&](auto p) {
+        constexpr int kPhase = decltype(p)::value;
 #pragma unroll
         for (int m = 0; m < MP; ++m)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t chunk = (uint32_t)(4 * (NT * wn + nt)) + h;
-                *reinterpret_cast<f32x4*>(place(wm * MP + m) + r * (TN * 4) + 16 * (chunk ^ r)) =
-                    t.acc[phase * MP + m][nt];
+                *reinterpret_cast<f32x4*>(place(wm * MP + m) + r * (TN * 4) +
+                                          chunk_at((uint32_t)(4 * (NT * wn + nt)) + h, r)) =
+                    t.acc[kPhase * MP + m][nt];
             }
-        // (rows of the phase: group by group; row `in` of the phase is this row of the tile)
-        auto row_of = [&](int i) {
-            const uint32_t in = (uint32_t)tid / kCols + kStep * i, group = in / 16;
-            return 16 * (MT * (group / MP) + phase * MP + group % MP) + in % 16;
-        };
-        typename E::In next;
-        epi.fetch(row_of(0), next);
-        meet();
+        // (keeps the compiler from merging the phases' code, with pointers into the sums)
+        asm volatile("; phase %0" ::"n"(kPhase));
+    };
+    // (rows of a phase: group by group; step i of all is row `in` of phase i / kSteps, which is
+    // this row of the tile)
+    auto row_of = [&](int i) {
+        const uint32_t in = (uint32_t)tid / kCols + kStep * (i % kSteps), group = in / 16;
+        return 16 * (MT * (group / MP) + i / kSteps * MP + group % MP) + in % 16;
+    };
+    typename E::In in[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+        epi.fetch(row_of(u), in[u]);
 #pragma unroll 1
-        for (int i = 0; i < kRows / kStep; ++i) {
-            const typename E::In now = next;
-            if (i + 1 < kRows / kStep)
-                epi.fetch(row_of(i + 1), next);
-            const uint32_t in = (uint32_t)tid / kCols + kStep * i, rr = in % 16;
-            const uint8_t* const from = place(__builtin_amdgcn_readfirstlane((int)(in / 16))) + rr * (TN * 4);
+    for (int b = 0; b < kBatches; ++b) {
+        if (b % (kSteps / kBatch) == 0) {
+            if (b == 0) {
+                write(std::integral_constant<int, 0>{});
+            } else {
+                meet();                           // the rows of the phase before have been read
+                write(std::integral_constant<int, kPhases - 1>{});
+            }
+            meet();
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = b * kBatch + u;
+            const uint32_t at_row = (uint32_t)tid / kCols + kStep * (i % kSteps), rr = at_row % 16;
+            const uint8_t* const from = place(__builtin_amdgcn_readfirstlane((int)(at_row / 16))) + rr * (TN * 4);
             float v[kParts][8];
 #pragma unroll
             for (int p = 0; p < kParts; ++p)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const f32x4 s = *reinterpret_cast<const f32x4*>(from + 16 * ((p * (TN / 8) + 2 * c + j) ^ rr));
+                    const f32x4 s = *reinterpret_cast<const f32x4*>(from + chunk_at(p * (TN / 8) + 2 * c + j, rr));
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         v[p][4 * j + e] = s[e];
                 }
-            epi.template apply<true>(row_of(i), v, now);
+            epi.template apply<TN / kParts % 128 == 0>(row_of(i), v, in[u]);
+            if (b + 1 < kBatches)
+                epi.fetch(row_of(i + kBatch), in[u]);
         }
     }
 }
 
-template <int MT, int KIND>
+template <class W, Kind KIND>
+__global__ __launch_bounds__(64 * W::kWM * W::kWN, W::kD == 2 ? 2 : 1) void ffn_tile_kernel(
+    const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
+    const float* __restrict__ sw, Ffn f, const int32_t* __restrict__ offs, int G, int64_t N, int64_t K, uint32_t ntn)
+{
+    constexpr int kParts = Epilogue<KIND>::kParts;
+    // separate arrays: what is loaded into one does not hold up reads of another
+    __shared__ __attribute__((aligned(16))) uint8_t lds0[W::kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds1[W::kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds2[W::kBuf2];
+    __shared__ __attribute__((aligned(16))) uint8_t lds3[W::kBuf3];
+    TileAt at;
+    if (!tile_place<W::TM, W::TN, kParts, W::TM == 256>(offs, G, N, ntn, at))
+        return;                                   // uniform over the workgroup
+    auto tile = [&](auto type) {
+        typedef decltype(type) T;
+        typename T::State t;
+        tile_sums<T, kParts>(lds0, lds1, lds2, lds3, a, sa, w, sw, N, K, at, t);
+        tile_out<T, KIND>(lds0, lds1, lds2, lds3, t, f, at, N);
+    };
+    if constexpr (W::TM == 256) {
+        // half a tile's rows or fewer: a tile of half the size
+        typedef Tile<2, 4, 4, 4, 2> Half;
+        static_assert(Half::kBuf <= W::kBuf && Half::kBuf2 <= W::kBuf2 && Half::kBuf3 <= W::kBuf3, "the same LDS");
+        if (at.rows > Half::TM)
+            tile(W{});
+        else
+            tile(Half{});
+    } else {
+        tile(W{});
+    }
+}
+
+template <int MT, Kind KIND>
 __global__ __launch_bounds__(64 * kRowsWaves) void ffn_rows_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
     const float* __restrict__ sw, Ffn f, const int32_t* __restrict__ offs, int G, int64_t N, int64_t K, uint32_t ntm)
@@ -342,12 +383,14 @@ typedef Tile<1, 4, 2, 4, 4> Tile32x256;
 typedef Tile<1, 4, 2, 2, 4> Tile32;
 typedef Tile<1, 4, 2, 2, 3> Tile32Shared;
 
-// The kernel of a call: the K-splitting one with 16 or 32 tokens, or a tile.
-enum Which { kRows16, kRows32, kSmall, kSmallShared, kMedium, kLarge };
+// The kernel of a call: the K-splitting one with 16 or 32 tokens, or a tile.  kWide ones have
+// 256 rows of the weights, so that a gated tile has whole scale blocks.
+enum Which { kRows16, kRows32, kSmall, kSmallShared, kSmallWide, kMedium, kMediumWide, kLarge };
 
-Which choose(int32_t G, int64_t M_cap, int64_t N, int64_t K, int parts)
+// fp8: E4M3 outputs are wanted.
+Which choose(Kind kind, bool fp8, int32_t G, int64_t M_cap, int64_t N, int64_t K)
 {
-    const int64_t n = parts * N;
+    const int64_t n = kind == kGated ? 2 * N : N;
     const int64_t rows16 = tiles(M_cap, G, n, 16, kRowsTN), rows32 = tiles(M_cap, G, n, 32, kRowsTN);
     if (rows16 <= 320 || (rows16 <= 512 && rows32 > 320 && K > 4096))
         return kRows16;
@@ -355,73 +398,79 @@ Which choose(int32_t G, int64_t M_cap, int64_t N, int64_t K, int parts)
         return kRows32;
     if (M_cap >= 192 * (int64_t)G && tiles(M_cap, G, n, 256, 256) >= 192)
         return kLarge;
+    const bool wide = kind == kGated && fp8;
     if (M_cap >= 12 * (int64_t)G && tiles(M_cap, G, n, 128, 128) >= 128)
-        return kMedium;
-    return tiles(M_cap, G, n, 32, 128) <= 256 ? kSmall : kSmallShared;
+        return wide && 4 * M_cap * N > (8 << 20) ? kMediumWide : kMedium;
+    return tiles(M_cap, G, n, 32, 128) <= 256 ? kSmall : wide ? kSmallWide : kSmallShared;
 }
 
-template <int KIND>
+// Whether E4M3 outputs of a kernel go through FP32 sums and a second launch.
+bool by_sums(Kind kind, Which w)
+{
+    return w == kRows16 || w == kRows32 || (kind == kGated && (w == kSmall || w == kMedium));
+}
+
+template <Kind KIND>
 hipError_t launch_ffn(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, Ffn f,
                       const int32_t* offs, int32_t G, int64_t M_cap, int64_t N, int64_t K, hipStream_t stream)
 {
     constexpr int kParts = Epilogue<KIND>::kParts;
+    const Which which = choose(KIND, f.q != nullptr, G, M_cap, N, K);
+    const bool then = f.q && by_sums(KIND, which);
     int g = G;
     int64_t n = N, k = K;
     uint32_t nt = 0;                              // feature tiles (tile kernel), token tiles (rows kernel)
     void* args[] = {(void*)&a, (void*)&sa, (void*)&w, (void*)&sw, (void*)&f, (void*)&offs, (void*)&g,
                     (void*)&n, (void*)&k, (void*)&nt};
-    auto tile = [&](auto W, const void* kernel) {
-        typedef decltype(W) T;
-        nt = (uint32_t)((N + T::TN / kParts - 1) / (T::TN / kParts));
-        const int64_t grid = tiles(M_cap, G, N, T::TM, T::TN / kParts);
-        f.sums = nullptr;
+    auto launch = [&](const void* kernel, int TM, int features, int threads) {
+        const int64_t grid = tiles(M_cap, G, N, TM, features);
         return grid > 0x7FFFFFFF ? hipErrorInvalidValue
-                                 : launch_kernel(kernel, dim3((unsigned)grid), dim3(64 * T::kWaves), args, stream);
+                                 : launch_kernel(kernel, dim3((unsigned)grid), dim3((unsigned)threads), args, stream, !then);
+    };
+    auto tile = [&](auto type) {
+        typedef decltype(type) T;
+        nt = (uint32_t)((N + T::TN / kParts - 1) / (T::TN / kParts));
+        return launch((const void*)ffn_tile_kernel<T, KIND>, T::TM, T::TN / kParts, 64 * T::kWaves);
     };
     auto rows = [&](int TM, const void* kernel) {
         nt = (uint32_t)tiles(M_cap, G, 1, TM, 1);
-        const int64_t grid = tiles(M_cap, G, N, TM, kRowsTN / kParts);
-        const bool then = f.q != nullptr;
-        hipError_t e = launch_kernel(kernel, dim3((unsigned)grid), dim3(64 * kRowsWaves), args, stream, !then);
-        if (e != hipSuccess || !then)
-            return e;
-        uint32_t cols = (uint32_t)(Epilogue<KIND>::kQuant * N), blocks = (cols + 127) / 128;
-        void* more[] = {(void*)&f.sums, (void*)&f.q, (void*)&f.q_scales, (void*)&offs, (void*)&g, (void*)&cols,
-                        (void*)&blocks};
-        const int64_t lanes = M_cap * blocks * 16;
-        return launch_kernel((const void*)quantize_sums_kernel, dim3((unsigned)((lanes + kThreads - 1) / kThreads)),
-                             dim3(kThreads), more, stream);
+        return launch(kernel, TM, kRowsTN / kParts, 64 * kRowsWaves);
     };
-    switch (choose(G, M_cap, N, K, kParts)) {
-    case kRows16: return rows(16, (const void*)ffn_rows_kernel<1, KIND>);
-    case kRows32: return rows(32, (const void*)ffn_rows_kernel<2, KIND>);
-    case kLarge: return tile(Tile256{}, (const void*)ffn_tile_kernel<Tile256, KIND>);
-    case kMedium:
+    auto first = [&]() {
+        switch (which) {
+        case kRows16: return rows(16, (const void*)ffn_rows_kernel<1, KIND>);
+        case kRows32: return rows(32, (const void*)ffn_rows_kernel<2, KIND>);
+        case kLarge: return tile(Tile256{});
+        case kMedium: return tile(Tile128{});
+        case kSmall: return tile(Tile32{});
+        case kSmallShared: return tile(Tile32Shared{});
+        default: break;
+        }
         if constexpr (KIND == kGated)
-            return tile(Tile128x256{}, (const void*)ffn_tile_kernel<Tile128x256, KIND>);
-        else
-            return tile(Tile128{}, (const void*)ffn_tile_kernel<Tile128, KIND>);
-    default:
-        if constexpr (KIND == kGated)
-            return tile(Tile32x256{}, (const void*)ffn_tile_kernel<Tile32x256, KIND>);
-        else if (tiles(M_cap, G, N, 32, 128) <= 256)
-            return tile(Tile32{}, (const void*)ffn_tile_kernel<Tile32, KIND>);
-        else
-            return tile(Tile32Shared{}, (const void*)ffn_tile_kernel<Tile32Shared, KIND>);
-    }
+            return which == kMediumWide ? tile(Tile128x256{}) : tile(Tile32x256{});
+        return hipErrorInvalidValue;              // (no other kind chooses these)
+    };
+    const hipError_t e = first();
+    if (e != hipSuccess || !then)
+        return e;
+    uint32_t cols = (uint32_t)(Epilogue<KIND>::kQuant * N), blocks = (cols + 127) / 128;
+    void* more[] = {(void*)&f.sums, (void*)&f.q, (void*)&f.q_scales, (void*)&offs, (void*)&g, (void*)&cols,
+                    (void*)&blocks};
+    const int64_t groups = (M_cap * blocks * 16 + kThreads - 1) / kThreads;
+    return groups > 0x7FFFFFFF ? hipErrorInvalidValue
+                               : launch_kernel((const void*)quantize_sums_kernel, dim3((unsigned)groups),
+                                               dim3(kThreads), more, stream);
 }
-
-bool splits_k(Which w) { return w == kRows16 || w == kRows32; }
 
 }  // namespace
 
 int64_t gated_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
 {
-    return splits_k(choose(G, M_cap, I, K, 2)) ? 4 * M_cap * I : 0;
+    return by_sums(kGated, choose(kGated, true, G, M_cap, I, K)) ? 4 * M_cap * I : 0;
 }
 int64_t gated_backward_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
 {
-    return splits_k(choose(G, M_cap, I, K, 1)) ? 8 * M_cap * I : 0;
+    return by_sums(kGradient, choose(kGradient, true, G, M_cap, I, K)) ? 8 * M_cap * I : 0;
 }
 
 hipError_t launch_gated_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, const float* bias,

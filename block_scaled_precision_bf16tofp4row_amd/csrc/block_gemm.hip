@@ -47,10 +47,11 @@ __global__ __launch_bounds__(64 * WM * WN, D == 2 ? 2 : 1) void block_gemm_tile_
     __shared__ __attribute__((aligned(16))) uint8_t lds1[W::kBuf];
     __shared__ __attribute__((aligned(16))) uint8_t lds2[W::kBuf2];
     __shared__ __attribute__((aligned(16))) uint8_t lds3[W::kBuf3];
-    typename W::State t;
     TileAt at;
-    if (!tile_sums<W, 1>(lds0, lds1, lds2, lds3, a, sa, w, sw, offs, G, N, K, ntn, t, at))
+    if (!tile_place<TM, TN, 1, false>(offs, G, N, ntn, at))
         return;                                   // uniform over the workgroup
+    typename W::State t;
+    tile_sums<W, 1>(lds0, lds1, lds2, lds3, a, sa, w, sw, N, K, at, t);
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wn = wave / WM;

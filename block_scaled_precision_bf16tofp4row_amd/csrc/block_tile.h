@@ -106,7 +106,7 @@ struct Tile {
     static_assert(D >= 2 && D <= 4, "stage buffers");
     static_assert(TM % (8 * kWaves) == 0 && TN % (8 * kWaves) == 0 && TM <= kSlots, "loads");
     static_assert(TN % 128 == 0 && 128 % (16 * NT) == 0, "a wave's features lie in one scale block");
-    static_assert(!kHalves || (MT % 2 == 0 && kLoadsA % 4 == 0 && MT >= 4), "halves");
+    static_assert(!kHalves || (MT % 2 == 0 && kLoadsA % 2 == 0 && MT >= 4), "halves");
     static_assert((MT == 2 || MT % 4 == 0) && kTiles % 4 == 0, "scale reads, ring of products");
 
     struct State {
@@ -142,7 +142,7 @@ struct Tile {
             const int half = tok && kHalves ? i / (kLoadsA / 2) : 0, in_half = tok && kHalves ? i % (kLoadsA / 2) : i;
             const int rows = 8 * (in_half + half * MT);
             uint8_t* const to_buf = half ? cx.late[b] : cx.buf[b];
-            const uint32_t c = tok ? (i & 1 ? cx.ac1 : cx.ac0) : (i & 1 ? cx.wc1 : cx.wc0);
+            const uint32_t c = tok ? (in_half & 1 ? cx.ac1 : cx.ac0) : (i & 1 ? cx.wc1 : cx.wc0);
             const uint32_t off = c + k0 < K ? (tok ? cx.abase : cx.wbase) + c : kOutOfRange;
             load16_to_lds(tok ? cx.ra : cx.rw, to_buf + (tok ? cx.lds_a : cx.lds_w) + 8 * in_half * kBK,
                           off + (uint32_t)rows * cx.K, k0);
@@ -263,46 +263,85 @@ struct Tile {
 // memory each stage, and D = 3 where there are more: two then fit its LDS, and one works while
 // the other starts or ends (64 rows over 256 experts x 4096 x 2048: 80 us, D = 4 83, D = 2 87;
 // 128 rows over 32 experts x 4096 x 7168: 146, 148, 179).
-//
-// tile_sums: a tile's sums, in t: lane (r, h) = (lane % 16, lane / 16) of wave (wm, wn) =
-// (wave % WM, wave / WM) holds in acc[mt][nt] those of token 16 (MT wm + mt) + r and tile
-// features 16 (NT wn + nt) + 4 h + (0..3).  False if the workgroup has no tile.  The LDS
-// arrays are free again afterwards.  lds2 and lds3 are the third and fourth buffer, or the late
-// rows of two.
+
 struct TileAt {
     int g;                                        // expert
     int64_t row0;                                 // first row
     int rows;
     int64_t n0;                                   // first feature (of a part)
     int cols;
+    uint32_t ntile;
 };
 
-template <class W, int kParts>
-__device__ __forceinline__ bool tile_sums(uint8_t* lds0, uint8_t* lds1, uint8_t* lds2, uint8_t* lds3,
-                                          const uint8_t* __restrict__ a, const float* __restrict__ sa,
-                                          const uint8_t* __restrict__ w, const float* __restrict__ sw,
-                                          const int32_t* __restrict__ offs, int G, int64_t N, int64_t K, uint32_t ntn,
-                                          typename W::State& t, TileAt& at)
+// find_tile, but with the tiles in another order: all whole ones, then the experts' last
+// partial ones with more than half the rows, then the others.  A workgroup of a kernel whose
+// small tiles take less time then comes last.
+template <int TM>
+__device__ __forceinline__ bool find_tile_whole_first(const int32_t* __restrict__ offs, int G, uint32_t mtile, int& g,
+                                                      int64_t& row0, int& rows)
 {
-    constexpr int WM = W::kWM, WN = W::kWN, MT = W::kMT, NT = W::kNT, D = W::kD, TM = W::TM, TN = W::TN;
-    static_assert(kParts == 1 || (WN % 2 == 0 && W::kWaves % 2 == 0), "a wave loads and multiplies one part");
-    const int tid = threadIdx.x;
-    const int lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    uint32_t mtile, ntile;
+    const int lane = threadIdx.x & 63;
+    uint32_t run = 0;
+    for (int pass = 0; pass < 3; ++pass)
+        for (int g0 = 0; g0 < G; g0 += 64) {
+            const int h = g0 + lane;
+            const int32_t from = offs[min(h, G)], m = offs[min(h + 1, G)] - from;
+            const uint32_t whole = (uint32_t)m / TM, rest = (uint32_t)m % TM;
+            const uint32_t own = pass == 0 ? whole : (pass == 1) == (rest > TM / 2) && rest ? 1 : 0;
+            const uint32_t incl = wave_scan(own), first = run + incl - own;
+            const uint64_t mask = __ballot(mtile >= first && mtile - first < own);
+            if (mask) {
+                const int src = __builtin_ctzll(mask);
+                const uint32_t skip = pass == 0 ? mtile - first : whole;
+                g = g0 + src;
+                row0 = (int64_t)__builtin_amdgcn_readlane(from, src) +
+                       (int64_t)TM * (uint32_t)__builtin_amdgcn_readlane((int)skip, src);
+                rows = pass == 0 ? TM : __builtin_amdgcn_readlane((int)rest, src);
+                return true;
+            }
+            run += (uint32_t)__builtin_amdgcn_readlane((int)incl, 63);
+        }
+    return false;
+}
+
+// The workgroup's tile of TM rows and TN rows of the weights; false if it has none.
+template <int TM, int TN, int kParts, bool kWholeFirst>
+__device__ __forceinline__ bool tile_place(const int32_t* __restrict__ offs, int G, int64_t N, uint32_t ntn, TileAt& at)
+{
+    uint32_t mtile;
     // Workgroups go round-robin over the 8 XCDs, so with pairs of token tiles an XCD has every
     // second token tile and every fourth feature tile of a stretch: 8 x 4 of 256 workgroups,
     // all of them on one expert or a few neighbours, and an expert with few rows spread over
     // all XCDs.  (Groups of 4 dealt to one XCD each, as the other GEMM has them: 2048 rows over
     // 32 experts 225 us, here 213; 65536 rows x 7168 x 2048 975, 955; 32768 rows 905, 892.)
-    tile_of<2>(blockIdx.x, gridDim.x, ntn, mtile, ntile);
-    int g;
-    int64_t row0;
-    int rows;
-    if (!find_tile<TM>(offs, G, mtile, g, row0, rows))
-        return false;                             // uniform over the workgroup
-    const int64_t n0 = (int64_t)(TN / kParts) * ntile;
-    const int cols = (int)min((int64_t)(TN / kParts), N - n0);
+    tile_of<2>(blockIdx.x, gridDim.x, ntn, mtile, at.ntile);
+    bool found;
+    if constexpr (kWholeFirst)
+        found = find_tile_whole_first<TM>(offs, G, mtile, at.g, at.row0, at.rows);
+    else
+        found = find_tile<TM>(offs, G, mtile, at.g, at.row0, at.rows);
+    at.n0 = (int64_t)(TN / kParts) * at.ntile;
+    at.cols = (int)min((int64_t)(TN / kParts), N - at.n0);
+    return found;
+}
+
+// A tile's sums, in t: lane (r, h) = (lane % 16, lane / 16) of wave (wm, wn) = (wave % WM,
+// wave / WM) holds in acc[mt][nt] those of token 16 (MT wm + mt) + r and tile features
+// 16 (NT wn + nt) + 4 h + (0..3).  The LDS arrays are free again afterwards.  lds2 and lds3 are
+// the third and fourth buffer, or the late rows of two.
+template <class W, int kParts>
+__device__ __forceinline__ void tile_sums(uint8_t* lds0, uint8_t* lds1, uint8_t* lds2, uint8_t* lds3,
+                                          const uint8_t* __restrict__ a, const float* __restrict__ sa,
+                                          const uint8_t* __restrict__ w, const float* __restrict__ sw, int64_t N,
+                                          int64_t K, const TileAt& at, typename W::State& t)
+{
+    constexpr int WM = W::kWM, WN = W::kWN, MT = W::kMT, NT = W::kNT, D = W::kD, TN = W::TN;
+    static_assert(kParts == 1 || (WN % 2 == 0 && W::kWaves % 2 == 0), "a wave loads and multiplies one part");
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = at.g, rows = at.rows, cols = at.cols;
+    const int64_t row0 = at.row0, n0 = at.n0;
     const uint32_t kb_n = (uint32_t)((K + kBK - 1) / kBK);
     const uint32_t nb_n = (uint32_t)((N + 127) / 128);
     const int wm = wave % WM, wn = wave / WM;
@@ -337,7 +376,7 @@ __device__ __forceinline__ bool tile_sums(uint8_t* lds0, uint8_t* lds1, uint8_t*
     cx.rsw = strip_rsrc(sw + ((kParts * (int64_t)g + part) * nb_n + nb) * kb_n, (uint64_t)kb_n * 4);
     cx.K = (uint32_t)K;
     cx.blocks = kb_n;
-    cx.turn = K % 4096 == 0 ? (ntile + 5 * (uint32_t)g) % kb_n : 0;
+    cx.turn = K % 4096 == 0 ? (at.ntile + 5 * (uint32_t)g) % kb_n : 0;
     cx.abase = (8 * ag + l8) * cx.K;
     cx.wbase = (8 * wg - lpart * (TN / kParts) + l8) * cx.K;
     cx.ac0 = 16 * (lc ^ ((4 * ag + l16) & 7));
@@ -406,8 +445,6 @@ __device__ __forceinline__ bool tile_sums(uint8_t* lds0, uint8_t* lds1, uint8_t*
     W::template add<-1>(t);
     __builtin_amdgcn_s_waitcnt(vmcnt_at_most(0));  // no load into LDS is left
     __syncthreads();
-    at = {g, row0, rows, n0, cols};
-    return true;
 }
 
 // The loop for few rows and few tiles, where a tile's walk along K would be the time: a
@@ -548,7 +585,7 @@ __device__ __forceinline__ bool rows_sums(uint8_t* lds0, uint8_t* lds1, uint8_t*
         for (int nt = 0; nt < NT; ++nt)
             *reinterpret_cast<f32x4*>(&part[wave][16 * mt + r][16 * nt + 4 * h]) = acc[mt][nt];
     __syncthreads();
-    at = {g, row0, rows, n0, cols};
+    at = {g, row0, rows, n0, cols, lin / ntm};
     return true;
 }
 

@@ -136,6 +136,8 @@ SHAPES = [
     ([50, 51, 49, 0, 64, 1, 100, 85], 8200, 144),
     ([301, 300, 280], 1544, 528),
     ([900, 3], 12296, 144),                       # large
+    ([356, 100, 0, 640, 1, 385], 12296, 400),     # large, with partial tiles of 100, 128, 1 and 129 rows
+    ([1000, 129], 8208, 272), ([700, 260], 9984, 16),
     ([2500, 0, 700], 4104, 272),
     ([1] * 300, 520, 112),
 ]
