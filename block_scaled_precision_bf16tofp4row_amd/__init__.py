@@ -651,17 +651,31 @@ def mxfp4_fp8_block_gemm(a, a_scales, w, w_scales, y, offs, G=None, M_cap=None, 
 
 def _take_here(what: str, args):
     """_take, and every tensor has to be on the current device, whose stream the call goes to."""
-    at = _take(what, args)
-    here = None
-    for t, _, name, _ in args:
-        if t is None or isinstance(t, int):
+    at = []
+    here = -1
+    for t, nbytes, name, dtypes in args:
+        if t is None or type(t) is int:
+            at.append(t)
             continue
-        if here is None:
-            import torch
-            here = _device() if _device is not None else torch.cuda.current_device()
-        if t.get_device() != here:
-            raise ValueError(f"{what}: {name} is on cuda:{t.get_device()}, the current device is cuda:{here}")
+        if isinstance(t, int):
+            at.append(int(t))
+            continue
+        device = t.get_device()
+        if device < 0 or t.nbytes < nbytes or _dtype_name[t.dtype] not in dtypes or not t.is_contiguous():
+            _take(what, args)                     # (says what is wrong)
+        if here < 0:
+            here = _current_device()
+        if device != here:
+            raise ValueError(f"{what}: {name} is on cuda:{device}, the current device is cuda:{here}")
+        at.append(t.data_ptr() or 16)
     return at
+
+
+def _current_device() -> int:
+    if _device is not None:
+        return _device()
+    import torch
+    return torch.cuda.current_device()
 
 
 _ACTS = {"none": MXFP4_ACT_NONE, "relu": MXFP4_ACT_RELU, "silu": MXFP4_ACT_SILU, "gelu": MXFP4_ACT_GELU,
@@ -669,9 +683,12 @@ _ACTS = {"none": MXFP4_ACT_NONE, "relu": MXFP4_ACT_RELU, "silu": MXFP4_ACT_SILU,
 
 
 def _act(act) -> int:
-    if isinstance(act, str) and act not in _ACTS:
-        raise ValueError(f"act must be one of {', '.join(map(repr, _ACTS))}, got {act!r}")
-    return _ACTS.get(act, act)
+    code = _ACTS.get(act)
+    if code is None:
+        if isinstance(act, str):
+            raise ValueError(f"act must be one of {', '.join(map(repr, _ACTS))}, got {act!r}")
+        code = int(act)                           # (the library refuses what it does not know)
+    return code
 
 
 def _ffn_dims(a, w, offs, G, M_cap, N, K, parts=1):

@@ -5,7 +5,7 @@
 //
 // What bounds it is its bytes.  A thread has eight columns and every eighth row of a tile, 32
 // threads a row's 512 bytes, so that the columns' sums stay in registers until the tile's end,
-// where the eight rows of threads meet in LDS.  With many rows a tile is kActRows rows of one expert and its
+// where the eight rows of threads meet in LDS.  A tile is 128 or 32 rows of one expert and its
 // sums go to the workspace, where a second launch adds them, tile by tile in a fixed order (no
 // atomics: the same call gives the same bits); with few rows a workgroup takes all rows of an
 // expert and writes the sums itself.
@@ -18,7 +18,7 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kActRows = 128;                     // rows of a tile
+constexpr int kManyRows = 128, kFewRows = 32;     // rows of a tile
 constexpr int kActCols = 256, kLanes = kActCols / 8, kRowGroups = kThreads / kLanes;
 constexpr int kBatch = 4;                         // rows of a thread in flight
 constexpr int kSumCols = 64, kSumSplit = 16;      // second launch: columns and tile runs of a workgroup
@@ -26,7 +26,8 @@ constexpr uint32_t kNowhere = 0x80000000u;        // offset past every buffer's 
 
 }  // namespace
 
-template <bool kWhole>
+// ROWS: rows of a tile; 0: all of an expert's.
+template <int ROWS>
 __global__ __launch_bounds__(kThreads) void act_rows_kernel(
     const uint16_t* dout, const uint16_t* pre, uint16_t* dpre, uint8_t* q, float* q_scales, float* sums,
     const int32_t* __restrict__ offs, int G, uint32_t N, uint32_t strips, int act)
@@ -36,11 +37,11 @@ __global__ __launch_bounds__(kThreads) void act_rows_kernel(
     int g;
     int64_t row0;
     int rows;
-    if constexpr (kWhole) {
+    if constexpr (ROWS == 0) {
         g = (int)tile;
         row0 = offs[g];
         rows = offs[g + 1] - (int)row0;
-    } else if (!find_tile<kActRows>(offs, G, tile, g, row0, rows)) {
+    } else if (!find_tile<ROWS>(offs, G, tile, g, row0, rows)) {
         return;                                   // uniform over the workgroup
     }
     const uint32_t tid = threadIdx.x, c = tid % kLanes, group = tid / kLanes, col = n0 + 8 * c;
@@ -101,13 +102,13 @@ __global__ __launch_bounds__(kThreads) void act_rows_kernel(
     for (int i = 0; i < kRowGroups; ++i)
         s += part[i][tid];
     if (n0 + tid < N)
-        sums[(uint64_t)(kWhole ? (uint32_t)g : tile) * N + n0 + tid] = s;
+        sums[(uint64_t)tile * N + n0 + tid] = s;
 }
 
 // dbias_g = the sum of its tiles' sums.
 __global__ __launch_bounds__(kSumCols* kSumSplit) void bias_sum_kernel(
     const float* __restrict__ sums, float* __restrict__ dbias, const int32_t* __restrict__ offs, uint32_t N,
-    uint32_t strips)
+    uint32_t strips, uint32_t rows)
 {
     __shared__ float part[kSumSplit][kSumCols];
     const int g = (int)(blockIdx.x / strips);
@@ -116,10 +117,10 @@ __global__ __launch_bounds__(kSumCols* kSumSplit) void bias_sum_kernel(
     uint64_t first = 0;                           // tiles of the experts before
     for (int e0 = 0; e0 < g; e0 += 64) {
         const int e = e0 + lane;
-        const uint32_t n = e < g ? (uint32_t)(offs[e + 1] - offs[e] + kActRows - 1) / kActRows : 0;
+        const uint32_t n = e < g ? ((uint32_t)(offs[e + 1] - offs[e]) + rows - 1) / rows : 0;
         first += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(n), 63);
     }
-    const uint32_t n = (uint32_t)(offs[g + 1] - offs[g] + kActRows - 1) / kActRows;
+    const uint32_t n = ((uint32_t)(offs[g + 1] - offs[g]) + rows - 1) / rows;
     const uint32_t t0 = (uint32_t)((uint64_t)n * run / kSumSplit), t1 = (uint32_t)((uint64_t)n * (run + 1) / kSumSplit);
     float s = 0.0f;
     if (col < N) {
@@ -141,47 +142,56 @@ __global__ __launch_bounds__(kSumCols* kSumSplit) void bias_sum_kernel(
 
 namespace {
 
-// Whether a workgroup takes an expert's rows whole.
-bool whole_experts(int64_t M_cap) { return M_cap <= 128; }
-
-int64_t act_tiles(int32_t G, int64_t M_cap)
+int64_t act_tiles(int32_t G, int64_t M_cap, int rows)
 {
     const int64_t live = G < M_cap ? G : M_cap;
-    return (M_cap + live * (kActRows - 1)) / kActRows;
+    return (M_cap + live * (rows - 1)) / rows;
+}
+
+// Rows of a tile; 0: all of an expert's.
+int act_tile_rows(int32_t G, int64_t M_cap, int64_t N)
+{
+    if (M_cap <= 128)
+        return 0;
+    const int64_t strips = (N + kActCols - 1) / kActCols;
+    return act_tiles(G, M_cap, kManyRows) * strips < 1024 ? kFewRows : kManyRows;
 }
 
 }  // namespace
 
 int64_t act_rows_workspace(int32_t G, int64_t M_cap, int64_t N)
 {
-    return whole_experts(M_cap) ? 0 : 4 * act_tiles(G, M_cap) * N;
+    const int rows = act_tile_rows(G, M_cap, N);
+    return rows ? 4 * act_tiles(G, M_cap, rows) * N : 0;
 }
 
 hipError_t launch_act_rows_backward(const uint16_t* dout, const uint16_t* pre, uint16_t* dpre, uint8_t* q,
                                     float* q_scales, float* dbias, float* work, const int32_t* offs, int32_t G,
                                     int64_t M_cap, int64_t N, int act, hipStream_t stream)
 {
-    const bool whole = whole_experts(M_cap);
+    const int rows = act_tile_rows(G, M_cap, N);
     uint32_t n = (uint32_t)N, strips = (uint32_t)((N + kActCols - 1) / kActCols);
     int g = G;
-    float* sums = dbias ? whole ? dbias : work : nullptr;
-    const int64_t grid = (whole ? G : act_tiles(G, M_cap)) * (int64_t)strips;
+    float* sums = dbias ? rows ? work : dbias : nullptr;
+    const int64_t grid = (rows ? act_tiles(G, M_cap, rows) : G) * (int64_t)strips;
     const int64_t columns = (N + kSumCols - 1) / kSumCols;
-    const bool then = dbias && !whole;
+    const bool then = dbias && rows;
     if (grid > 0x7FFFFFFF || (then && G * columns > 0x7FFFFFFF))
         return hipErrorInvalidValue;
     void* args[] = {(void*)&dout, (void*)&pre, (void*)&dpre, (void*)&q, (void*)&q_scales, (void*)&sums,
                     (void*)&offs, (void*)&g, (void*)&n, (void*)&strips, (void*)&act};
     if (grid > 0) {
-        const hipError_t e = launch_kernel(whole ? (const void*)act_rows_kernel<true> : (const void*)act_rows_kernel<false>,
-                                           dim3((unsigned)grid), dim3(kThreads), args, stream, !then);
+        const void* const kernel = rows == 0          ? (const void*)act_rows_kernel<0>
+                                   : rows == kFewRows ? (const void*)act_rows_kernel<kFewRows>
+                                                      : (const void*)act_rows_kernel<kManyRows>;
+        const hipError_t e = launch_kernel(kernel, dim3((unsigned)grid), dim3(kThreads), args, stream, !then);
         if (e != hipSuccess)
             return e;
     }
     if (!then)
         return hipSuccess;
-    uint32_t sum_strips = (uint32_t)columns;
-    void* more[] = {(void*)&work, (void*)&dbias, (void*)&offs, (void*)&n, (void*)&sum_strips};
+    uint32_t sum_strips = (uint32_t)columns, tile_rows = (uint32_t)rows;
+    void* more[] = {(void*)&work, (void*)&dbias, (void*)&offs, (void*)&n, (void*)&sum_strips, (void*)&tile_rows};
     return launch_kernel((const void*)bias_sum_kernel, dim3((unsigned)(G * columns)), dim3(kSumCols * kSumSplit), more,
                          stream);
 }

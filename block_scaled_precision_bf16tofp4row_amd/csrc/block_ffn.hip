@@ -134,11 +134,13 @@ struct Epilogue {
     __device__ __forceinline__ void apply(uint32_t row, float (&v)[kParts][8], const In& in) const
     {
         float slope[8];
+        if constexpr (KIND != kGradient) {
 #pragma unroll
-        for (int p = 0; p < kParts; ++p)
+            for (int p = 0; p < kParts; ++p)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[p][i] += bias[p][i];
+                for (int i = 0; i < 8; ++i)
+                    v[p][i] += bias[p][i];
+        }
         if constexpr (KIND == kGated) {
             if (f.rows) {
                 put(rrows, at_byte(row, 2, 0, 2), to_bf16(v[0]));
@@ -322,16 +324,19 @@ __global__ __launch_bounds__(64 * kRowsWaves) void ffn_rows_kernel(
     __shared__ __attribute__((aligned(16))) uint8_t lds3[kRowsWaves * R::kBuf];
     __shared__ __attribute__((aligned(16))) typename R::Part part[kRowsWaves];
     TileAt at;
-    if (!rows_sums<MT, kParts>(lds0, lds1, lds2, lds3, part, a, sa, w, sw, offs, G, N, K, ntm, at))
+    if (!rows_place<R::TM, kParts>(offs, G, N, ntm, at))
         return;                                   // uniform over the workgroup
     constexpr int kCols = R::TN / kParts / 8;
     static_assert(R::TM * kCols <= 64 * kRowsWaves, "one item a thread");
     const uint32_t row = threadIdx.x / kCols, c = threadIdx.x % kCols;
-    if (row >= R::TM)
-        return;
+    // what the epilogue reads is on its way before the product's loads (the loop's counted
+    // waits then wait for it too, never for less)
     const E epi(f, at, (uint32_t)N, c);
     typename E::In in;
     epi.fetch(row, in);
+    rows_sums<MT, kParts>(lds0, lds1, lds2, lds3, part, a, sa, w, sw, N, K, at);
+    if (row >= R::TM)
+        return;
     float v[kParts][8];
 #pragma unroll
     for (int p = 0; p < kParts; ++p)

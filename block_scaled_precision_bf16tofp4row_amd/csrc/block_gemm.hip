@@ -106,8 +106,9 @@ __global__ __launch_bounds__(64 * kRowsWaves) void block_gemm_rows_kernel(
     __shared__ __attribute__((aligned(16))) uint8_t lds3[kRowsWaves * R::kBuf];
     __shared__ __attribute__((aligned(16))) typename R::Part part[kRowsWaves];
     TileAt at;
-    if (!rows_sums<MT, 1>(lds0, lds1, lds2, lds3, part, a, sa, w, sw, offs, G, N, K, ntm, at))
+    if (!rows_place<R::TM, 1>(offs, G, N, ntm, at))
         return;                                   // uniform over the workgroup
+    rows_sums<MT, 1>(lds0, lds1, lds2, lds3, part, a, sa, w, sw, N, K, at);
     for (int i = threadIdx.x; i < R::TM * R::TN / 4; i += 64 * kRowsWaves) {
         const int m = i / (R::TN / 4), n = i % (R::TN / 4) * 4;
         const f32x4 v = R::sum(part, m, n);

@@ -475,13 +475,25 @@ struct RowsTile {
     }
 };
 
-// The waves' sums, in part.  False if the workgroup has no tile.
+// The workgroup's tile of TM rows and kRowsTN rows of the weights; false if it has none.  Feature
+// tile by feature tile, token tiles inside: the token tiles of an expert follow each other on
+// one XCD and share the weights in its L2.
+template <int TM, int kParts>
+__device__ __forceinline__ bool rows_place(const int32_t* __restrict__ offs, int G, int64_t N, uint32_t ntm, TileAt& at)
+{
+    const uint32_t lin = xcd_remap(blockIdx.x, gridDim.x);
+    at.ntile = lin / ntm;
+    at.n0 = (int64_t)(kRowsTN / kParts) * at.ntile;
+    at.cols = (int)min((int64_t)(kRowsTN / kParts), N - at.n0);
+    return find_tile<TM>(offs, G, lin % ntm, at.g, at.row0, at.rows);
+}
+
+// The waves' sums, in part.
 template <int MT, int kParts>
-__device__ __forceinline__ bool rows_sums(uint8_t* lds0, uint8_t* lds1, uint8_t* lds2, uint8_t* lds3,
+__device__ __forceinline__ void rows_sums(uint8_t* lds0, uint8_t* lds1, uint8_t* lds2, uint8_t* lds3,
                                           typename RowsTile<MT>::Part* part, const uint8_t* __restrict__ a,
                                           const float* __restrict__ sa, const uint8_t* __restrict__ w,
-                                          const float* __restrict__ sw, const int32_t* __restrict__ offs, int G,
-                                          int64_t N, int64_t K, uint32_t ntm, TileAt& at)
+                                          const float* __restrict__ sw, int64_t N, int64_t K, const TileAt& at)
 {
     typedef RowsTile<MT> R;
     constexpr int TM = R::TM, TN = R::TN, W = kRowsWaves, NT = R::NT, kAhead = R::kAhead;
@@ -489,16 +501,8 @@ __device__ __forceinline__ bool rows_sums(uint8_t* lds0, uint8_t* lds1, uint8_t*
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    // feature tile by feature tile, token tiles inside: the token tiles of an expert follow
-    // each other on one XCD and share the weights in its L2
-    const uint32_t lin = xcd_remap(blockIdx.x, gridDim.x);
-    int g;
-    int64_t row0;
-    int rows;
-    if (!find_tile<TM>(offs, G, lin % ntm, g, row0, rows))
-        return false;                             // uniform over the workgroup
-    const int64_t n0 = (int64_t)(TN / kParts) * (lin / ntm);
-    const int cols = (int)min((int64_t)(TN / kParts), N - n0);
+    const int g = at.g, rows = at.rows, cols = at.cols;
+    const int64_t row0 = at.row0, n0 = at.n0;
     const uint32_t kb_n = (uint32_t)((K + kBK - 1) / kBK);
     const uint32_t nb_n = (uint32_t)((N + 127) / 128);
     const uint32_t kb0 = kb_n * wave / W, kb1 = kb_n * (wave + 1) / W;
@@ -585,8 +589,6 @@ __device__ __forceinline__ bool rows_sums(uint8_t* lds0, uint8_t* lds1, uint8_t*
         for (int nt = 0; nt < NT; ++nt)
             *reinterpret_cast<f32x4*>(&part[wave][16 * mt + r][16 * nt + 4 * h]) = acc[mt][nt];
     __syncthreads();
-    at = {g, row0, rows, n0, cols, lin / ntm};
-    return true;
 }
 
 // Workgroups of TM x TN tiles that a call can need: m rows make at most (m + TM - 1) / TM

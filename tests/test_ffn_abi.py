@@ -90,7 +90,7 @@ def test_workspaces():
     assert mx.mxfp4_fp8_gated_gemm_backward_workspace(1, 1, 2048, 7168) == 8 * 2048
     assert mx.mxfp4_fp8_gated_gemm_backward_workspace(8, 32768, 2048, 7168) == 0
     assert mx.mxfp4_act_rows_backward_workspace(3, 5, 64) == 0
-    assert mx.mxfp4_act_rows_backward_workspace(8, 32768, 64) == 4 * 64 * (32768 // 128 + 7)
+    assert mx.mxfp4_act_rows_backward_workspace(8, 32768, 4096) == 4 * 4096 * (32768 // 128 + 7)
     for fn in (one, mx.mxfp4_fp8_gated_gemm_backward_workspace):
         for bad in ((0, 1, 64, 128), (1, -1, 64, 128), (1, 1, 12, 128), (1, 1, 64, 24), (1, 1, (1 << 19) + 8, 128)):
             assert fn(*bad) == -1, bad
