@@ -13,6 +13,8 @@
 // The sums go through LDS as FP32, a tile's rows in one phase or two: a thread then has eight
 // consecutive features of a row, 16 lanes a scale block, and its loads and stores are 16 bytes
 // in whole lines.
+#include <math.h>
+
 #include "activation.h"
 #include "block_tile.h"
 
@@ -194,26 +196,29 @@ __device__ __forceinline__ void tile_out(uint8_t* lds0, uint8_t* lds1, uint8_t* 
                                          const typename W::State& t, const Ffn& f, const TileAt& at, int64_t N)
 {
     constexpr int kParts = Epilogue<KIND>::kParts;
-    constexpr int WM = W::kWM, MT = W::kMT, NT = W::kNT, TM = W::TM, TN = W::TN, kThreads = 64 * W::kWaves;
+    constexpr int WM = W::kWM, MT = W::kMT, NT = W::kNT, TM = W::TM, TN = W::TN, kThreads = W::kThreads;
     // Groups of 16 rows, those of wave row wm one after the other; kGroups of them fit the LDS.
-    // 16-byte chunk c of row r is at chunk c ^ (r % 16).
-    auto chunk_at = [](uint32_t ch, uint32_t row) { return 16 * (ch ^ row); };
     constexpr int kGroup = 16 * TN * 4, kIn0 = W::kBuf / kGroup, kIn2 = W::kBuf2 / kGroup, kIn3 = W::kBuf3 / kGroup;
     constexpr int kGroups = 2 * kIn0 + kIn2 + kIn3, kPhases = TM / 16 <= kGroups ? 1 : 2;
     constexpr int MP = MT / kPhases, kRows = TM / kPhases;
     static_assert(kIn0 >= 1 && kRows / 16 <= kGroups && MT % kPhases == 0, "a phase's rows fit the LDS");
-    auto place = [&](int group) {
-        return group < kIn0             ? lds0 + group * kGroup
-               : group < 2 * kIn0        ? lds1 + (group - kIn0) * kGroup
-               : group < 2 * kIn0 + kIn2 ? lds2 + (group - 2 * kIn0) * kGroup
-                                         : lds3 + (group - 2 * kIn0 - kIn2) * kGroup;
+    auto place = [&](int group, int q) {           // (q: the group of waves whose sums they are)
+        return group < kIn0             ? lds0 + q * W::kBuf + group * kGroup
+               : group < 2 * kIn0        ? lds1 + q * W::kBuf + (group - kIn0) * kGroup
+               : group < 2 * kIn0 + kIn2 ? lds2 + q * W::kBuf2 + (group - 2 * kIn0) * kGroup
+                                         : lds3 + q * W::kBuf3 + (group - 2 * kIn0 - kIn2) * kGroup;
     };
+    // 16-byte chunk c of row r is at chunk c ^ (r % 16).
+    auto chunk_at = [](uint32_t ch, uint32_t row) { return 16 * (ch ^ row); };
     const int tid = threadIdx.x;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % W::kWaves;
+    const int mine = W::kSplit == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 6) / W::kWaves;
     const int wm = wave % WM, wn = wave / WM;
     const uint32_t r = (uint32_t)(tid & 15), h = (uint32_t)(tid >> 4 & 3);
-    constexpr int kCols = TN / kParts / 8, kStep = kThreads / kCols;      // threads of a row, rows of a step
-    static_assert(kThreads % kCols == 0 && kRows % kStep == 0 && kStep % (64 / kCols) == 0 && 64 % kCols == 0, "rows");
+    // threads of a row, and rows of a step; threads past kWork have nothing to do
+    constexpr int kCols = TN / kParts / 8, kWork = kThreads < kRows * kCols ? kThreads : kRows * kCols;
+    constexpr int kStep = kWork / kCols;
+    static_assert(kWork % 64 == 0 && kRows % kStep == 0 && kStep % (64 / kCols) == 0 && 64 % kCols == 0, "rows");
     const uint32_t c = (uint32_t)tid % kCols;
     typedef Epilogue<KIND> E;
     const E epi(f, at, (uint32_t)N, c);
@@ -226,7 +231,7 @@ __device__ __forceinline__ void tile_out(uint8_t* lds0, uint8_t* lds1, uint8_t* 
         for (int m = 0; m < MP; ++m)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                *reinterpret_cast<f32x4*>(place(wm * MP + m) + r * (TN * 4) +
+                *reinterpret_cast<f32x4*>(place(wm * MP + m, mine) + r * (TN * 4) +
                                           chunk_at((uint32_t)(4 * (NT * wn + nt)) + h, r)) =
                     t.acc[kPhase * MP + m][nt];
             }
@@ -254,17 +259,23 @@ __device__ __forceinline__ void tile_out(uint8_t* lds0, uint8_t* lds1, uint8_t* 
             }
             meet();
         }
+        if (kWork < kThreads && tid >= kWork)
+            continue;
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int i = b * kBatch + u;
             const uint32_t at_row = (uint32_t)tid / kCols + kStep * (i % kSteps), rr = at_row % 16;
-            const uint8_t* const from = place(__builtin_amdgcn_readfirstlane((int)(at_row / 16))) + rr * (TN * 4);
+            const int group = __builtin_amdgcn_readfirstlane((int)(at_row / 16));
             float v[kParts][8];
 #pragma unroll
             for (int p = 0; p < kParts; ++p)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const f32x4 s = *reinterpret_cast<const f32x4*>(from + chunk_at(p * (TN / 8) + 2 * c + j, rr));
+                    const uint32_t from = rr * (TN * 4) + chunk_at(p * (TN / 8) + 2 * c + j, rr);
+                    f32x4 s = *reinterpret_cast<const f32x4*>(place(group, 0) + from);
+#pragma unroll
+                    for (int q = 1; q < W::kSplit; ++q)
+                        s += *reinterpret_cast<const f32x4*>(place(group, q) + from);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         v[p][4 * j + e] = s[e];
@@ -277,16 +288,16 @@ __device__ __forceinline__ void tile_out(uint8_t* lds0, uint8_t* lds1, uint8_t* 
 }
 
 template <class W, Kind KIND>
-__global__ __launch_bounds__(64 * W::kWM * W::kWN, W::kD == 2 ? 2 : 1) void ffn_tile_kernel(
+__global__ __launch_bounds__(W::kThreads, W::kD == 2 && W::kSplit == 1 ? 2 : 1) void ffn_tile_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
     const float* __restrict__ sw, Ffn f, const int32_t* __restrict__ offs, int G, int64_t N, int64_t K, uint32_t ntn)
 {
     constexpr int kParts = Epilogue<KIND>::kParts;
     // separate arrays: what is loaded into one does not hold up reads of another
-    __shared__ __attribute__((aligned(16))) uint8_t lds0[W::kBuf];
-    __shared__ __attribute__((aligned(16))) uint8_t lds1[W::kBuf];
-    __shared__ __attribute__((aligned(16))) uint8_t lds2[W::kBuf2];
-    __shared__ __attribute__((aligned(16))) uint8_t lds3[W::kBuf3];
+    __shared__ __attribute__((aligned(16))) uint8_t lds0[W::kSplit * W::kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds1[W::kSplit * W::kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t lds2[W::kSplit * W::kBuf2];
+    __shared__ __attribute__((aligned(16))) uint8_t lds3[W::kSplit * W::kBuf3];
     TileAt at;
     if (!tile_place<W::TM, W::TN, kParts, W::TM == 256>(offs, G, N, ntn, at))
         return;                                   // uniform over the workgroup
@@ -381,38 +392,75 @@ __global__ __launch_bounds__(kThreads) void quantize_sums_kernel(
 
 namespace {
 
-typedef Tile<2, 4, 8, 4, 2> Tile256;
-typedef Tile<2, 4, 4, 4, 3> Tile128x256;
-typedef Tile<2, 2, 4, 4, 2> Tile128;
-typedef Tile<1, 4, 2, 4, 4> Tile32x256;
-typedef Tile<1, 4, 2, 2, 4> Tile32;
-typedef Tile<1, 4, 2, 2, 3> Tile32Shared;
+// The kernels of a call: rows_kernel with 16 or 32 tokens, and the tile kernel of TM tokens x TN
+// rows of the weights.  "Split" ones have groups of waves that share K; "Pair" ones fit a CU
+// twice and have no groups; the others have a CU for themselves.
+enum Which { kRows16, kRows32, k32x64Split, k32x128Split, k32x128Pair, k32x256, k64x64Split, k64x128Split, k128x128Split,
+             k128x128Pair, k128x256, k256x256, kKernels };
 
-// The kernel of a call: the K-splitting one with 16 or 32 tokens, or a tile.  kWide ones have
-// 256 rows of the weights, so that a gated tile has whole scale blocks.
-enum Which { kRows16, kRows32, kSmall, kSmallShared, kSmallWide, kMedium, kMediumWide, kLarge };
+typedef Tile<1, 2, 2, 2, 3, 4> T32x64Split;
+typedef Tile<1, 4, 2, 2, 3, 2> T32x128Split;
+typedef Tile<1, 4, 2, 2, 3> T32x128Pair;
+typedef Tile<1, 4, 2, 4, 4> T32x256;
+typedef Tile<2, 2, 2, 2, 4, 2> T64x64Split;
+typedef Tile<1, 4, 4, 2, 3, 2> T64x128Split;
+typedef Tile<2, 2, 4, 4, 2, 2> T128x128Split;
+typedef Tile<2, 2, 4, 4, 2> T128x128Pair;
+typedef Tile<2, 4, 4, 4, 3> T128x256;
+typedef Tile<2, 4, 8, 4, 2> T256x256;
 
-// fp8: E4M3 outputs are wanted.
+// What a kernel's workgroup costs: us per block of K, and for its beginning and end.  A CU with
+// one workgroup loads 65-75 GB/s whatever the tile, so a block costs by the rows loaded, until
+// the matrix instructions count (256 x 256); two workgroups a CU load less each.  Measured over
+// 24 to 4096 rows of 1 to 8 experts x 512 to 4096 features x 512 to 7168 deep: the choice was
+// within 10 % of the best kernel but for a few sizes where two are within 20 %.
+struct Cost {
+    int TM, TN;
+    bool pair;
+    float block, ends;
+};
+constexpr Cost kCost[kKernels] = {
+    {16, 32, false, 0.090f, 2.0f},  {32, 32, false, 0.120f, 2.0f},  {32, 64, false, 0.190f, 2.0f},
+    {32, 128, false, 0.275f, 2.0f}, {32, 128, true, 0.340f, 0.5f},  {32, 256, false, 0.480f, 2.0f},
+    {64, 64, false, 0.260f, 2.0f},  {64, 128, false, 0.370f, 2.0f}, {128, 128, false, 0.570f, 3.0f},
+    {128, 128, true, 0.680f, 1.0f}, {128, 256, false, 0.840f, 3.0f}, {256, 256, false, 1.800f, 5.0f}};
+constexpr int64_t kMaxSums = 16 << 20;            // bytes of FP32 sums that are worth a second launch
+
+// Whether a kernel's tiles have whole scale blocks of an E4M3 output.
+constexpr bool whole_blocks(Kind kind, Which w) { return kCost[w].TN >= (kind == kGated ? 256 : 128); }
+
+// The kernel of a call, by its estimated time.  fp8: E4M3 outputs are wanted.  The rows are taken
+// to be M_cap, the only count that the host has, over all experts.
 Which choose(Kind kind, bool fp8, int32_t G, int64_t M_cap, int64_t N, int64_t K)
 {
-    const int64_t n = kind == kGated ? 2 * N : N;
-    const int64_t rows16 = tiles(M_cap, G, n, 16, kRowsTN), rows32 = tiles(M_cap, G, n, 32, kRowsTN);
-    if (rows16 <= 320 || (rows16 <= 512 && rows32 > 320 && K > 4096))
-        return kRows16;
-    if (rows32 <= 320)
-        return kRows32;
-    if (M_cap >= 192 * (int64_t)G && tiles(M_cap, G, n, 256, 256) >= 192)
-        return kLarge;
-    const bool wide = kind == kGated && fp8;
-    if (M_cap >= 12 * (int64_t)G && tiles(M_cap, G, n, 128, 128) >= 128)
-        return wide && 4 * M_cap * N > (8 << 20) ? kMediumWide : kMedium;
-    return tiles(M_cap, G, n, 32, 128) <= 256 ? kSmall : wide ? kSmallWide : kSmallShared;
-}
-
-// Whether E4M3 outputs of a kernel go through FP32 sums and a second launch.
-bool by_sums(Kind kind, Which w)
-{
-    return w == kRows16 || w == kRows32 || (kind == kGated && (w == kSmall || w == kMedium));
+    const double n = kind == kGated ? 2.0 * N : N, blocks = (double)((K + kBK - 1) / kBK);
+    const double live = (double)(G < M_cap ? G : M_cap);
+    const int64_t sums = 4 * M_cap * (kind == kGradient ? 2 * N : N);
+    Which best = k256x256;
+    double least = 0;
+    for (int i = 0; i < kKernels; ++i) {
+        const Which w = (Which)i;
+        const Cost& c = kCost[i];
+        const bool whole = whole_blocks(kind, w);
+        if ((kind != kGated || !fp8) && (w == k32x256 || w == k128x256))
+            continue;                             // (there for whole scale blocks alone)
+        if (fp8 && !whole && sums > kMaxSums)
+            continue;
+        // an expert's last tile is half full on average, and every expert has one
+        const double per = M_cap / (double)c.TM;
+        const double tiles = (live > 1 ? fmax(per + 0.5 * live, live) : ceil(per)) * ceil(n / c.TN) / 256;
+        double rounds = fmax(1, c.pair || w == k256x256 ? tiles : ceil(tiles)), block = c.block;
+        if (w == k256x256 && tiles < 1)
+            block *= 0.67 + 0.33 * tiles;         // (free CUs leave the others more of the caches and of the clock)
+        double us = rounds * (blocks * block + c.ends);
+        if (fp8 && !whole)
+            us += 3 + sums * 2e-6;                // (the second launch)
+        if (i == 0 || us < least) {
+            best = w;
+            least = us;
+        }
+    }
+    return best;
 }
 
 template <Kind KIND>
@@ -421,7 +469,7 @@ hipError_t launch_ffn(const uint8_t* a, const float* sa, const uint8_t* w, const
 {
     constexpr int kParts = Epilogue<KIND>::kParts;
     const Which which = choose(KIND, f.q != nullptr, G, M_cap, N, K);
-    const bool then = f.q && by_sums(KIND, which);
+    const bool then = f.q && !whole_blocks(KIND, which);
     int g = G;
     int64_t n = N, k = K;
     uint32_t nt = 0;                              // feature tiles (tile kernel), token tiles (rows kernel)
@@ -435,7 +483,7 @@ hipError_t launch_ffn(const uint8_t* a, const float* sa, const uint8_t* w, const
     auto tile = [&](auto type) {
         typedef decltype(type) T;
         nt = (uint32_t)((N + T::TN / kParts - 1) / (T::TN / kParts));
-        return launch((const void*)ffn_tile_kernel<T, KIND>, T::TM, T::TN / kParts, 64 * T::kWaves);
+        return launch((const void*)ffn_tile_kernel<T, KIND>, T::TM, T::TN / kParts, T::kThreads);
     };
     auto rows = [&](int TM, const void* kernel) {
         nt = (uint32_t)tiles(M_cap, G, 1, TM, 1);
@@ -445,14 +493,18 @@ hipError_t launch_ffn(const uint8_t* a, const float* sa, const uint8_t* w, const
         switch (which) {
         case kRows16: return rows(16, (const void*)ffn_rows_kernel<1, KIND>);
         case kRows32: return rows(32, (const void*)ffn_rows_kernel<2, KIND>);
-        case kLarge: return tile(Tile256{});
-        case kMedium: return tile(Tile128{});
-        case kSmall: return tile(Tile32{});
-        case kSmallShared: return tile(Tile32Shared{});
+        case k32x64Split: return tile(T32x64Split{});
+        case k32x128Split: return tile(T32x128Split{});
+        case k32x128Pair: return tile(T32x128Pair{});
+        case k64x64Split: return tile(T64x64Split{});
+        case k64x128Split: return tile(T64x128Split{});
+        case k128x128Split: return tile(T128x128Split{});
+        case k128x128Pair: return tile(T128x128Pair{});
+        case k256x256: return tile(T256x256{});
         default: break;
         }
         if constexpr (KIND == kGated)
-            return which == kMediumWide ? tile(Tile128x256{}) : tile(Tile32x256{});
+            return which == k32x256 ? tile(T32x256{}) : tile(T128x256{});
         return hipErrorInvalidValue;              // (no other kind chooses these)
     };
     const hipError_t e = first();
@@ -471,11 +523,11 @@ hipError_t launch_ffn(const uint8_t* a, const float* sa, const uint8_t* w, const
 
 int64_t gated_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
 {
-    return by_sums(kGated, choose(kGated, true, G, M_cap, I, K)) ? 4 * M_cap * I : 0;
+    return whole_blocks(kGated, choose(kGated, true, G, M_cap, I, K)) ? 0 : 4 * M_cap * I;
 }
 int64_t gated_backward_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
 {
-    return by_sums(kGradient, choose(kGradient, true, G, M_cap, I, K)) ? 8 * M_cap * I : 0;
+    return whole_blocks(kGradient, choose(kGradient, true, G, M_cap, I, K)) ? 0 : 8 * M_cap * I;
 }
 
 hipError_t launch_gated_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, const float* bias,

@@ -70,14 +70,16 @@ struct TileCtx {
     uint32_t arow, wrow, c0, c1;                  // fragments: LDS offsets of the lane's rows, chunks
     uint32_t scl_at;                              // slot of the lane's first token scale
     uint32_t turn, blocks;                        // the block of K that stage 0 takes, and their number
+    uint32_t first, count;                        // where groups of waves share K: this group's blocks
 };
 
-// The tile of WM x WN waves, each 16 MT tokens x 16 NT features, with D stage buffers.
-template <int WM, int WN, int MT, int NT, int D>
+// The tile of WM x WN waves, each 16 MT tokens x 16 NT features, with D stage buffers.  SPLIT > 1:
+// so many groups of these waves, each with buffers of its own and a run of K's blocks.
+template <int WM, int WN, int MT, int NT, int D, int SPLIT = 1>
 struct Tile {
-    static constexpr int kWM = WM, kWN = WN, kMT = MT, kNT = NT, kD = D;
+    static constexpr int kWM = WM, kWN = WN, kMT = MT, kNT = NT, kD = D, kSplit = SPLIT;
     static constexpr int TM = 16 * MT * WM, TN = 16 * NT * WN;
-    static constexpr int kWaves = WM * WN;
+    static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves * SPLIT;      // (of a group; of all)
     static constexpr int kLoadsA = TM / 8 / kWaves, kLoadsW = TN / 8 / kWaves;   // 8-row loads of a wave
     static constexpr int kSlots = 64 * kWaves;              // scale slots (those past TM are not read)
     static constexpr int kTiles = MT * NT;
@@ -105,7 +107,7 @@ struct Tile {
     static constexpr int kBuf2 = D > 2 ? kBuf : kLate, kBuf3 = D > 3 ? kBuf : kHalves ? kLate : 16;   // lds2, lds3
     static_assert(D >= 2 && D <= 4, "stage buffers");
     static_assert(TM % (8 * kWaves) == 0 && TN % (8 * kWaves) == 0 && TM <= kSlots, "loads");
-    static_assert(TN % 128 == 0 && 128 % (16 * NT) == 0, "a wave's features lie in one scale block");
+    static_assert((TN % 128 == 0 || 128 % TN == 0) && 128 % (16 * NT) == 0, "a wave's features lie in one scale block");
     static_assert(!kHalves || (MT % 2 == 0 && kLoadsA % 2 == 0 && MT >= 4), "halves");
     static_assert((MT == 2 || MT % 4 == 0) && kTiles % 4 == 0, "scale reads, ring of products");
 
@@ -117,9 +119,14 @@ struct Tile {
         float wsc[D];                             // the weights' scale of the stages
     };
 
+    static constexpr uint32_t kNoBlock = 0xFFFFFF;          // past K for every K
     // The block of K that stage s takes.
     static __device__ __forceinline__ uint32_t block_of(const TileCtx<D>& cx, uint32_t s)
     {
+        if constexpr (SPLIT > 1) {
+            const uint32_t in = kTurn ? s + cx.turn < cx.count ? s + cx.turn : s + cx.turn - cx.count : s;
+            return s < cx.count ? cx.first + in : kNoBlock;
+        }
         if constexpr (!kTurn)
             return s;
         const uint32_t b = s + cx.turn;
@@ -139,7 +146,8 @@ struct Tile {
         for (int j = from; j < to; ++j) {
             const bool tok = j >= kLoadsW;
             const int i = tok ? j - kLoadsW : j;
-            const int half = tok && kHalves ? i / (kLoadsA / 2) : 0, in_half = tok && kHalves ? i % (kLoadsA / 2) : i;
+            constexpr int kInHalf = kHalves ? kLoadsA / 2 : kLoadsA + 1;
+            const int half = tok ? i / kInHalf : 0, in_half = tok ? i % kInHalf : i;
             const int rows = 8 * (in_half + half * MT);
             uint8_t* const to_buf = half ? cx.late[b] : cx.buf[b];
             const uint32_t c = tok ? (in_half & 1 ? cx.ac1 : cx.ac0) : (i & 1 ? cx.wc1 : cx.wc0);
@@ -328,7 +336,8 @@ __device__ __forceinline__ bool tile_place(const int32_t* __restrict__ offs, int
 // A tile's sums, in t: lane (r, h) = (lane % 16, lane / 16) of wave (wm, wn) = (wave % WM,
 // wave / WM) holds in acc[mt][nt] those of token 16 (MT wm + mt) + r and tile features
 // 16 (NT wn + nt) + 4 h + (0..3).  The LDS arrays are free again afterwards.  lds2 and lds3 are
-// the third and fourth buffer, or the late rows of two.
+// the third and fourth buffer, or the late rows of two; every array has a part for each group,
+// whose sums are of its blocks alone.
 template <class W, int kParts>
 __device__ __forceinline__ void tile_sums(uint8_t* lds0, uint8_t* lds1, uint8_t* lds2, uint8_t* lds3,
                                           const uint8_t* __restrict__ a, const float* __restrict__ sa,
@@ -339,7 +348,8 @@ __device__ __forceinline__ void tile_sums(uint8_t* lds0, uint8_t* lds1, uint8_t*
     static_assert(kParts == 1 || (WN % 2 == 0 && W::kWaves % 2 == 0), "a wave loads and multiplies one part");
     const int tid = threadIdx.x;
     const int lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % W::kWaves;
+    const uint32_t group = W::kSplit == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 6) / W::kWaves;
     const int g = at.g, rows = at.rows, cols = at.cols;
     const int64_t row0 = at.row0, n0 = at.n0;
     const uint32_t kb_n = (uint32_t)((K + kBK - 1) / kBK);
@@ -356,27 +366,32 @@ __device__ __forceinline__ void tile_sums(uint8_t* lds0, uint8_t* lds1, uint8_t*
     const uint32_t al = (uint32_t)(W::kLoadsA * wave) / (W::kHalves ? 2 : 1);      // first 8-row groups: in LDS
     const uint32_t ag = W::kHalves ? 2 * MT * (al / MT) + al % MT : al;            // of the tile
     const uint32_t wg = (uint32_t)(W::kLoadsW * wave);
-    const uint32_t slot = (uint32_t)tid;
+    const uint32_t slot = (uint32_t)tid % (64 * W::kWaves);
     const uint32_t srow = slot / (16 * MT) * (16 * MT) + slot % MT * 16 + slot / MT % 16;
     // the part that the wave loads, and the one that it multiplies
     const uint32_t lpart = 8 * wg / (TN / kParts), part = (uint32_t)(16 * NT * wn) / (TN / kParts);
     const uint32_t nb = min(((uint32_t)n0 + 16 * NT * wn - part * (TN / kParts)) / 128, nb_n - 1);
     TileCtx<D> cx;
-    cx.buf[0] = lds0;
-    cx.buf[1] = lds1;
+    cx.buf[0] = lds0 + group * W::kBuf;
+    cx.buf[1] = lds1 + group * W::kBuf;
     if constexpr (D > 2)
-        cx.buf[2] = lds2;
+        cx.buf[2] = lds2 + group * W::kBuf2;
     if constexpr (D > 3)
-        cx.buf[3] = lds3;
-    cx.late[0] = lds2;                            // (of two buffers)
-    cx.late[1] = lds3;
+        cx.buf[3] = lds3 + group * W::kBuf3;
+    cx.late[0] = lds2 + group * W::kBuf2;         // (of two buffers)
+    cx.late[1] = lds3 + group * W::kBuf3;
     cx.ra = strip_rsrc(a + row0 * K, (uint64_t)rows * (uint64_t)K);
     cx.rw = strip_rsrc(w + ((kParts * (int64_t)g + lpart) * N + n0) * K, (uint64_t)cols * (uint64_t)K);
     cx.rsa = strip_rsrc(sa + row0 * kb_n, (uint64_t)rows * kb_n * 4);
     cx.rsw = strip_rsrc(sw + ((kParts * (int64_t)g + part) * nb_n + nb) * kb_n, (uint64_t)kb_n * 4);
     cx.K = (uint32_t)K;
     cx.blocks = kb_n;
-    cx.turn = K % 4096 == 0 ? (at.ntile + 5 * (uint32_t)g) % kb_n : 0;
+    // (every group runs the same number of stages, as they meet at the same barriers)
+    const uint32_t stages = (kb_n + W::kSplit - 1) / W::kSplit;
+    cx.first = group * stages;
+    cx.count = cx.first >= kb_n ? 0 : min(stages, kb_n - cx.first);
+    const uint32_t run = W::kSplit == 1 ? kb_n : max(cx.count, 1u);
+    cx.turn = K % 4096 == 0 ? (at.ntile + 5 * (uint32_t)g) % run : 0;
     cx.abase = (8 * ag + l8) * cx.K;
     cx.wbase = (8 * wg - lpart * (TN / kParts) + l8) * cx.K;
     cx.ac0 = 16 * (lc ^ ((4 * ag + l16) & 7));
@@ -424,7 +439,7 @@ __device__ __forceinline__ void tile_sums(uint8_t* lds0, uint8_t* lds1, uint8_t*
     // this takes 15.5, 1501 rows x 1352 x 1744); the loads and reads for a stage past the last
     // find zeros
     uint32_t s = 0;
-    for (; s + D <= kb_n; s += D) {
+    for (; s + D <= stages; s += D) {
         W::template stage<0>(cx, t, s);
         W::template stage<1>(cx, t, s + 1);
         if constexpr (D > 2)
@@ -432,13 +447,13 @@ __device__ __forceinline__ void tile_sums(uint8_t* lds0, uint8_t* lds1, uint8_t*
         if constexpr (D > 3)
             W::template stage<3>(cx, t, s + 3);
     }
-    if (s < kb_n)
+    if (s < stages)
         W::template stage<0>(cx, t, s);
     if constexpr (D > 2)
-        if (s + 1 < kb_n)
+        if (s + 1 < stages)
             W::template stage<1>(cx, t, s + 1);
     if constexpr (D > 3)
-        if (s + 2 < kb_n)
+        if (s + 2 < stages)
             W::template stage<2>(cx, t, s + 2);
     W::template add<-3>(t);
     W::template add<-2>(t);

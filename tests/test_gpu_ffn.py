@@ -123,7 +123,6 @@ def check_dense(counts, N, K, act="gelu", bias=True, residual=True, pre=True, sl
         fr.check_bf16(got[1], want_p, ep, "pre")
 
 
-# (counts, features, K) that reach each kernel by the rules of block_ffn.hip
 SHAPES = [
     ([1], 8, 16), ([1], 256, 128), ([3], 24, 144), ([0, 1, 0, 2], 136, 272), ([16], 512, 1024), ([17], 512, 1024),
     ([0] * 5, 64, 64), ([33, 0, 5], 1000, 336), ([64, 65, 63], 384, 640), ([257], 1352, 1744), ([2, 0, 4, 1, 7, 0, 3, 8], 2048, 1040),
@@ -161,6 +160,40 @@ def test_gradient(counts, N, K):
 @pytest.mark.parametrize("counts,N,K", SHAPES)
 def test_dense(counts, N, K):
     check_dense(counts, N, K, act=ACTS[(N // 8 + K + 3) % 5], seed=N + K)
+
+
+# sizes that the estimate of block_ffn.hip gives to kernels the above do not reach: groups of
+# waves that share K (with blocks for all of them, and with fewer), pairs on a CU, wide tiles
+GATED = [
+    ([17], 2064, 1040), ([1, 0, 2], 1552, 2064), ([1, 0, 2], 3088, 4096), ([16, 20, 1, 0, 40, 16, 30, 7], 1024, 4096),
+    ([130, 120, 139], 2064, 1040), ([60, 64, 129, 1, 0, 70, 88, 90], 1552, 4096), ([50, 51, 49, 0, 64, 1, 100, 85], 2064, 128),
+    ([30, 0, 57], 8208, 128), ([600, 500], 4112, 272), ([900, 1000], 2064, 144),
+]
+OTHERS = [
+    ([17], 4112, 1040), ([1, 2], 4112, 2064), ([1, 2], 8208, 4096), ([37], 8208, 4096), ([130, 120, 139], 4112, 1040), ([2], 256, 4096),
+    ([127], 12304, 4096), ([50, 51, 49, 0, 64, 1, 100, 85], 4112, 128), ([45, 0, 1, 0, 0], 1552, 4096),
+]
+
+
+@pytest.mark.parametrize("counts,N,K", GATED)
+def test_gated_every_kernel(counts, N, K):
+    check_gated(counts, N, K, fp8=False, seed=N)
+    check_gated(counts, N, K, act="gelu", h=False, seed=N + 1)
+
+
+@pytest.mark.parametrize("counts,N,K", OTHERS)
+def test_others_every_kernel(counts, N, K):
+    check_gradient(counts, N, K, fp8=False, seed=N)
+    check_gradient(counts, N // 128 * 128, K, act="gelu", seed=N + 1)
+    check_dense(counts, N, K, seed=N + 2)
+
+
+@pytest.mark.parametrize("K", [16, 144, 272, 400, 528, 656])
+@pytest.mark.parametrize("counts,N", [([17], 4112), ([1, 2], 8208), ([140, 130, 129], 4112), ([70, 0, 64, 33], 4104)])
+def test_few_blocks_of_k(counts, N, K):
+    """One to six blocks of K, the last one partial: fewer than the waves or groups that share them."""
+    check_dense(counts, N, K, seed=K + N)
+    check_gated(counts, N // 32 * 16, K, seed=K + N)
 
 
 @pytest.mark.parametrize("act", ACTS)
