@@ -711,17 +711,20 @@ def _ffn_workspace(name: str, *sizes: int) -> int:
 
 
 def mxfp4_fp8_gated_gemm_workspace(G: int, M_cap: int, I: int, K: int) -> int:
-    """Bytes of workspace of mxfp4_fp8_gated_gemm with FP8 outputs; -1 for invalid sizes."""
+    """Bytes of workspace for calls of mxfp4_fp8_gated_gemm with FP8 outputs on up to M_cap rows;
+    -1 for invalid sizes."""
     return _ffn_workspace("mxfp4_fp8_gated_gemm_workspace", int(G), int(M_cap), int(I), int(K))
 
 
 def mxfp4_fp8_gated_gemm_backward_workspace(G: int, M_cap: int, I: int, K: int) -> int:
-    """Bytes of workspace of mxfp4_fp8_gated_gemm_backward with FP8 outputs; -1 for invalid sizes."""
+    """Bytes of workspace for calls of mxfp4_fp8_gated_gemm_backward with FP8 outputs on up to M_cap
+    rows; -1 for invalid sizes."""
     return _ffn_workspace("mxfp4_fp8_gated_gemm_backward_workspace", int(G), int(M_cap), int(I), int(K))
 
 
 def mxfp4_act_rows_backward_workspace(G: int, M_cap: int, N: int) -> int:
-    """Bytes of workspace of mxfp4_act_rows_backward with bias gradients; -1 for invalid sizes."""
+    """Bytes of workspace for calls of mxfp4_act_rows_backward with bias gradients on up to M_cap
+    rows; -1 for invalid sizes."""
     return _ffn_workspace("mxfp4_act_rows_backward_workspace", int(G), int(M_cap), int(N))
 
 

@@ -48,8 +48,11 @@ hipError_t launch_fp8_rows_f32(const uint16_t*, uint8_t*, float*, const int32_t*
                                hipStream_t);
 hipError_t launch_block_gemm(const uint8_t*, const float*, const uint8_t*, const float*, uint16_t*, const int32_t*,
                              int32_t, int64_t, int64_t, int64_t, hipStream_t);
-int64_t gated_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K);
-int64_t gated_backward_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K);
+bool act_rows_uses_workspace(int64_t M_cap);
+bool gated_uses_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K);
+bool gated_backward_uses_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K);
+int64_t gated_workspace(int64_t M_cap, int64_t I);
+int64_t gated_backward_workspace(int64_t M_cap, int64_t I);
 hipError_t launch_gated_gemm(const uint8_t*, const float*, const uint8_t*, const float*, const float*, uint16_t*,
                              uint8_t*, float*, uint16_t*, float*, const int32_t*, int32_t, int64_t, int64_t, int64_t,
                              int, hipStream_t);
@@ -558,7 +561,7 @@ mxfp4_status mxfp4_fp8_block_gemm(const uint8_t* a_e4m3, const float* a_scales, 
 
 int64_t mxfp4_fp8_gated_gemm_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
 {
-    return check_product(G, M_cap, I, K, 2) == MXFP4_OK ? mxfp4::gated_workspace(G, M_cap, I, K) : -1;
+    return check_product(G, M_cap, I, K, 2) == MXFP4_OK ? mxfp4::gated_workspace(M_cap, I) : -1;
 }
 
 mxfp4_status mxfp4_fp8_gated_gemm(const uint8_t* a_e4m3, const float* a_scales, const uint8_t* w_e4m3,
@@ -574,7 +577,7 @@ mxfp4_status mxfp4_fp8_gated_gemm(const uint8_t* a_e4m3, const float* a_scales, 
         return st;
     if (!check_act(act) || (q_e4m3 && I % 16 != 0))
         return MXFP4_ERR_SHAPE;
-    if (q_e4m3 && !workspace && mxfp4::gated_workspace(G, M_cap, I, K) > 0)
+    if (q_e4m3 && !workspace && M_cap > 0 && mxfp4::gated_uses_workspace(G, M_cap, I, K))
         return MXFP4_ERR_NULL;
     if (!aligned(a_e4m3, 16) || !aligned(a_scales, 16) || !aligned(w_e4m3, 16) || !aligned(w_scales, 16) ||
         !aligned(bias, 16) || !aligned(out_bf16, 16) || !aligned(q_e4m3, 16) || !aligned(q_scales, 16) ||
@@ -590,7 +593,7 @@ mxfp4_status mxfp4_fp8_gated_gemm(const uint8_t* a_e4m3, const float* a_scales, 
 int64_t mxfp4_fp8_gated_gemm_backward_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
 {
     return check_product(G, M_cap, I, K, 1) == MXFP4_OK && I <= kMaxGemmDim / 2
-               ? mxfp4::gated_backward_workspace(G, M_cap, I, K) : -1;
+               ? mxfp4::gated_backward_workspace(M_cap, I) : -1;
 }
 
 mxfp4_status mxfp4_fp8_gated_gemm_backward(const uint8_t* a_e4m3, const float* a_scales, const uint8_t* w_e4m3,
@@ -608,7 +611,7 @@ mxfp4_status mxfp4_fp8_gated_gemm_backward(const uint8_t* a_e4m3, const float* a
     if (!check_act(act) || I > kMaxGemmDim / 2 || (M_cap > 0 && 2 * I > kMaxElems / M_cap) ||
         (dq_e4m3 && I % 128 != 0))
         return MXFP4_ERR_SHAPE;
-    if (dq_e4m3 && !workspace && mxfp4::gated_backward_workspace(G, M_cap, I, K) > 0)
+    if (dq_e4m3 && !workspace && M_cap > 0 && mxfp4::gated_backward_uses_workspace(G, M_cap, I, K))
         return MXFP4_ERR_NULL;
     if (!aligned(a_e4m3, 16) || !aligned(a_scales, 16) || !aligned(w_e4m3, 16) || !aligned(w_scales, 16) ||
         !aligned(h_bf16, 16) || !aligned(dh_bf16, 16) || !aligned(dq_e4m3, 16) || !aligned(dq_scales, 16) ||
@@ -668,7 +671,7 @@ mxfp4_status mxfp4_act_rows_backward(const uint16_t* dout_bf16, const uint16_t* 
         return st;
     if (!check_act(act) || (q_e4m3 && N % 16 != 0))
         return MXFP4_ERR_SHAPE;
-    if (dbias && !workspace && mxfp4::act_rows_workspace(G, M_cap, N) > 0)
+    if (dbias && !workspace && mxfp4::act_rows_uses_workspace(M_cap))
         return MXFP4_ERR_NULL;
     if (!aligned(dout_bf16, 16) || !aligned(pre_bf16, 16) || !aligned(dpre_bf16, 16) || !aligned(q_e4m3, 16) ||
         !aligned(q_scales, 16) || !aligned(dbias, 16) || !aligned(workspace, 16) || !aligned(group_offsets, 4))

@@ -140,6 +140,8 @@ __global__ __launch_bounds__(kSumCols* kSumSplit) void bias_sum_kernel(
     }
 }
 
+bool act_rows_uses_workspace(int64_t M_cap) { return M_cap > 128; }
+
 namespace {
 
 int64_t act_tiles(int32_t G, int64_t M_cap, int rows)
@@ -148,10 +150,10 @@ int64_t act_tiles(int32_t G, int64_t M_cap, int rows)
     return (M_cap + live * (rows - 1)) / rows;
 }
 
-// Rows of a tile; 0: all of an expert's.
+// Rows of a tile; 0: all of an expert's.  (One launch is XXX)
 int act_tile_rows(int32_t G, int64_t M_cap, int64_t N)
 {
-    if (M_cap <= 128)
+    if (!act_rows_uses_workspace(M_cap))
         return 0;
     const int64_t strips = (N + kActCols - 1) / kActCols;
     return act_tiles(G, M_cap, kManyRows) * strips < 1024 ? kFewRows : kManyRows;
@@ -159,10 +161,10 @@ int act_tile_rows(int32_t G, int64_t M_cap, int64_t N)
 
 }  // namespace
 
+// Bytes that a call with bias gradients and every one of fewer rows use at most.
 int64_t act_rows_workspace(int32_t G, int64_t M_cap, int64_t N)
 {
-    const int rows = act_tile_rows(G, M_cap, N);
-    return rows ? 4 * act_tiles(G, M_cap, rows) * N : 0;
+    return act_rows_uses_workspace(M_cap) ? 4 * act_tiles(G, M_cap, kFewRows) * N : 0;
 }
 
 hipError_t launch_act_rows_backward(const uint16_t* dout, const uint16_t* pre, uint16_t* dpre, uint8_t* q,

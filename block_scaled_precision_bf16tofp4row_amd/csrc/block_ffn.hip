@@ -15,6 +15,8 @@
 // in whole lines.
 #include <math.h>
 
+#include <algorithm>
+
 #include "activation.h"
 #include "block_tile.h"
 
@@ -99,7 +101,7 @@ struct Epilogue {
         if constexpr (KIND == kGradient) {
 #pragma unroll
             for (int p = 0; p < 2; ++p)
-                in.h[p] = __builtin_amdgcn_raw_buffer_load_b128(rh, at_byte(row, 2, p, 2), 0, 0);
+                in.h[p] = __builtin_amdgcn_raw_buffer_load_b128(rh, at_byte(row, 2, p, 2), 0, 2);      // (past the caches)
         } else if constexpr (KIND == kDense) {
             if (f.h)
                 in.h[0] = __builtin_amdgcn_raw_buffer_load_b128(rh, at_byte(row, 1, 0, 2), 0, 0);
@@ -521,14 +523,18 @@ hipError_t launch_ffn(const uint8_t* a, const float* sa, const uint8_t* w, const
 
 }  // namespace
 
-int64_t gated_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
+// Whether a call with E4M3 outputs uses its workspace, and the bytes that it and every call of
+// fewer rows use at most.
+bool gated_uses_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
 {
-    return whole_blocks(kGated, choose(kGated, true, G, M_cap, I, K)) ? 0 : 4 * M_cap * I;
+    return !whole_blocks(kGated, choose(kGated, true, G, M_cap, I, K));
 }
-int64_t gated_backward_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
+bool gated_backward_uses_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K)
 {
-    return whole_blocks(kGradient, choose(kGradient, true, G, M_cap, I, K)) ? 0 : 8 * M_cap * I;
+    return !whole_blocks(kGradient, choose(kGradient, true, G, M_cap, I, K));
 }
+int64_t gated_workspace(int64_t M_cap, int64_t I) { return std::min(4 * M_cap * I, kMaxSums); }
+int64_t gated_backward_workspace(int64_t M_cap, int64_t I) { return std::min(8 * M_cap * I, kMaxSums); }
 
 hipError_t launch_gated_gemm(const uint8_t* a, const float* sa, const uint8_t* w, const float* sw, const float* bias,
                              uint16_t* out, uint8_t* q, float* q_scales, uint16_t* h, float* work,

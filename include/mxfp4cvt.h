@@ -346,8 +346,9 @@ mxfp4_status mxfp4_fp8_block_gemm(const uint8_t* a_e4m3, const float* a_scales, 
  * result on ordinary data.  FP8 outputs are E4M3 rows with one FP32 scale per 1x128 block,
  * made as mxfp4_dispatch_fp8_rows makes them, but from the FP32 values: the operand of the
  * next mxfp4_fp8_block_gemm or mxfp4_fp8_block_gemm_act.
- * workspace: the bytes that the call's _workspace function gives (NULL where that is 0; -1
- * for invalid sizes), not shared by calls that overlap; nothing has to be in it. */
+ * workspace: the bytes that the call's _workspace function gives (-1 for invalid sizes), which
+ * are enough for every call of at most M_cap rows; not shared by calls that overlap; nothing
+ * has to be in it.  NULL is an error (MXFP4_ERR_NULL) only where the call would use it. */
 typedef enum {
     MXFP4_ACT_NONE = 0,
     MXFP4_ACT_RELU = 1,
@@ -366,7 +367,7 @@ typedef enum {
  *   out_bf16 [M_cap, I] (optional), q_e4m3 [M_cap, I] with q_scales [M_cap, ceil(I/128)]
  *           (optional, both or none): out in either form; at least one is given.
  *   h_bf16  [M_cap, 2 I] (optional): for the gradient.
- *   workspace: for q, where few rows let workgroups share K.
+ *   workspace: for q, where a workgroup has no whole scale blocks (few rows); at most 2^24 bytes.
  *   I must be a multiple of 8, of 16 for q, and at most 2^19. */
 mxfp4_status mxfp4_fp8_gated_gemm(const uint8_t* a_e4m3, const float* a_scales, const uint8_t* w_e4m3,
                                   const float* w_scales, const float* bias, uint16_t* out_bf16, uint8_t* q_e4m3,
@@ -413,7 +414,7 @@ mxfp4_status mxfp4_fp8_block_gemm_act(const uint8_t* a_e4m3, const float* a_scal
  *   q_scales [M_cap, ceil(N/128)] (optional, both or none), dbias [G, N] FP32 (optional; every
  *   element is written, 0 for an expert without rows, also when M_cap == 0): at least one of
  *   the three is given.  dbias is summed in a fixed order.
- *   workspace: for dbias of many rows.   N must be a multiple of 8, of 16 for q, and at most
+ *   workspace: for dbias of more than 128 rows.   N must be a multiple of 8, of 16 for q, and at most
  *   2^20. */
 mxfp4_status mxfp4_act_rows_backward(const uint16_t* dout_bf16, const uint16_t* pre_bf16, uint16_t* dpre_bf16,
                                      uint8_t* q_e4m3, float* q_scales, float* dbias, void* workspace,

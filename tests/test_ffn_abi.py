@@ -47,17 +47,17 @@ PRODUCT_SHAPES = [dict(G=0), dict(M=-1), dict(M=1 << 31), dict(K=0), dict(K=24),
 def test_gated_refusals(lib):
     c = functools.partial(_gated, lib)
     _refuses(c, NULL, [dict(a=None), dict(sa=None), dict(w=None), dict(sw=None), dict(offs=None), dict(q=None),
-                       dict(qs=None), dict(out=None, q=None, qs=None), dict(ws=None)])
+                       dict(qs=None), dict(out=None, q=None, qs=None), dict(ws=None, M=1, I=2048, K=7168)])
     _refuses(c, SHAPE, PRODUCT_SHAPES + [dict(I=0), dict(I=-8), dict(I=12), dict(I=72), dict(I=(1 << 19) + 16)])
     _refuses(c, ALIGN, [dict(a=A + 8), dict(sa=A + 4), dict(w=A + 1), dict(sw=A + 4), dict(bias=A + 4), dict(out=B + 2),
                         dict(q=B + 8), dict(qs=B + 4), dict(h=B + 2), dict(ws=B + 4), dict(offs=A + 2)])
-    _refuses(c, OK, [dict(M=0), dict(M=0, I=72, q=None, qs=None), dict(M=0, ws=None), dict(M=0, out=None, h=None)])
+    _refuses(c, OK, [dict(M=0), dict(M=0, I=72, q=None, qs=None), dict(M=0, ws=None, I=2048, K=7168), dict(M=0, out=None, h=None)])
 
 
 def test_gated_backward_refusals(lib):
     c = functools.partial(_back, lib)
     _refuses(c, NULL, [dict(a=None), dict(sa=None), dict(w=None), dict(sw=None), dict(h=None), dict(offs=None),
-                       dict(q=None), dict(qs=None), dict(dh=None, q=None, qs=None), dict(ws=None)])
+                       dict(q=None), dict(qs=None), dict(dh=None, q=None, qs=None), dict(ws=None, M=1, I=256, K=4096)])
     _refuses(c, SHAPE, PRODUCT_SHAPES + [dict(I=0), dict(I=12), dict(I=64), dict(I=(1 << 19) + 128)])
     _refuses(c, ALIGN, [dict(a=A + 8), dict(sa=A + 4), dict(w=A + 1), dict(sw=A + 4), dict(h=A + 4), dict(dh=B + 2),
                         dict(q=B + 8), dict(qs=B + 4), dict(out=B + 2), dict(ws=B + 4), dict(offs=A + 2)])
@@ -86,11 +86,16 @@ def test_act_rows_refusals(lib):
 
 def test_workspaces():
     one = mx.mxfp4_fp8_gated_gemm_workspace
-    assert one(1, 1, 2048, 7168) == 4 * 2048 and one(8, 32768, 2048, 7168) == 0
-    assert mx.mxfp4_fp8_gated_gemm_backward_workspace(1, 1, 2048, 7168) == 8 * 2048
-    assert mx.mxfp4_fp8_gated_gemm_backward_workspace(8, 32768, 2048, 7168) == 0
-    assert mx.mxfp4_act_rows_backward_workspace(3, 5, 64) == 0
-    assert mx.mxfp4_act_rows_backward_workspace(8, 32768, 4096) == 4 * 4096 * (32768 // 128 + 7)
+    back = mx.mxfp4_fp8_gated_gemm_backward_workspace
+    assert one(1, 1, 2048, 7168) == 4 * 2048 and back(1, 1, 2048, 7168) == 8 * 2048
+    rows = mx.mxfp4_act_rows_backward_workspace
+    assert rows(3, 5, 64) == 0 and rows(8, 32768, 4096) == 4 * 4096 * (32768 // 32 + 7)
+    # enough for every call of fewer rows
+    for G in (1, 7, 40):
+        for fn in (lambda M: one(G, M, 1040, 512), lambda M: back(G, M, 1024, 512), lambda M: rows(G, M, 1040)):      # noqa: E731
+            sizes = [fn(M) for M in (0, 1, 3, 40, 128, 129, 500, 2000, 4000, 8000, 100000)]
+            assert sizes == sorted(sizes), (G, sizes)
+    assert one(8, 1 << 30, 2048, 7168) == back(8, 1 << 30, 2048, 7168) == 1 << 24
     for fn in (one, mx.mxfp4_fp8_gated_gemm_backward_workspace):
         for bad in ((0, 1, 64, 128), (1, -1, 64, 128), (1, 1, 12, 128), (1, 1, 64, 24), (1, 1, (1 << 19) + 8, 128)):
             assert fn(*bad) == -1, bad
