@@ -48,7 +48,7 @@ hipError_t launch_fp8_rows_f32(const uint16_t*, uint8_t*, float*, const int32_t*
                                hipStream_t);
 hipError_t launch_block_gemm(const uint8_t*, const float*, const uint8_t*, const float*, uint16_t*, const int32_t*,
                              int32_t, int64_t, int64_t, int64_t, hipStream_t);
-bool act_rows_uses_workspace(int64_t M_cap);
+bool act_rows_uses_workspace(int32_t G, int64_t M_cap);
 bool gated_uses_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K);
 bool gated_backward_uses_workspace(int32_t G, int64_t M_cap, int64_t I, int64_t K);
 int64_t gated_workspace(int64_t M_cap, int64_t I);
@@ -671,7 +671,7 @@ mxfp4_status mxfp4_act_rows_backward(const uint16_t* dout_bf16, const uint16_t* 
         return st;
     if (!check_act(act) || (q_e4m3 && N % 16 != 0))
         return MXFP4_ERR_SHAPE;
-    if (dbias && !workspace && mxfp4::act_rows_uses_workspace(M_cap))
+    if (dbias && !workspace && mxfp4::act_rows_uses_workspace(G, M_cap))
         return MXFP4_ERR_NULL;
     if (!aligned(dout_bf16, 16) || !aligned(pre_bf16, 16) || !aligned(dpre_bf16, 16) || !aligned(q_e4m3, 16) ||
         !aligned(q_scales, 16) || !aligned(dbias, 16) || !aligned(workspace, 16) || !aligned(group_offsets, 4))

@@ -140,7 +140,15 @@ __global__ __launch_bounds__(kSumCols* kSumSplit) void bias_sum_kernel(
     }
 }
 
-bool act_rows_uses_workspace(int64_t M_cap) { return M_cap > 128; }
+// Whether sums go to the workspace and a second launch, or a workgroup takes all rows of an
+// expert, which is faster while those are few: 256 rows over 3 experts x 1360: 8.0 us, with
+// tiles 10.2; 500 over 16 x 2048: 8.0, 10.2; 128 rows of one expert x 1360: 9.2, 10.6; but 200 of
+// one x 4096: 13.4, 10.9.  The rows may all be one expert's, so there is a limit (500 of one:
+// 27).
+bool act_rows_uses_workspace(int32_t G, int64_t M_cap)
+{
+    return M_cap > 128 && (M_cap > 96 * (int64_t)G || M_cap > 512);
+}
 
 namespace {
 
@@ -150,10 +158,11 @@ int64_t act_tiles(int32_t G, int64_t M_cap, int rows)
     return (M_cap + live * (rows - 1)) / rows;
 }
 
-// Rows of a tile; 0: all of an expert's.  (One launch is XXX)
+// Rows of a tile; 0: all of an expert's.  Tiles of 32 rows where those of 128 leave CUs free:
+// 2048 rows over 8 experts x 4096: 15.4 us, with 128 rows 19.9; 300 over 3 x 1360: 10.9, 13.2.
 int act_tile_rows(int32_t G, int64_t M_cap, int64_t N)
 {
-    if (!act_rows_uses_workspace(M_cap))
+    if (!act_rows_uses_workspace(G, M_cap))
         return 0;
     const int64_t strips = (N + kActCols - 1) / kActCols;
     return act_tiles(G, M_cap, kManyRows) * strips < 1024 ? kFewRows : kManyRows;
@@ -164,7 +173,7 @@ int act_tile_rows(int32_t G, int64_t M_cap, int64_t N)
 // Bytes that a call with bias gradients and every one of fewer rows use at most.
 int64_t act_rows_workspace(int32_t G, int64_t M_cap, int64_t N)
 {
-    return act_rows_uses_workspace(M_cap) ? 4 * act_tiles(G, M_cap, kFewRows) * N : 0;
+    return act_rows_uses_workspace(G, M_cap) ? 4 * act_tiles(G, M_cap, kFewRows) * N : 0;
 }
 
 hipError_t launch_act_rows_backward(const uint16_t* dout, const uint16_t* pre, uint16_t* dpre, uint8_t* q,
