@@ -292,7 +292,8 @@ __device__ __forceinline__ void tile_out(uint8_t* lds0, uint8_t* lds1, uint8_t* 
 template <class W, Kind KIND>
 __global__ __launch_bounds__(W::kThreads, W::kD == 2 && W::kSplit == 1 ? 2 : 1) void ffn_tile_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
-    const float* __restrict__ sw, Ffn f, const int32_t* __restrict__ offs, int G, int64_t N, int64_t K, uint32_t ntn)
+    const float* __restrict__ sw, Ffn f, const int32_t* __restrict__ offs, int G, int64_t N, int64_t K, uint32_t ntn,
+    bool by_feature)
 {
     constexpr int kParts = Epilogue<KIND>::kParts;
     // separate arrays: what is loaded into one does not hold up reads of another
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(W::kThreads, W::kD == 2 && W::kSplit == 1 ? 2 : 1) 
     __shared__ __attribute__((aligned(16))) uint8_t lds2[W::kSplit * W::kBuf2];
     __shared__ __attribute__((aligned(16))) uint8_t lds3[W::kSplit * W::kBuf3];
     TileAt at;
-    if (!tile_place<W::TM, W::TN, kParts, W::TM == 256>(offs, G, N, ntn, at))
+    if (!tile_place<W::TM, W::TN, kParts, W::TM == 256>(offs, G, N, ntn, at, by_feature))
         return;                                   // uniform over the workgroup
     auto tile = [&](auto type) {
         typedef decltype(type) T;
@@ -413,19 +414,21 @@ typedef Tile<2, 4, 8, 4, 2> T256x256;
 
 // What a kernel's workgroup costs: us per block of K, and for its beginning and end.  A CU with
 // one workgroup loads 65-75 GB/s whatever the tile, so a block costs by the rows loaded, until
-// the matrix instructions count (256 x 256); two workgroups a CU load less each.  Measured over
-// 24 to 4096 rows of 1 to 8 experts x 512 to 4096 features x 512 to 7168 deep: the choice was
-// within 10 % of the best kernel but for a few sizes where two are within 20 %.
+// the matrix instructions count (256 x 256); two workgroups a CU load less each.  Fitted to the
+// times of all kernels at 2100 sizes over 1 to 16000 rows of 1 to 32 experts, 16 to 7168
+// features and 16 to 7680 deep: the chosen kernel takes 1.03 times the best one's time in the
+// mean, 1.11 at most at nine sizes of ten, 1.6 at the worst.
 struct Cost {
     int TM, TN;
     bool pair;
     float block, ends;
 };
 constexpr Cost kCost[kKernels] = {
-    {16, 32, false, 0.090f, 2.0f},  {32, 32, false, 0.120f, 2.0f},  {32, 64, false, 0.190f, 2.0f},
-    {32, 128, false, 0.275f, 2.0f}, {32, 128, true, 0.340f, 0.5f},  {32, 256, false, 0.480f, 2.0f},
-    {64, 64, false, 0.260f, 2.0f},  {64, 128, false, 0.370f, 2.0f}, {128, 128, false, 0.570f, 3.0f},
-    {128, 128, true, 0.680f, 1.0f}, {128, 256, false, 0.840f, 3.0f}, {256, 256, false, 1.800f, 5.0f}};
+    {16, 32, false, 0.097f, 2.8f},  {32, 32, false, 0.110f, 2.8f},  {32, 64, false, 0.157f, 3.0f},
+    {32, 128, false, 0.290f, 1.9f}, {32, 128, true, 0.360f, 0.45f}, {32, 256, false, 0.540f, 2.2f},
+    {64, 64, false, 0.230f, 2.3f},  {64, 128, false, 0.365f, 2.6f}, {128, 128, false, 0.505f, 3.3f},
+    {128, 128, true, 0.680f, 1.2f}, {128, 256, false, 0.830f, 4.5f}, {256, 256, false, 1.550f, 5.8f}};
+constexpr double kBytesUs = 1 / 10.5e6;           // us a byte of weights
 constexpr int64_t kMaxSums = 16 << 20;            // bytes of FP32 sums that are worth a second launch
 
 // Whether a kernel's tiles have whole scale blocks of an E4M3 output.
@@ -439,7 +442,7 @@ Which choose(Kind kind, bool fp8, int32_t G, int64_t M_cap, int64_t N, int64_t K
     const double live = (double)(G < M_cap ? G : M_cap);
     const int64_t sums = 4 * M_cap * (kind == kGradient ? 2 * N : N);
     Which best = k256x256;
-    double least = 0;
+    double least = INFINITY;
     for (int i = 0; i < kKernels; ++i) {
         const Which w = (Which)i;
         const Cost& c = kCost[i];
@@ -450,14 +453,30 @@ Which choose(Kind kind, bool fp8, int32_t G, int64_t M_cap, int64_t N, int64_t K
             continue;
         // an expert's last tile is half full on average, and every expert has one
         const double per = M_cap / (double)c.TM;
-        const double tiles = (live > 1 ? fmax(per + 0.5 * live, live) : ceil(per)) * ceil(n / c.TN) / 256;
-        double rounds = fmax(1, c.pair || w == k256x256 ? tiles : ceil(tiles)), block = c.block;
-        if (w == k256x256 && tiles < 1)
-            block *= 0.67 + 0.33 * tiles;         // (free CUs leave the others more of the caches and of the clock)
+        const double each = live > 1 ? fmax(per / live + 0.5, 1) : ceil(per);
+        const double wide = ceil(n / c.TN), t = each * live * wide / 256;
+        double rounds = ceil(t), block = c.block;
+        if (w == k256x256) {
+            rounds = fmax(1, t + 0.27 * (ceil(t) - t));        // (partial tiles come last)
+            if (t < 1)                            // free CUs leave the others more of the caches and of the clock
+                block *= 0.88f + 0.12f * t;
+            if (M_cap <= 128 * live)              // tiles of half the size
+                block *= 0.57f;
+        } else if (c.pair) {
+            // past 256 workgroups, empty ones among them, some CUs have two and others none
+            rounds = fmax(t, tiles(M_cap, G, (int64_t)n, c.TM, c.TN) > 256 ? 1.4 : 1);
+        } else if (live > 1) {
+            // the number of tiles is off by the last ones' parts: whether it is past a whole round
+            // is a matter of chance
+            const double off = sqrt(live / 12) * wide / 256, near = fmax(1, nearbyint(t));
+            rounds = fmax(1, near + 0.5 * erfc((near - t) / off * M_SQRT1_2));
+        }
         double us = rounds * (blocks * block + c.ends);
+        // (the weights' bytes, which reach two XCDs where an expert has more tiles of rows than one)
+        us = fmax(us, live * n * K * fmin(each, 2) * kBytesUs);
         if (fp8 && !whole)
-            us += 3 + sums * 2e-6;                // (the second launch)
-        if (i == 0 || us < least) {
+            us += 4 + sums * 0.5e-6;              // (the second launch)
+        if (us < least) {
             best = w;
             least = us;
         }
@@ -475,21 +494,24 @@ hipError_t launch_ffn(const uint8_t* a, const float* sa, const uint8_t* w, const
     int g = G;
     int64_t n = N, k = K;
     uint32_t nt = 0;                              // feature tiles (tile kernel), token tiles (rows kernel)
+    bool by_feature = false;                      // (tile kernel)
     void* args[] = {(void*)&a, (void*)&sa, (void*)&w, (void*)&sw, (void*)&f, (void*)&offs, (void*)&g,
-                    (void*)&n, (void*)&k, (void*)&nt};
-    auto launch = [&](const void* kernel, int TM, int features, int threads) {
-        const int64_t grid = tiles(M_cap, G, N, TM, features);
+                    (void*)&n, (void*)&k, (void*)&nt, (void*)&by_feature};
+    auto launch = [&](const void* kernel, int64_t grid, int threads) {
         return grid > 0x7FFFFFFF ? hipErrorInvalidValue
                                  : launch_kernel(kernel, dim3((unsigned)grid), dim3((unsigned)threads), args, stream, !then);
     };
     auto tile = [&](auto type) {
         typedef decltype(type) T;
         nt = (uint32_t)((N + T::TN / kParts - 1) / (T::TN / kParts));
-        return launch((const void*)ffn_tile_kernel<T, KIND>, T::TM, T::TN / kParts, T::kThreads);
+        // (pairs read the weights on two XCDs and the rows on four, the others the weights on one
+        // and the rows on eight)
+        by_feature = T::TM < 256 && (G < M_cap ? G : M_cap) * kParts * N > 4 * M_cap;
+        return launch((const void*)ffn_tile_kernel<T, KIND>, tiles(M_cap, G, N, T::TM, T::TN / kParts), T::kThreads);
     };
     auto rows = [&](int TM, const void* kernel) {
         nt = (uint32_t)tiles(M_cap, G, 1, TM, 1);
-        return launch(kernel, TM, kRowsTN / kParts, 64 * kRowsWaves);
+        return launch(kernel, tiles(M_cap, G, N, TM, kRowsTN / kParts), 64 * kRowsWaves);
     };
     auto first = [&]() {
         switch (which) {

@@ -314,7 +314,8 @@ __device__ __forceinline__ bool find_tile_whole_first(const int32_t* __restrict_
 
 // The workgroup's tile of TM rows and TN rows of the weights; false if it has none.
 template <int TM, int TN, int kParts, bool kWholeFirst>
-__device__ __forceinline__ bool tile_place(const int32_t* __restrict__ offs, int G, int64_t N, uint32_t ntn, TileAt& at)
+__device__ __forceinline__ bool tile_place(const int32_t* __restrict__ offs, int G, int64_t N, uint32_t ntn, TileAt& at,
+                                           bool by_feature = false)
 {
     uint32_t mtile;
     // Workgroups go round-robin over the 8 XCDs, so with pairs of token tiles an XCD has every
@@ -322,14 +323,22 @@ __device__ __forceinline__ bool tile_place(const int32_t* __restrict__ offs, int
     // all of them on one expert or a few neighbours, and an expert with few rows spread over
     // all XCDs.  (Groups of 4 dealt to one XCD each, as the other GEMM has them: 2048 rows over
     // 32 experts 225 us, here 213; 65536 rows x 7168 x 2048 975, 955; 32768 rows 905, 892.)
-    tile_of<2>(blockIdx.x, gridDim.x, ntn, mtile, at.ntile);
+    // by_feature: a run of feature tiles to each XCD, with the token tiles inside: weights that
+    // are most of the bytes are then read by one XCD.
+    if (by_feature) {
+        const uint32_t lin = xcd_remap(blockIdx.x, gridDim.x), ntm = gridDim.x / ntn;
+        at.ntile = lin / ntm;
+        mtile = lin % ntm;
+    } else {
+        tile_of<2>(blockIdx.x, gridDim.x, ntn, mtile, at.ntile);
+    }
+    at.n0 = (int64_t)(TN / kParts) * at.ntile;
+    at.cols = (int)min((int64_t)(TN / kParts), N - at.n0);
     bool found;
     if constexpr (kWholeFirst)
         found = find_tile_whole_first<TM>(offs, G, mtile, at.g, at.row0, at.rows);
     else
         found = find_tile<TM>(offs, G, mtile, at.g, at.row0, at.rows);
-    at.n0 = (int64_t)(TN / kParts) * at.ntile;
-    at.cols = (int)min((int64_t)(TN / kParts), N - at.n0);
     return found;
 }
 

@@ -165,13 +165,16 @@ def test_dense(counts, N, K):
 # sizes that the estimate of block_ffn.hip gives to kernels the above do not reach: groups of
 # waves that share K (with blocks for all of them, and with fewer), pairs on a CU, wide tiles
 GATED = [
-    ([17], 2064, 1040), ([1, 0, 2], 1552, 2064), ([1, 0, 2], 3088, 4096), ([16, 20, 1, 0, 40, 16, 30, 7], 1024, 4096),
-    ([130, 120, 139], 2064, 1040), ([60, 64, 129, 1, 0, 70, 88, 90], 1552, 4096), ([50, 51, 49, 0, 64, 1, 100, 85], 2064, 128),
-    ([30, 0, 57], 8208, 128), ([600, 500], 4112, 272), ([900, 1000], 2064, 144),
+    ([2], 512, 4096), ([17], 2064, 1040), ([40], 2048, 4096), ([21, 19], 3088, 2064), ([1, 0, 2], 1552, 2064), ([1, 0, 2], 1552, 4096), ([1, 0, 2], 3088, 4096),
+    ([16, 20, 1, 0, 40, 16, 30, 7], 1024, 4096), ([130, 120, 139], 2064, 1040), ([130, 120, 150], 2064, 2064),
+    ([20, 30, 0, 60, 10, 40, 17, 20], 1552, 4096), ([60, 64, 129, 1, 0, 70, 88, 90], 1552, 4096),
+    ([300, 100, 200, 90, 207], 1552, 4096), ([50, 51, 49, 0, 64, 1, 100, 85], 2064, 128), ([30, 0, 57], 8208, 128),
+    ([897], 1024, 272), ([600, 500], 4112, 272), ([900, 1000], 2064, 144),
 ]
 OTHERS = [
-    ([17], 4112, 1040), ([1, 2], 4112, 2064), ([1, 2], 8208, 4096), ([37], 8208, 4096), ([130, 120, 139], 4112, 1040), ([2], 256, 4096),
-    ([127], 12304, 4096), ([50, 51, 49, 0, 64, 1, 100, 85], 4112, 128), ([45, 0, 1, 0, 0], 1552, 4096),
+    ([2], 256, 4096), ([17], 4112, 1040), ([40], 4096, 4096), ([30, 0, 31], 4112, 2064), ([1, 2], 4112, 2064), ([1, 2], 4112, 4096), ([1, 2], 8208, 4096),
+    ([37], 8208, 4096), ([130, 120, 139], 4112, 1040), ([127], 12304, 4096), ([45, 0, 1, 0, 0], 1552, 4096),
+    ([50, 51, 49, 0, 64, 1, 100, 85], 4112, 128), ([897], 2064, 272), ([1097], 1552, 272), ([75] * 20, 1032, 2064),
 ]
 
 
