@@ -504,9 +504,16 @@ hipError_t launch_ffn(const uint8_t* a, const float* sa, const uint8_t* w, const
     auto tile = [&](auto type) {
         typedef decltype(type) T;
         nt = (uint32_t)((N + T::TN / kParts - 1) / (T::TN / kParts));
-        // (pairs read the weights on two XCDs and the rows on four, the others the weights on one
-        // and the rows on eight)
-        by_feature = T::TM < 256 && (G < M_cap ? G : M_cap) * kParts * N > 4 * M_cap;
+        // Pairs of token tiles read the weights on two XCDs and the rows on four, runs of feature
+        // tiles the weights on one and the rows on eight.  So runs, where the weights are most of
+        // the bytes and an expert has more than a tile of rows: on average over 194 such sizes
+        // 0.92 of the pairs' time (330 rows over 6 experts x 5376 x 3584 23.2 us, pairs 35.2;
+        // 1044 over 10, gradient, x 768 x 4864 16.5, 24.8), at worst 1.4 (826 over 22, gradient,
+        // x 752 x 2416 23.6, 16.5).  With a tile or less there is nothing to share, and pairs
+        // spread an expert over all XCDs: 197 rows over 5 experts x 4736 x 2432 14.4 us, runs 21.8.
+        const int64_t live = G < M_cap ? G : M_cap;
+        by_feature = T::TM < 256 && live * kParts * N > 4 * M_cap &&
+                     (live > 1 ? 10 * M_cap > 11 * live * T::TM : M_cap > T::TM);
         return launch((const void*)ffn_tile_kernel<T, KIND>, tiles(M_cap, G, N, T::TM, T::TN / kParts), T::kThreads);
     };
     auto rows = [&](int TM, const void* kernel) {
