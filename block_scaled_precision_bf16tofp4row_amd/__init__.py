@@ -691,7 +691,7 @@ def _act(act) -> int:
     return code
 
 
-def _ffn_dims(a, w, offs, G, M_cap, N, K, parts=1):
+def _ffn_dims(what, a, w, offs, G, M_cap, N, K, parts=1):
     """G, M_cap, N (the features of a part) and K, from the tensors where they are not given."""
     if G is None:
         G = offs.numel() - 1
@@ -702,6 +702,8 @@ def _ffn_dims(a, w, offs, G, M_cap, N, K, parts=1):
     if N is None:
         shape = w.shape
         N = shape[-2] if len(shape) > 3 or parts == 1 else shape[-2] // parts
+        if w.numel() != G * parts * N * K:
+            raise ValueError(f"{what}: w has shape {tuple(shape)}, expected {G} x {'2 x ' if parts == 2 else ''}features x {K}")
     return int(G), int(M_cap), int(N), int(K)
 
 
@@ -735,7 +737,7 @@ def mxfp4_fp8_gated_gemm(a, a_scales, w, w_scales, offs, out=None, q=None, q_sca
     ceil(K/128)]), bias [G, 2 I] float32.  Outputs: out [M_cap, I] BF16, or q [M_cap, I] E4M3 with
     FP32 q_scales [M_cap, ceil(I/128)], or both; h [M_cap, 2 I] BF16 for the gradient (see the
     header).  act: "silu", "gelu", "gelu_tanh", "relu" or "none"."""
-    G, M_cap, I, K = _ffn_dims(a, w, offs, G, M_cap, I, K, 2)
+    G, M_cap, I, K = _ffn_dims("mxfp4_fp8_gated_gemm", a, w, offs, G, M_cap, I, K, 2)
     nb, kb = (I + 127) // 128, (K + 127) // 128
     need = _ffn_workspace("mxfp4_fp8_gated_gemm_workspace", G, M_cap, I, K) if q is not None else 0
     at = _take_here("mxfp4_fp8_gated_gemm", (
@@ -754,7 +756,7 @@ def mxfp4_fp8_gated_gemm_backward(a, a_scales, w, w_scales, h, offs, dh=None, dq
     projection's transposed weights w [G, I, K]; h [M_cap, 2 I] as mxfp4_fp8_gated_gemm left it.
     Outputs: dh [M_cap, 2 I] BF16 (may be h), or dq [M_cap, 2 I] E4M3 with FP32 dq_scales
     [M_cap, 2 I / 128], or both; out [M_cap, I] BF16: the forward's output again (see the header)."""
-    G, M_cap, I, K = _ffn_dims(a, w, offs, G, M_cap, I, K)
+    G, M_cap, I, K = _ffn_dims("mxfp4_fp8_gated_gemm_backward", a, w, offs, G, M_cap, I, K)
     nb, kb, n = (I + 127) // 128, (K + 127) // 128, 2 * M_cap * I
     need = _ffn_workspace("mxfp4_fp8_gated_gemm_backward_workspace", G, M_cap, I, K) if dq is not None else 0
     at = _take_here("mxfp4_fp8_gated_gemm_backward", (
@@ -771,7 +773,7 @@ def mxfp4_fp8_block_gemm_act(a, a_scales, w, w_scales, y, offs, bias=None, resid
     """mxfp4_fp8_block_gemm with an epilogue: y = act(a w^T + bias) + residual, bias [G, N] float32,
     residual [M_cap, N] BF16 (may be y); pre [M_cap, N] BF16: a w^T + bias, for the gradient (see
     the header)."""
-    G, M_cap, N, K = _ffn_dims(a, w, offs, G, M_cap, N, K)
+    G, M_cap, N, K = _ffn_dims("mxfp4_fp8_block_gemm_act", a, w, offs, G, M_cap, N, K)
     nb, kb, n = (N + 127) // 128, (K + 127) // 128, 2 * M_cap * N
     at = _take_here("mxfp4_fp8_block_gemm_act", (
         (a, M_cap * K, "a", _FP8), (a_scales, 4 * M_cap * kb, "a_scales", _F32), (w, G * N * K, "w", _FP8),

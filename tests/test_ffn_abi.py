@@ -134,6 +134,12 @@ def test_binding_checks_tensors():
         mx.mxfp4_fp8_gated_gemm(1, 1, 1, 1, 1, out=1, act="swish", G=1, M_cap=0, I=16, K=16)
     with raises(match="w_scales holds"):
         mx.mxfp4_fp8_gated_gemm(a, sa, w, torch.zeros(G, 1, 1, 2), offs, out=bf(M, I))
+    for bad in (u8(2, I + 1, K), u8(G, 2 * I + 1, K), u8(G, 2 * I, K - 16), u8(G + 1, 2 * I, K)):
+        with raises(match="w has shape"):
+            mx.mxfp4_fp8_gated_gemm(a, sa, bad, sw, offs, out=bf(M, I))
+    for bad in (u8(I, K), u8(G, I, K - 16), u8(G + 1, I, K)):
+        with raises(match="w has shape"):
+            mx.mxfp4_fp8_block_gemm_act(a, sa, bad, sw, bf(M, I), offs)
     back = functools.partial(mx.mxfp4_fp8_gated_gemm_backward, a, sa, u8(G, I, K), torch.zeros(G, 1, 2))
     with raises(match="h holds"):
         back(bf(M, I), offs, dh=bf(M, 2 * I))

@@ -165,7 +165,7 @@ def test_dense(counts, N, K):
 # sizes that the estimate of block_ffn.hip gives to kernels the above do not reach: groups of
 # waves that share K (with blocks for all of them, and with fewer), pairs on a CU, wide tiles
 GATED = [
-    ([2], 512, 4096), ([17], 2064, 1040), ([40], 2048, 4096), ([21, 19], 3088, 2064), ([1, 0, 2], 1552, 2064), ([1, 0, 2], 1552, 4096), ([1, 0, 2], 3088, 4096),
+    ([2], 512, 4096), ([17], 2064, 1040), ([40], 2048, 4096), ([21, 19], 3088, 2064), ([20, 30, 17], 2064, 2064), ([1, 0, 2], 1552, 2064), ([1, 0, 2], 1552, 4096), ([1, 0, 2], 3088, 4096),
     ([16, 20, 1, 0, 40, 16, 30, 7], 1024, 4096), ([130, 120, 139], 2064, 1040), ([130, 120, 150], 2064, 2064),
     ([20, 30, 0, 60, 10, 40, 17, 20], 1552, 4096), ([60, 64, 129, 1, 0, 70, 88, 90], 1552, 4096),
     ([300, 100, 200, 90, 207], 1552, 4096), ([50, 51, 49, 0, 64, 1, 100, 85], 2064, 128), ([30, 0, 57], 8208, 128),
@@ -462,6 +462,26 @@ def test_graph_replays(counts):
         b.run()
         for g, w in zip(got, b.outputs()):
             assert torch.equal(g[:b.M] if len(g) == b.M_cap else g, w[:b.M] if len(w) == b.M_cap else w), i
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    b = Block([3, 0, 2], 400, 256, seed=9)
+    b.run()
+    monkeypatch.setattr(mx, "_current_device", lambda: 1)
+    with pytest.raises(ValueError, match="the current device is cuda:1"):
+        b.run()
+
+
+def test_same_bits_every_time():
+    """No sum depends on the order in which workgroups run."""
+    for counts in ([3, 0, 2], [60, 0, 33, 7], [300, 41]):
+        b = Block(counts, 528, 384, seed=10)
+        b.run()
+        want = b.outputs()
+        for _ in range(5):
+            b.run()
+            for got, exp in zip(b.outputs(), want):
+                assert torch.equal(got, exp)
 
 
 def test_two_calls_at_once():
