@@ -3,12 +3,16 @@
 // dp leaves as BF16, or as E4M3 rows with an FP32 scale per 1x128 block (both from the FP32
 // value; the bias takes that one too).
 //
-// What bounds it is its bytes.  A thread has eight columns and every eighth row of a tile, 32
-// threads a row's 512 bytes, so that the columns' sums stay in registers until the tile's end,
-// where the eight rows of threads meet in LDS.  A tile is 128 or 32 rows of one expert and its
-// sums go to the workspace, where a second launch adds them, tile by tile in a fixed order (no
-// atomics: the same call gives the same bits); with few rows a workgroup takes all rows of an
-// expert and writes the sums itself.
+// What bounds it is its bytes: 32768 rows of 8 experts x 4096, BF16 out and the bias, 97 us
+// without an activation (537 MB, 5.5 TB/s), 145 with GELU (805 MB, 5.6 TB/s).  A thread has eight
+// columns and every eighth row of a tile, 32 threads a row's 512 bytes, so that the columns' sums
+// stay in registers until the tile's end, where the eight rows of threads meet in LDS.  A tile is
+// 32 rows of one expert, which a thread loads all at once, and its sums go to the workspace, where
+// a second launch adds them, tile by tile in a fixed order (no atomics: the same call gives the
+// same bits); with few rows a workgroup takes all rows of an expert and writes the sums itself.
+// (Rows of a tile, 32768 rows of 8 experts x 7168, GELU: 16 351 us, 32 253, 64 260, 128 272; 8192
+// x 2048: 34, 24, 24, 30.  32 is best at every size tried above 12 us, of 4 widths and 4
+// activations; below, where the launches are the time, they differ by what two timings do.)
 #include "activation.h"
 #include "tiles.h"
 
@@ -18,7 +22,7 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kManyRows = 128, kFewRows = 32;     // rows of a tile
+constexpr int kTileRows = 32;
 constexpr int kActCols = 256, kLanes = kActCols / 8, kRowGroups = kThreads / kLanes;
 constexpr int kBatch = 4;                         // rows of a thread in flight
 constexpr int kSumCols = 64, kSumSplit = 16;      // second launch: columns and tile runs of a workgroup
@@ -26,8 +30,8 @@ constexpr uint32_t kNowhere = 0x80000000u;        // offset past every buffer's 
 
 }  // namespace
 
-// ROWS: rows of a tile; 0: all of an expert's.
-template <int ROWS>
+// ALL: a workgroup has all rows of an expert, not a tile of them.
+template <bool ALL>
 __global__ __launch_bounds__(kThreads) void act_rows_kernel(
     const uint16_t* dout, const uint16_t* pre, uint16_t* dpre, uint8_t* q, float* q_scales, float* sums,
     const int32_t* __restrict__ offs, int G, uint32_t N, uint32_t strips, int act)
@@ -37,11 +41,11 @@ __global__ __launch_bounds__(kThreads) void act_rows_kernel(
     int g;
     int64_t row0;
     int rows;
-    if constexpr (ROWS == 0) {
+    if constexpr (ALL) {
         g = (int)tile;
         row0 = offs[g];
         rows = offs[g + 1] - (int)row0;
-    } else if (!find_tile<ROWS>(offs, G, tile, g, row0, rows)) {
+    } else if (!find_tile<kTileRows>(offs, G, tile, g, row0, rows)) {
         return;                                   // uniform over the workgroup
     }
     const uint32_t tid = threadIdx.x, c = tid % kLanes, group = tid / kLanes, col = n0 + 8 * c;
@@ -108,7 +112,7 @@ __global__ __launch_bounds__(kThreads) void act_rows_kernel(
 // dbias_g = the sum of its tiles' sums.
 __global__ __launch_bounds__(kSumCols* kSumSplit) void bias_sum_kernel(
     const float* __restrict__ sums, float* __restrict__ dbias, const int32_t* __restrict__ offs, uint32_t N,
-    uint32_t strips, uint32_t rows)
+    uint32_t strips)
 {
     __shared__ float part[kSumSplit][kSumCols];
     const int g = (int)(blockIdx.x / strips);
@@ -117,10 +121,10 @@ __global__ __launch_bounds__(kSumCols* kSumSplit) void bias_sum_kernel(
     uint64_t first = 0;                           // tiles of the experts before
     for (int e0 = 0; e0 < g; e0 += 64) {
         const int e = e0 + lane;
-        const uint32_t n = e < g ? ((uint32_t)(offs[e + 1] - offs[e]) + rows - 1) / rows : 0;
+        const uint32_t n = e < g ? ((uint32_t)(offs[e + 1] - offs[e]) + kTileRows - 1) / kTileRows : 0;
         first += (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(n), 63);
     }
-    const uint32_t n = ((uint32_t)(offs[g + 1] - offs[g]) + rows - 1) / rows;
+    const uint32_t n = ((uint32_t)(offs[g + 1] - offs[g]) + kTileRows - 1) / kTileRows;
     const uint32_t t0 = (uint32_t)((uint64_t)n * run / kSumSplit), t1 = (uint32_t)((uint64_t)n * (run + 1) / kSumSplit);
     float s = 0.0f;
     if (col < N) {
@@ -141,31 +145,21 @@ __global__ __launch_bounds__(kSumCols* kSumSplit) void bias_sum_kernel(
 }
 
 // Whether sums go to the workspace and a second launch, or a workgroup takes all rows of an
-// expert, which is faster while those are few: 256 rows over 3 experts x 1360: 8.0 us, with
-// tiles 10.2; 500 over 16 x 2048: 8.0, 10.2; 128 rows of one expert x 1360: 9.2, 10.6; but 200 of
-// one x 4096: 13.4, 10.9.  The rows may all be one expert's, so there is a limit (500 of one:
-// 27).
+// expert, which is faster while those are few: 256 rows of 16 experts x 7168, GELU: 8.4 us, in
+// tiles 14.2; 512 of 32: 9.5, 21.7; 64 of one: 8.0, 10.7; but 128 of one: 12.5, 10.7, and 384 of 4:
+// 15.4, 11.3 (without an activation 8.1, 10.8 and 8.8, 11.0).  The rows may all be one expert's,
+// so there is a limit (512 of 4, hardly split, 18.8, 11.5).
 bool act_rows_uses_workspace(int32_t G, int64_t M_cap)
 {
-    return M_cap > 128 && (M_cap > 96 * (int64_t)G || M_cap > 512);
+    return M_cap > 64 * (int64_t)G || M_cap > 512;
 }
 
 namespace {
 
-int64_t act_tiles(int32_t G, int64_t M_cap, int rows)
+int64_t act_tiles(int32_t G, int64_t M_cap)
 {
     const int64_t live = G < M_cap ? G : M_cap;
-    return (M_cap + live * (rows - 1)) / rows;
-}
-
-// Rows of a tile; 0: all of an expert's.  Tiles of 32 rows where those of 128 leave CUs free:
-// 2048 rows over 8 experts x 4096: 15.4 us, with 128 rows 19.9; 300 over 3 x 1360: 10.9, 13.2.
-int act_tile_rows(int32_t G, int64_t M_cap, int64_t N)
-{
-    if (!act_rows_uses_workspace(G, M_cap))
-        return 0;
-    const int64_t strips = (N + kActCols - 1) / kActCols;
-    return act_tiles(G, M_cap, kManyRows) * strips < 1024 ? kFewRows : kManyRows;
+    return (M_cap + live * (kTileRows - 1)) / kTileRows;
 }
 
 }  // namespace
@@ -173,36 +167,34 @@ int act_tile_rows(int32_t G, int64_t M_cap, int64_t N)
 // Bytes that a call with bias gradients and every one of fewer rows use at most.
 int64_t act_rows_workspace(int32_t G, int64_t M_cap, int64_t N)
 {
-    return act_rows_uses_workspace(G, M_cap) ? 4 * act_tiles(G, M_cap, kFewRows) * N : 0;
+    return act_rows_uses_workspace(G, M_cap) ? 4 * act_tiles(G, M_cap) * N : 0;
 }
 
 hipError_t launch_act_rows_backward(const uint16_t* dout, const uint16_t* pre, uint16_t* dpre, uint8_t* q,
                                     float* q_scales, float* dbias, float* work, const int32_t* offs, int32_t G,
                                     int64_t M_cap, int64_t N, int act, hipStream_t stream)
 {
-    const int rows = act_tile_rows(G, M_cap, N);
+    const bool all = dbias && !act_rows_uses_workspace(G, M_cap);
     uint32_t n = (uint32_t)N, strips = (uint32_t)((N + kActCols - 1) / kActCols);
     int g = G;
-    float* sums = dbias ? rows ? work : dbias : nullptr;
-    const int64_t grid = (rows ? act_tiles(G, M_cap, rows) : G) * (int64_t)strips;
+    float* sums = dbias ? all ? dbias : work : nullptr;
+    const int64_t grid = (all ? G : act_tiles(G, M_cap)) * (int64_t)strips;
     const int64_t columns = (N + kSumCols - 1) / kSumCols;
-    const bool then = dbias && rows;
+    const bool then = dbias && !all;
     if (grid > 0x7FFFFFFF || (then && G * columns > 0x7FFFFFFF))
         return hipErrorInvalidValue;
     void* args[] = {(void*)&dout, (void*)&pre, (void*)&dpre, (void*)&q, (void*)&q_scales, (void*)&sums,
                     (void*)&offs, (void*)&g, (void*)&n, (void*)&strips, (void*)&act};
     if (grid > 0) {
-        const void* const kernel = rows == 0          ? (const void*)act_rows_kernel<0>
-                                   : rows == kFewRows ? (const void*)act_rows_kernel<kFewRows>
-                                                      : (const void*)act_rows_kernel<kManyRows>;
+        const void* const kernel = all ? (const void*)act_rows_kernel<true> : (const void*)act_rows_kernel<false>;
         const hipError_t e = launch_kernel(kernel, dim3((unsigned)grid), dim3(kThreads), args, stream, !then);
         if (e != hipSuccess)
             return e;
     }
     if (!then)
         return hipSuccess;
-    uint32_t sum_strips = (uint32_t)columns, tile_rows = (uint32_t)rows;
-    void* more[] = {(void*)&work, (void*)&dbias, (void*)&offs, (void*)&n, (void*)&sum_strips, (void*)&tile_rows};
+    uint32_t sum_strips = (uint32_t)columns;
+    void* more[] = {(void*)&work, (void*)&dbias, (void*)&offs, (void*)&n, (void*)&sum_strips};
     return launch_kernel((const void*)bias_sum_kernel, dim3((unsigned)(G * columns)), dim3(kSumCols * kSumSplit), more,
                          stream);
 }

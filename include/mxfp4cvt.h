@@ -414,8 +414,8 @@ mxfp4_status mxfp4_fp8_block_gemm_act(const uint8_t* a_e4m3, const float* a_scal
  *   q_scales [M_cap, ceil(N/128)] (optional, both or none), dbias [G, N] FP32 (optional; every
  *   element is written, 0 for an expert without rows, also when M_cap == 0): at least one of
  *   the three is given.  dbias is summed in a fixed order.
- *   workspace: for dbias, unless the rows are few.    N must be a multiple of 8, of 16 for q, and at most
- *   2^20. */
+ *   workspace: for dbias, unless the rows are few.   N must be a multiple of 8, of 16 for q, and
+ *   at most 2^20. */
 mxfp4_status mxfp4_act_rows_backward(const uint16_t* dout_bf16, const uint16_t* pre_bf16, uint16_t* dpre_bf16,
                                      uint8_t* q_e4m3, float* q_scales, float* dbias, void* workspace,
                                      const int32_t* group_offsets, int32_t G, int64_t M_cap, int64_t N, int32_t act,
