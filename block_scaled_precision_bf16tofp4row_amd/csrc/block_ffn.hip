@@ -13,6 +13,11 @@
 // The sums go through LDS as FP32, a tile's rows in one phase or two: a thread then has eight
 // consecutive features of a row, 16 lanes a scale block, and its loads and stores are 16 bytes
 // in whole lines.
+//
+// What bounds it: with many rows the product, as in block_gemm.hip (the loads into LDS, then
+// power), and the way out of each tile, which only the gradient's makes much of; with few rows
+// the weights' bytes; with few rows of few experts the load rate of a CU and, in a program without
+// a graph, the host's work per call.
 #include <math.h>
 
 #include <algorithm>
@@ -289,6 +294,16 @@ __device__ __forceinline__ void tile_out(uint8_t* lds0, uint8_t* lds1, uint8_t* 
     }
 }
 
+// The large tile, 256 x 256 with 8 waves, in us (8 experts, SiLU; the operations alone at the
+// 2639 TFLOP/s of a large product without block scales):
+//   gated, 16384 rows x 2048 x 7168, BF16 out and h: 483-501 (364)
+//   gradient of it, dh and out:                       302-308 (182; matrix units 36 % busy, gated 47 %)
+//   dense, 8192 rows x 4096 x 7168, GELU, p kept:     236-261, one expert (182)
+// The gradient's way out is about 11 us of vector work a tile and 134 MB of h, which nothing
+// hides, as a CU has one such workgroup.  Fetching h's lines during the last stages cost more
+// than it hid (342 -> 355 us, with an earlier form of both).
+// Few rows an expert, 32 a tile, read the weights at 5.7-6 TB/s: 128 rows over 32 experts
+// x 2048 x 7168 gated with FP8 out 155, 940 MB; dense x 7168 x 2048 80, 470 MB.
 template <class W, Kind KIND>
 __global__ __launch_bounds__(W::kThreads, W::kD == 2 && W::kSplit == 1 ? 2 : 1) void ffn_tile_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
@@ -323,6 +338,9 @@ __global__ __launch_bounds__(W::kThreads, W::kD == 2 && W::kSplit == 1 ? 2 : 1) 
     }
 }
 
+// One expert's 16 or 32 rows and 32 rows of the weights a workgroup, whose waves share K: one row
+// x 2048 x 7168 gated 9.0 us (29 MB of weights, 3.3 TB/s: what 128 of 256 CUs load), dense 7168 x
+// 2048 with a residual 5.5.
 template <int MT, Kind KIND>
 __global__ __launch_bounds__(64 * kRowsWaves) void ffn_rows_kernel(
     const uint8_t* __restrict__ a, const float* __restrict__ sa, const uint8_t* __restrict__ w,
@@ -365,7 +383,9 @@ __global__ __launch_bounds__(64 * kRowsWaves) void ffn_rows_kernel(
 }
 
 // FP32 rows [0, offs[G]) of `cols` values -> E4M3 rows with FP32 scales: 16 lanes of eight
-// values to a block, blocks of a row one after the other.
+// values to a block, blocks of a row one after the other.  2 us for a row of 2048.  (The tiles of
+// few rows are narrower than a block; joining their maxima in one launch would take counters that
+// every call has to find cleared.)
 __global__ __launch_bounds__(kThreads) void quantize_sums_kernel(
     const float* __restrict__ x, uint8_t* __restrict__ q, float* __restrict__ q_scales,
     const int32_t* __restrict__ offs, int G, uint32_t cols, uint32_t blocks)
@@ -413,7 +433,7 @@ typedef Tile<2, 4, 4, 4, 3> T128x256;
 typedef Tile<2, 4, 8, 4, 2> T256x256;
 
 // What a kernel's workgroup costs: us per block of K, and for its beginning and end.  A CU with
-// one workgroup loads 65-75 GB/s whatever the tile, so a block costs by the rows loaded, until
+// one workgroup loads 60-78 GB/s whatever the tile, so a block costs by the rows loaded, until
 // the matrix instructions count (256 x 256); two workgroups a CU load less each.  Fitted to the
 // times of all kernels at 2100 sizes over 1 to 16000 rows of 1 to 32 experts, 16 to 7168
 // features and 16 to 7680 deep: the chosen kernel takes 1.03 times the best one's time in the
