@@ -344,8 +344,8 @@ mxfp4_status mxfp4_fp8_block_gemm(const uint8_t* a_e4m3, const float* a_scales, 
  * an exponential's argument x adds (|x| + 2) 2^-24); every output is rounded once, from the
  * FP32 value and not from another output.  The matrix cores' own rounding is about 2^-16 of a
  * result on ordinary data.  FP8 outputs are E4M3 rows with one FP32 scale per 1x128 block,
- * made as mxfp4_dispatch_fp8_rows makes them, but from the FP32 values: the operand of the
- * next mxfp4_fp8_block_gemm or mxfp4_fp8_block_gemm_act.
+ * made as mxfp4_dispatch_fp8_rows makes them, but from the FP32 values, which have to be finite
+ * there as well: the operand of the next mxfp4_fp8_block_gemm or mxfp4_fp8_block_gemm_act.
  * workspace: the bytes that the call's _workspace function gives (-1 for invalid sizes), which
  * are enough for every call of at most M_cap rows; not shared by calls that overlap; nothing
  * has to be in it.  NULL is an error (MXFP4_ERR_NULL) only where the call would use it. */
