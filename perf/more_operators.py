@@ -287,14 +287,16 @@ def run(s):
     op, bf = case["op"], torch.bfloat16
     if op == "gated":
         if own:
-            mx.mxfp4_fp8_gated_gemm(s["a"], s["sa"], s["w"], s["sw"], s["offs"], out=s["out"], h=s["h"],
+            sw = s["sw"].view(case["experts"], 2, -1, s["sw"].shape[2])
+            mx.mxfp4_fp8_gated_gemm(s["a"], s["sa"], s["w"], sw, s["offs"], out=s["out"], h=s["h"],
                                     bias=s["bias"], act=case["act"])
             return {"h": s["h"], "out": s["out"]}
         h, out = _gated(s)
         return {"h": h.to(bf), "out": out.to(bf)}
     if op == "ffn":
         if own:
-            mx.mxfp4_fp8_gated_gemm(s["a"], s["sa"], s["w"], s["sw"], s["offs"], q=s["q"], q_scales=s["qs"],
+            sw = s["sw"].view(case["experts"], 2, -1, s["sw"].shape[2])
+            mx.mxfp4_fp8_gated_gemm(s["a"], s["sa"], s["w"], sw, s["offs"], q=s["q"], q_scales=s["qs"],
                                     bias=s["bias"], act=case["act"], workspace=s["ws"])
             mx.mxfp4_fp8_block_gemm_act(s["q"], s["qs"], s["w2"], s["sw2"], s["y"], s["offs"], bias=s["bias2"],
                                         residual=s["residual"])
