@@ -734,12 +734,19 @@ def mxfp4_fp8_gated_gemm(a, a_scales, w, w_scales, offs, out=None, q=None, q_sca
                          workspace=None, act="silu", G=None, M_cap=None, I=None, K=None, stream=None):
     """act(h[:, :I]) * h[:, I:] of h = a w^T + bias: E4M3 a [M_cap, K] (+ FP32 [M_cap, ceil(K/128)])
     and per-expert E4M3 w [G, 2, I, K] or [G, 2 I, K], gate before up (+ FP32 [G, 2, ceil(I/128),
-    ceil(K/128)]), bias [G, 2 I] float32.  Outputs: out [M_cap, I] BF16, or q [M_cap, I] E4M3 with
+    ceil(K/128)]: blocks of a part, also for a joined w), bias [G, 2 I] float32.  Outputs: out [M_cap, I] BF16, or q [M_cap, I] E4M3 with
     FP32 q_scales [M_cap, ceil(I/128)], or both; h [M_cap, 2 I] BF16 for the gradient (see the
     header).  act: "silu", "gelu", "gelu_tanh", "relu" or "none"."""
     G, M_cap, I, K = _ffn_dims("mxfp4_fp8_gated_gemm", a, w, offs, G, M_cap, I, K, 2)
     nb, kb = (I + 127) // 128, (K + 127) // 128
     need = _ffn_workspace("mxfp4_fp8_gated_gemm_workspace", G, M_cap, I, K) if q is not None else 0
+    if I % 128 > 64 and w_scales is not None and not isinstance(w_scales, int):
+        # blocks over the 2 I joined features, of which some have rows of both parts, are as many
+        # here as the parts' own, so only the shape tells them apart
+        shape = tuple(w_scales.shape)
+        if shape != (G, 2, nb, kb) and w_scales.nbytes >= 8 * G * nb * kb:
+            raise ValueError(f"mxfp4_fp8_gated_gemm: w_scales has shape {shape}, expected {(G, 2, nb, kb)}: "
+                             "blocks of 128 features of a part")
     at = _take_here("mxfp4_fp8_gated_gemm", (
         (a, M_cap * K, "a", _FP8), (a_scales, 4 * M_cap * kb, "a_scales", _F32), (w, 2 * G * I * K, "w", _FP8),
         (w_scales, 8 * G * nb * kb, "w_scales", _F32), (bias, 8 * G * I, "bias", _F32),
