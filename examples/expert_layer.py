@@ -175,7 +175,7 @@ class FeedForward:
             raise ValueError("inner widths are multiples of 128")
 
     def plan(self, T: int, device="cuda"):
-        """The buffers of calls on T tokens."""
+        """The buffers of calls on T tokens, no more and no fewer (the offsets say T)."""
         bf = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=device)      # noqa: E731
         b = {"offs": torch.tensor([0, T], dtype=torch.int32, device=device)}
         b["h"], b["dh"], b["y"], b["dx"] = bf(T, 2 * self.I), bf(T, 2 * self.I), bf(T, self.H), bf(T, self.H)
@@ -187,9 +187,15 @@ class FeedForward:
                               dtype=torch.uint8, device=device)
         return b
 
+    def planned(self, b, rows):
+        """The plan b, if the rows are those it is for: the calls go by its offsets."""
+        if rows.shape != b["y"].shape:
+            raise ValueError(f"rows {tuple(rows.shape)}, planned for {tuple(b['y'].shape)}")
+        return b
+
     def forward(self, x, plan, residual=None):
         """x [T, H] BF16 -> [T, H]."""
-        b = plan
+        b = self.planned(plan, x)
         mx.mxfp4_bf16_to_fp8_rows_f32(x, b["x"], b["x_s"], b["offs"])
         mx.mxfp4_fp8_gated_gemm(b["x"], b["x_s"], self.up, self.up_s, b["offs"], q=b["a"], q_scales=b["a_s"], h=b["h"],
                                 bias=self.b_up, workspace=b["ws"])
@@ -199,7 +205,7 @@ class FeedForward:
 
     def backward(self, dout, plan):
         """After forward: the gradients of x (the residual's is dout), of b_up and of b_down."""
-        b = plan
+        b = self.planned(plan, dout)
         db_up, db_down = torch.empty_like(self.b_up)[None], torch.empty_like(self.b_down)[None]
         mx.mxfp4_act_rows_backward(dout, None, b["offs"], q=b["dy"], q_scales=b["dy_s"], dbias=db_down, workspace=b["ws"])
         mx.mxfp4_fp8_gated_gemm_backward(b["dy"], b["dy_s"], self.down_t, self.down_ts, b["h"], b["offs"], dh=b["dh"],
