@@ -89,12 +89,14 @@ class ExpertLayer:
         if T > b["out"].shape[0]:
             raise ValueError(f"{T} tokens, planned for {b['out'].shape[0]}")
         rows = {"offs": None, "ws": None, "fws": None} | dict.fromkeys(("ids", "w", "pos", "out", "logits"), T)
-        return {name: v[:rows.get(name, T * self.k)] for name, v in b.items()}
+        return {name: v[:rows.get(name, T * self.k)] for name, v in b.items() if isinstance(v, torch.Tensor)}
 
     def forward(self, x, plan, row_mask=None, shared=None, keep=True):
         """x [T, H] BF16 -> [T, H]; shared: a shared expert's output, added in.  keep: for the
         gradients (without it a fused layer writes no BF16 rows between its products)."""
         b = self.part(plan, x.shape[0])
+        # the tokens whose rows the plan holds for backward, and for weight_gradients
+        plan["kept"], plan["graded"] = x.shape[0] if keep or not self.fused else None, None
         torch.matmul(x.float(), self.router.t(), out=b["logits"])
         mx.mxfp4_route_topk(b["logits"], b["ids"], b["w"], bias=self.bias, row_mask=row_mask, **self.how)
         mx.mxfp4_expert_map(b["ids"], b["offs"], b["pos"], b["ws"])
@@ -114,6 +116,9 @@ class ExpertLayer:
     def backward(self, dout, plan):
         """After forward: the gradients of the tokens (through the experts) and of the logits."""
         T = dout.shape[0]
+        if plan.get("kept") != T:
+            raise ValueError(f"the plan keeps no rows of a forward call on {T} tokens")
+        plan["graded"] = T if self.fused else None
         b = self.part(plan, T)
         dy = b["dy"] if self.fused else torch.zeros_like(b["y"])
         dw = torch.empty_like(b["w"])
@@ -142,6 +147,8 @@ class ExpertLayer:
 
     def weight_gradients(self, x, plan):
         """After backward of a fused layer: the gradients of w_up and w_down."""
+        if plan.get("graded") != x.shape[0]:
+            raise ValueError(f"the plan keeps no rows of a fused layer's backward call on {x.shape[0]} tokens")
         b = self.part(plan, x.shape[0])
         rows, E = b["y"].shape[0], self.E
         xr = torch.zeros_like(b["y"])             # the tokens in expert order
@@ -196,6 +203,7 @@ class FeedForward:
     def forward(self, x, plan, residual=None):
         """x [T, H] BF16 -> [T, H]."""
         b = self.planned(plan, x)
+        b["kept"] = True
         mx.mxfp4_bf16_to_fp8_rows_f32(x, b["x"], b["x_s"], b["offs"])
         mx.mxfp4_fp8_gated_gemm(b["x"], b["x_s"], self.up, self.up_s, b["offs"], q=b["a"], q_scales=b["a_s"], h=b["h"],
                                 bias=self.b_up, workspace=b["ws"])
@@ -206,6 +214,8 @@ class FeedForward:
     def backward(self, dout, plan):
         """After forward: the gradients of x (the residual's is dout), of b_up and of b_down."""
         b = self.planned(plan, dout)
+        if "kept" not in b:
+            raise ValueError("the plan keeps no rows of a forward call")
         db_up, db_down = torch.empty_like(self.b_up)[None], torch.empty_like(self.b_down)[None]
         mx.mxfp4_act_rows_backward(dout, None, b["offs"], q=b["dy"], q_scales=b["dy_s"], dbias=db_down, workspace=b["ws"])
         mx.mxfp4_fp8_gated_gemm_backward(b["dy"], b["dy_s"], self.down_t, self.down_ts, b["h"], b["offs"], dh=b["dh"],

@@ -32,7 +32,10 @@ def calls(monkeypatch):
         def call(*args, **kw):
             a = sig.bind(*args, **kw).arguments
             rows = next(iter(a.values())).shape[0]
-            if "offs" in a and name != "mxfp4_expert_map":
+            if name == "mxfp4_expert_map":        # every choice has a row, all of the first expert
+                a["offs"].fill_(a["pos"].numel())[0] = 0
+                a["pos"].copy_(torch.arange(a["pos"].numel()).view_as(a["pos"]))
+            elif "offs" in a:
                 assert int(a["offs"][-1]) <= rows, (name, a["offs"].tolist(), rows)
             made.append(name)
 
@@ -68,3 +71,56 @@ def test_dense_block_refuses_other_rows_than_planned(calls):
     assert len(calls) == 3
     block.backward(rows(20), b)
     assert len(calls) == 7
+
+
+def layer(fused):
+    return expert_layer.random_layer(4, 64, 128, 2, seed=1, device="cpu", fused=fused)
+
+
+def test_gradients_of_rows_that_were_not_kept_are_refused(calls):
+    """Without keep a fused layer writes no h: the plan's is an earlier call's, or none."""
+    m = layer(True)
+    b = m.plan(9, device="cpu")
+    with pytest.raises(ValueError, match="forward"):
+        m.backward(rows(9), b)
+    m.forward(rows(9), b)
+    m.forward(rows(9), b, keep=False)
+    with pytest.raises(ValueError, match="forward"):
+        m.backward(rows(9), b)
+    with pytest.raises(ValueError, match="backward"):
+        m.weight_gradients(rows(9), b)
+    assert "mxfp4_combine_rows_backward" not in calls
+    m.forward(rows(9), b)
+    m.backward(rows(9), b)
+    assert "mxfp4_fp8_gated_gemm_backward" in calls
+
+
+@pytest.mark.parametrize("fused", [True, False])
+def test_gradients_of_other_tokens_are_refused(calls, fused):
+    """The map in the plan is the last forward call's."""
+    m = layer(fused)
+    b = m.plan(9, device="cpu")
+    m.forward(rows(7), b)
+    for n in (0, 6, 8, 9):
+        with pytest.raises(ValueError, match="forward"):
+            m.backward(rows(n), b)
+    m.backward(rows(7), b)
+    if not fused:
+        with pytest.raises(ValueError, match="backward"):
+            m.weight_gradients(rows(7), b)
+        return
+    for n in (6, 8):
+        with pytest.raises(ValueError, match="backward"):
+            m.weight_gradients(rows(n), b)
+    m.forward(rows(7), b)
+    with pytest.raises(ValueError, match="backward"):
+        m.weight_gradients(rows(7), b)
+
+
+def test_dense_block_gradients_follow_a_forward_call(calls):
+    block = dense()
+    b = block.plan(5, device="cpu")
+    with pytest.raises(ValueError, match="forward"):
+        block.backward(rows(5), b)
+    block.forward(rows(5), b)
+    block.backward(rows(5), b)
