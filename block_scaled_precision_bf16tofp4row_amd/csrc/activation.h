@@ -13,7 +13,9 @@
 //              there would not
 //   gelu_tanh  x s, s = 1 / (1 + exp(-2 c (x + 0.044715 x^3))), c = sqrt(2 / pi), which is the
 //              usual form with the hyperbolic tangent
-// A NaN gives NaN, and so does -inf under silu and both gelu.
+// A NaN gives NaN in both.  Where a formula has infinity times zero it gives NaN too: silu and
+// gelu at -inf, their derivatives at both infinities, and gelu_tanh at -inf (its derivative is 1
+// and 0 there).
 #pragma once
 
 #include <type_traits>
@@ -35,7 +37,7 @@ __device__ __forceinline__ void activate(float x, float& f, float& slope)
         slope = 1.0f;
     } else if constexpr (ACT == kActRelu) {
         f = x < 0.0f ? 0.0f : x;
-        slope = x <= 0.0f ? 0.0f : 1.0f;
+        slope = x <= 0.0f ? 0.0f : x > 0.0f ? 1.0f : x;
     } else if constexpr (ACT == kActSilu) {
         const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-x));
         f = x * s;
