@@ -1,14 +1,15 @@
 // activation.h -- activations and their derivatives in FP32, and eight FP32 values to and from
 // BF16 and to E4M3 under the FP32 scale of their 1x128 block.
 //
-// With e = exp(-x) or exp(-x^2 / 2) from the hardware's 2^x (good to about (|argument| + 2)
-// 2^-24 of itself) and the hardware's reciprocal (2^-23):
+// With e = exp(-x) or exp(-x^2 / 2) from the hardware's 2^x (2^-23, and the argument E's own
+// roundings, 1 to 6 times E 2^-24) and the hardware's reciprocal (2^-23); tests/act_bounds.py has
+// the bounds that follow, and the header states them:
 //   relu       max(x, 0); derivative 1 where x > 0, else 0
 //   silu       x s, s = 1 / (1 + exp(-x)); derivative s (1 + x (1 - s))
 //   gelu       x P(x), P the normal distribution; derivative P + x exp(-x^2 / 2) / sqrt(2 pi).
 //              P(-z) = t Q(t) exp(-z^2 / 2) for z >= 0, t = 1 / (1 + 0.28 z), Q of degree 8 (a
-//              least-squares fit of its relative error, reweighted to be even: 1.8e-7; 5.3e-7
-//              evaluated in FP32), and P(z) = 1 - P(-z): one exponential for value and
+//              least-squares fit of its relative error, reweighted to be even: 1.8e-7; 5.3e-7 to 6.5e-7
+//              evaluated in FP32 with z up to 4), and P(z) = 1 - P(-z): one exponential for value and
 //              derivative, and small values on the left keep their precision, which 1 + erf
 //              there would not
 //   gelu_tanh  x s, s = 1 / (1 + exp(-2 c (x + 0.044715 x^3))), c = sqrt(2 / pi), which is the

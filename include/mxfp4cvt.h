@@ -340,10 +340,14 @@ mxfp4_status mxfp4_fp8_block_gemm(const uint8_t* a_e4m3, const float* a_scales, 
  * Operands, their limits, group_offsets and errors are mxfp4_fp8_block_gemm's; a dense layer
  * is G = 1.  act is one of mxfp4_act (else MXFP4_ERR_SHAPE).  Outputs called optional may be
  * NULL; rows [offs[G], M_cap) of every output keep what they hold.  Sums, biases and
- * activations are FP32 (activations and their derivatives good to a few 2^-22 of themselves,
- * an exponential's argument x adds (|x| + 2) 2^-24); every output is rounded once, from the
- * FP32 value and not from another output.  The matrix cores' own rounding is about 2^-16 of a
- * result on ordinary data.  FP8 outputs are E4M3 rows with one FP32 scale per 1x128 block,
+ * activations are FP32; every output is rounded once, from the FP32 value and not from another
+ * output.  Activations are good to 24 2^-24 of themselves, and for x < 0 as much more as their
+ * exponential's argument E is rounded: 1.25 E 2^-24 for SiLU (E = |x|), 2.25 E 2^-24 for GELU (E =
+ * x^2 / 2), 6.25 E 2^-24 for the tanh form (E = 1.6 |x| + 0.0714 |x|^3); below 2^-121 they may be
+ * 0.  Their derivatives, which have zeros, are good to 2^-18, 2^-19 and 2^-17 absolutely, and left
+ * of -4 to such multiples of themselves as well.  A NaN gives NaN, as do SiLU and both GELU at
+ * -inf and the derivatives of SiLU and GELU at either infinity.
+ * The matrix cores' own rounding is about 2^-16 of a result on ordinary data.  FP8 outputs are E4M3 rows with one FP32 scale per 1x128 block,
  * made as mxfp4_dispatch_fp8_rows makes them, but from the FP32 values, which have to be finite
  * there as well: the operand of the next mxfp4_fp8_block_gemm or mxfp4_fp8_block_gemm_act.
  * workspace: the bytes that the call's _workspace function gives (-1 for invalid sizes), which
