@@ -9,6 +9,7 @@
 // first, the others the same features of the second.
 #pragma once
 
+#include "tile_count.h"
 #include "tiles.h"
 
 namespace mxfp4 {
@@ -17,7 +18,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kBK = 128;                          // K per stage: one scale block
 constexpr uint32_t kOutOfRange = 0x80000000u;     // offset past every buffer's range
 // s_waitcnt immediate (gfx9 encoding) that waits for vmcnt <= n and nothing else.
 constexpr int vmcnt_at_most(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
@@ -613,14 +613,6 @@ __device__ __forceinline__ void rows_sums(uint8_t* lds0, uint8_t* lds1, uint8_t*
         for (int nt = 0; nt < NT; ++nt)
             *reinterpret_cast<f32x4*>(&part[wave][16 * mt + r][16 * nt + 4 * h]) = acc[mt][nt];
     __syncthreads();
-}
-
-// Workgroups of TM x TN tiles that a call can need: m rows make at most (m + TM - 1) / TM
-// token tiles, and at most min(G, M_cap) experts have rows.
-inline int64_t tiles(int64_t M_cap, int32_t G, int64_t N, int TM, int TN)
-{
-    const int64_t live = G < M_cap ? G : M_cap;
-    return (M_cap + live * (TM - 1)) / TM * ((N + TN - 1) / TN);
 }
 
 }  // namespace mxfp4
