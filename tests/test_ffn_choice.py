@@ -11,7 +11,7 @@ import subprocess
 
 import pytest
 
-from ffn_sizes import KERNELS, KINDS, NAMES
+from ffn_sizes import KERNELS, KINDS, MANY, NAMES
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "block_scaled_precision_bf16tofp4row_amd", "csrc")
@@ -53,7 +53,7 @@ def test_the_names(lib):
 
 
 def test_listed_sizes_reach_their_kernels(lib):
-    for kind, fp8, name, runs, *sizes in KERNELS:
+    for kind, fp8, name, runs, *sizes in KERNELS + MANY:
         assert choice(lib, kind, fp8, *sizes) == (name, runs), (kind, fp8, sizes)
     seen = [k[:4] for k in KERNELS]
     assert len(set(seen)) == len(seen)

@@ -11,7 +11,7 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
-from ffn_sizes import KERNELS
+from ffn_sizes import KERNELS, MANY
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -112,7 +112,7 @@ def workspace(n):
 
 
 @pytest.mark.parametrize("act", ["relu", "none"])
-@pytest.mark.parametrize("kind,e4m3,kernel,runs,G,M_cap,N,K", KERNELS)
+@pytest.mark.parametrize("kind,e4m3,kernel,runs,G,M_cap,N,K", KERNELS + MANY)
 def test_one_rounding(kind, e4m3, kernel, runs, G, M_cap, N, K, act):
     parts = 2 if kind == "gated" else 1
     rng, M, expert, p, (a, sa, w, sw, offs) = operands(G, M_cap, parts, N, K, N + K + len(act))
