@@ -294,13 +294,15 @@ __device__ __forceinline__ void tile_out(uint8_t* lds0, uint8_t* lds1, uint8_t* 
 }
 
 // The large tile, 256 x 256 with 8 waves, in us (8 experts, SiLU; the operations alone at the
-// 2639 TFLOP/s of a large product without block scales):
-//   gated, 16384 rows x 2048 x 7168, BF16 out and h: 483-501 (364)
-//   gradient of it, dh and out:                       302-308 (182; matrix units 36 % busy, gated 47 %)
-//   dense, 8192 rows x 4096 x 7168, GELU, p kept:     236-261, one expert (182)
-// The gradient's way out is about 11 us of vector work a tile and 134 MB of h, which nothing
-// hides, as a CU has one such workgroup.  Fetching h's lines during the last stages cost more
-// than it hid (342 -> 355 us, with an earlier form of both).
+// 3.25 PFLOP/s of a large product without block scales):
+//   gated, 16384 rows x 2048 x 7168, BF16 out and h: 481-501 (296)
+//   gradient of it, dh and out:                       295-308 (148; matrix units 36 % busy, gated 47 %)
+//   dense, 8192 rows x 4096 x 7168, GELU, p kept:     225-261, one expert (148)
+// A CU has one such workgroup.  So a last round that a part of the tiles needs costs nearly a
+// whole one: the same rows in equal shares, two rounds and four, take 254-258 and 449.  And
+// nothing hides the gradient's way out, about 11 us of vector work a tile and 134 MB of h.
+// Fetching h's lines during the last stages cost more than it hid (342 -> 355 us, with an earlier
+// form of both).
 // Few rows an expert, 32 a tile, read the weights at 5.7-6 TB/s: 128 rows over 32 experts
 // x 2048 x 7168 gated with FP8 out 155, 940 MB; dense x 7168 x 2048 80, 470 MB.
 template <class W, Kind KIND>
