@@ -53,7 +53,7 @@ inline Which choose(Kind kind, bool fp8, int32_t G, int64_t M_cap, int64_t N, in
         const Cost& c = kCost[i];
         const bool whole = whole_blocks(kind, w);
         if ((kind != kGated || !fp8) && (w == k32x256 || w == k128x256))
-            continue;                             // (there for whole scale blocks alone)
+            continue;                             // (there for whole scale blocks alone; not timed elsewhere)
         if (fp8 && !whole && sums > kMaxSums)
             continue;
         // an expert's last tile is half full on average, and every expert has one
